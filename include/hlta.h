@@ -422,6 +422,157 @@ hlta_status hlta_stream_load(hlta_stream_t c, const void *src, size_t bytes, voi
 hlta_status hlta_stream_destroy(hlta_stream_t c);
 
 /*
+ * Rotary positions over several axes (time, height, width of a video's tokens): hlta_rope with
+ * a position per axis. The first 2P channels of a head are P = pairs[0] + pairs[1] + pairs[2]
+ * pairs; pairs[0] of them turn with the token's first position (time), the next pairs[1] with
+ * the second (height), the last pairs[2] with the third (width). Pair j of the head, the i-th
+ * of its axis a, turns by the angle
+ *   p_a * base^(-i / pairs[a])   (shared_freq 0: every axis has frequencies from 1 down), or
+ *   p_a * base^(-j / P)          (shared_freq 1: one ladder of frequencies over the head).
+ * layout 0: pair j is (x_{2j}, x_{2j+1}), as in hlta_rope; layout 1: pair j is (x_j, x_{P+j}).
+ * Channels from 2P on pass through.
+ * Positions: `pos`, [B, L, 3] int32 device, or, with pos NULL, those of a grid of grid_h x
+ * grid_w tokens per frame in raster order: token l has (t0[b] + l / (grid_h grid_w),
+ * l / grid_w mod grid_h, l mod grid_w); t0: [B] int32 device, NULL for zero.
+ */
+typedef struct {
+    int pairs[3];        /* pairs per axis, each >= 0, 2 * their sum <= d */
+    int layout;          /* 0 or 1 */
+    int shared_freq;     /* 0 or 1 */
+    int grid_h, grid_w;  /* >= 1 when pos is NULL */
+    float base;          /* finite, > 1 */
+    const int *pos;
+    const int *t0;
+} hlta_rope_axes_t;
+
+/*
+ * Rotates q into q_out and k into k_out. q, q_out: [B, Hq, L, d] device, k, k_out: [B, Hk, L, d],
+ * element type `dt`, 1 <= d <= 128; q or k may be NULL (skipped). An output may be its own input
+ * (in place), else the four tensors must not overlap. inverse != 0 turns the other way, which is
+ * also the map of the gradient. The angle is formed in double precision (any int32 position), the
+ * result rounded to `dt` once. One launch on `stream`. Errors: HLTA_ERR_INVALID_ARG for bad
+ * shapes, fields, or misaligned (16-byte) pointers.
+ */
+hlta_status hlta_rope_axes(const void *q, const void *k, void *q_out, void *k_out, int B, int Hq,
+                           int Hk, long L, int d, const hlta_rope_axes_t *spec, int inverse,
+                           hlta_dtype dt, void *stream);
+
+/*
+ * Paged key/value cache: rollouts of different ages in one batch, each growing page by page (the
+ * streaming cache's rings advance in lockstep and keep only their windows). The caller owns the
+ * pool and the page tables; these calls only read the tables.
+ *   k_pages, v_pages: [num_pages, Hkv, page, d] device, element type `dt`; page 16, 32, 64 or 128.
+ *   table: [B, max_pages] int32 device: position p of rollout b is slot p % page of page
+ *     table[b][p / page]. Entries of positions that a call does not touch may hold anything; pages
+ *     may be shared by rollouts that only read them.
+ *   kv_lens: [B] int32 device: tokens in each rollout's cache, the chunk's own included.
+ *   new_lens: [B] int32 device: tokens of the chunk that each rollout really has (a padded batch),
+ *     NULL for all L.
+ * What the tables say is known on the device only: a page outside [0, num_pages), a length that
+ * is negative or does not fit, is reported through hlta_device_status (HLTA_DEVERR_TABLE) and
+ * never read or written through: such a token is not appended and reads as page 0, lengths are
+ * clamped to what fits; the outputs of that rollout are unspecified.
+ * All calls enqueue on `stream`, hold no state between calls, and can be captured into a CUDA
+ * graph (make the library's first call on a device before a capture). Calls that share a
+ * workspace must be ordered on one stream.
+ */
+
+/*
+ * Appends a chunk: token i of rollout b goes to position kv_lens[b] - n + i, n its new_lens.
+ * k, v: [B, Hkv, L, d] device. `spec` NULL stores k as it is; else its rotation is applied to k
+ * on the way (positions by the token's index i in the chunk). Every slot must be written by one
+ * rollout only. 1 <= d <= 128. One launch. Errors as hlta_rope_axes.
+ */
+hlta_status hlta_paged_append(const void *k, const void *v, void *k_pages, void *v_pages,
+                              const int *table, const int *kv_lens, const int *new_lens, int B,
+                              int Hkv, long L, int d, long num_pages, int page, int max_pages,
+                              const hlta_rope_axes_t *spec, hlta_dtype dt, void *stream);
+
+/*
+ * Workspace bytes of hlta_paged_attn_fwd (`weights`: whether w_out is asked for; for the device
+ * that is current).
+ */
+size_t hlta_paged_attn_workspace_bytes(int B, int Hq, int Hkv, long L, int d, int page,
+                                       int max_pages, int weights, hlta_dtype dt);
+
+/*
+ * Attention of a chunk of new tokens over the paged cache (the chunk appended before). The chunk
+ * starts at a frame border: row i of a rollout with n new tokens is position h + i, h =
+ * kv_lens[b] - n, and lies in frame i / N of the chunk. It attends to positions
+ *   max(0, h + (i/N - w + 1) N) ... min(kv_lens[b], h + (i/N + 1) N) - 1
+ * (bidirectional inside a frame, causal across frames, the last w frames of N tokens, w = 0 for the
+ * whole history; N = 1: causal by token). A row that sees no position gets o = 0, lse = -inf.
+ * q, o: [B, Hq, L, d] device; query head h reads key head h / (Hq / Hkv). lse: [B, Hq, L] float32
+ * (natural log-sum-exp of the scaled scores) or NULL. Rows at or behind new_lens[b] are left as
+ * they were. Slots that no row of the chunk sees (past a rollout's end, before its window) may
+ * hold anything, NaN included.
+ * Accumulated attention weights, for eviction: w_out NULL, or [B, Hkv, max_pages * page] float32:
+ * w_out[j] = decay * w_in[j] + the sum of the softmax weights that the chunk's rows of the head
+ * group give position j; w_in is read for the positions before the chunk only (NULL for zero),
+ * may be w_out, else must not overlap it; decay is finite; positions from kv_lens[b] on are left as they were.
+ * bf16: d = 128, Hq / Hkv <= 128; fp32: 1 <= d <= 128. N >= 1, w >= 0; max_pages * page <= 2^30.
+ * workspace: at least hlta_paged_attn_workspace_bytes(...), 256-byte aligned; its contents on entry
+ * are ignored. Sums run in a fixed order: equal calls give equal bits. Errors: HLTA_ERR_INVALID_ARG,
+ * HLTA_ERR_UNSUPPORTED; a bounded wait that expires as hlta_swa_fwd.
+ */
+hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages,
+                                const int *table, const int *kv_lens, const int *new_lens,
+                                void *o, float *lse, const float *w_in, float *w_out, float decay,
+                                int B, int Hq, int Hkv, long L, int d, long num_pages, int page,
+                                int max_pages, int N, int w, float scale, void *workspace,
+                                size_t ws_bytes, hlta_dtype dt, void *stream);
+
+/* Workspace bytes of hlta_paged_evict. */
+size_t hlta_paged_evict_workspace_bytes(int B, int Hkv, int budget);
+
+/*
+ * Eviction by accumulated attention weight. Per rollout and key head: with n = kv_lens[b] <=
+ * budget every position is kept; else the first `sink`, the last `recent`, and of those between
+ * them the budget - sink - recent of largest weight (equal weights: the lowest position first; a
+ * NaN counts as the least). The kept positions, in rising order, are copied to positions 0, 1, ...
+ * of the destination's pages: k_dst, v_dst [num_dst, Hkv, page, d] with dst_table [B, max_dst]. The
+ * destination's pages must not be pages that the call reads (copied, not moved: pages that other
+ * rollouts share stay whole); it may be the same pool.
+ * weights: [B, Hkv, max_pages * page] float32. new_lens: [B] int32, receives min(n, budget). kept:
+ * [B, Hkv, budget] int32, the kept positions, -1 behind them, or NULL. w_out: [B, Hkv, max_dst *
+ * page] float32, the kept weights, left as it was behind them, or NULL.
+ * budget >= 1, sink, recent >= 0, sink + recent <= budget <= max_dst * page, 1 <= d <= 128.
+ * workspace as above. Errors as hlta_paged_attn_fwd.
+ */
+hlta_status hlta_paged_evict(const float *weights, const void *k_pages, const void *v_pages,
+                             const int *table, const int *kv_lens, int B, int Hkv, int d,
+                             long num_pages, int page, int max_pages, int budget, int sink,
+                             int recent, void *k_dst, void *v_dst, const int *dst_table,
+                             long num_dst, int max_dst, int *new_lens, int *kept, float *w_out,
+                             void *workspace, size_t ws_bytes, hlta_dtype dt, void *stream);
+
+/*
+ * Gated delta rule, recurrent form, over a pool of states: the recurrence of hlta_gdn_chunk_fwd
+ * token by token, for steps of one or a few tokens per rollout (the chunk form prepares 64-token
+ * chunks whatever L is, and is the faster one from some dozens of tokens on).
+ * q, k, v, o: [B, H, L, d] device; a, b: [B, H, L] float32. S, S_out: [num_slots, H, d, d] float32,
+ * S_out may be S (in place), else must not overlap it. slots: [B] int32 device, the state of each
+ * rollout, NULL for 0 .. B-1; a negative slot marks a padded rollout: its rows of o are left as
+ * they were. Slots that no rollout names are left as they were. lens: [B] int32 device: tokens that
+ * each rollout really has, NULL for all L; rows behind are left as they were; with no token the
+ * state is copied. A slot >= num_slots, a slot that an earlier rollout of the call names too, or a
+ * length outside [0, L] is reported through hlta_device_status (HLTA_DEVERR_TABLE) and the rollout
+ * skipped. bf16: d = 128; fp32: 1 <= d <= 128. The state is updated in fp32 and rounded nowhere.
+ * One launch; no workspace. Errors as hlta_gdn_chunk_fwd.
+ */
+hlta_status hlta_gdn_step(const void *q, const void *k, const void *v, const float *a,
+                          const float *b, void *o, const float *S, float *S_out, const int *slots,
+                          const int *lens, int B, int H, long L, int d, long num_slots,
+                          hlta_dtype dt, void *stream);
+
+/* hlta_gdn_step from raw q, k and raw gate inputs x, y, as hlta_gdn_chunk_fwd_raw; q and k are
+ * scaled to unit norm in fp32 and not rounded to `dt` again. */
+hlta_status hlta_gdn_step_raw(const void *q, const void *k, const void *v, const float *x,
+                              const float *y, float c, void *o, const float *S, float *S_out,
+                              const int *slots, const int *lens, int B, int H, long L, int d,
+                              long num_slots, hlta_dtype dt, void *stream);
+
+/*
  * Profiling hook for hlta_hybrid_fwd(_raw) and the streaming steps (measurement, not needed
  * for results). `events` is NULL (off) or an array of 5 cudaEvent_t created by the caller on
  * the current device. While set, each hybrid call or streaming step records events[0] where
@@ -443,15 +594,17 @@ hlta_status hlta_set_profile_events(void *const *events);
 unsigned long long hlta_kernel_launches(void);
 
 /* Bits of the device error word (hlta_device_status): the kernel kind whose bounded wait
- * expired. */
+ * expired, or what a kernel refused in the tables it was given. */
 #define HLTA_DEVERR_ATTN_WAIT 0x1u  /* a window-attention kernel (forward or backward) */
 #define HLTA_DEVERR_GDN_WAIT 0x2u   /* a gated-delta-rule kernel */
 #define HLTA_DEVERR_SELFTEST 0x4u   /* hlta_wait_expiry_selftest */
+#define HLTA_DEVERR_TABLE 0x8u      /* a page, slot or length out of range (no wait expired) */
 
 /*
  * Synchronizes `stream`, then reads and clears the library's device error word.
  * *code receives the raw word (0: no kernel stopped early; otherwise HLTA_DEVERR_* bits).
  * Returns HLTA_ERR_TIMEOUT if a bounded wait expired in any kernel since the last call,
+ * HLTA_ERR_INVALID_ARG if none did but a table entry was refused (HLTA_DEVERR_TABLE),
  * HLTA_ERR_CUDA on a CUDA error.
  */
 hlta_status hlta_device_status(void *stream, unsigned int *code);

@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_PKG, "libhlta.so")
 HLTA_OK, HLTA_ERR_INVALID_ARG, HLTA_ERR_UNSUPPORTED, HLTA_ERR_CUDA, HLTA_ERR_TIMEOUT = range(5)
 HLTA_BF16, HLTA_FP32 = 0, 1
 HLTA_DEVERR_ATTN_WAIT, HLTA_DEVERR_GDN_WAIT, HLTA_DEVERR_SELFTEST = 0x1, 0x2, 0x4
+HLTA_DEVERR_TABLE = 0x8
 _STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT"}
 
 
@@ -28,6 +29,14 @@ class HltaError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"HLTA_ERR_{_STATUS.get(status, status)}: {msg}")
         self.status = status
+
+
+class hlta_rope_axes_t(ctypes.Structure):
+    """The rotation of hlta_rope_axes and hlta_paged_append (include/hlta.h)."""
+    _fields_ = [("pairs", ctypes.c_int * 3), ("layout", ctypes.c_int),
+                ("shared_freq", ctypes.c_int), ("grid_h", ctypes.c_int),
+                ("grid_w", ctypes.c_int), ("base", ctypes.c_float),
+                ("pos", ctypes.c_void_p), ("t0", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -70,6 +79,15 @@ def _load() -> ctypes.CDLL:
         "hlta_gdn_bwd_workspace_bytes": (Z, [I, I, L, I, I]),
         "hlta_gdn_chunk_bwd": (I, [P, P, P, P, P, P, P, P, P, P, P, P, P, P, I, I, L, I, I, P, Z, I,
                                    P]),
+        "hlta_rope_axes": (I, [P, P, P, P, I, I, I, L, I, P, I, I, P]),
+        "hlta_paged_append": (I, [P, P, P, P, P, P, P, I, I, L, I, L, I, I, P, I, P]),
+        "hlta_paged_attn_workspace_bytes": (Z, [I, I, I, L, I, I, I, I, I]),
+        "hlta_paged_attn_fwd": (I, [P] * 10 + [F, I, I, I, L, I, L, I, I, I, I, F, P, Z, I, P]),
+        "hlta_paged_evict_workspace_bytes": (Z, [I, I, I]),
+        "hlta_paged_evict": (I, [P] * 5 + [I, I, I, L, I, I, I, I, I, P, P, P, L, I, P, P, P, P, Z,
+                                 I, P]),
+        "hlta_gdn_step": (I, [P] * 10 + [I, I, L, I, L, I, P]),
+        "hlta_gdn_step_raw": (I, [P] * 5 + [F] + [P] * 5 + [I, I, L, I, L, I, P]),
         "hlta_device_status": (I, [P, ctypes.POINTER(ctypes.c_uint)]),
         "hlta_kernel_launches": (ctypes.c_ulonglong, []),
         "hlta_wait_expiry_selftest": (I, [ctypes.c_ulonglong, P]),
@@ -295,6 +313,150 @@ def hlta_gdn_chunk_bwd(q, k, v, a, b, S0, dO, dS_final, dq, dk, dv, da, db, dS0,
                                    _stream(stream)))
 
 
+def _need_here(*named):
+    """Tensors of the serving calls: contiguous, on the current device (their kernels are
+    launched there)."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t, n in named:
+        if t is None:
+            continue
+        _need(t, n)
+        if t.device.index != dev:
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _need_dtype(dtype, *named):
+    for t, n in named:
+        if t is not None and t.dtype != dtype:
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {dtype} (got {t.dtype})")
+
+
+def _need_shape(t, n, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {list(shape)} (got {list(t.shape)})")
+
+
+def rope_axes_spec(pairs, grid=None, pos=None, t0=None, base=10000.0, halves=False,
+                   shared_freq=False):
+    """hlta_rope_axes_t from its parts: pairs = (time, height, width); grid = (height, width) of
+    a frame, or pos [B, L, 3] int32; t0 [B] int32, the first frame's index of each rollout."""
+    import torch
+    if (grid is None) == (pos is None):
+        raise HltaError(HLTA_ERR_INVALID_ARG, "give either a grid or positions")
+    if pos is not None and t0 is not None:
+        raise HltaError(HLTA_ERR_INVALID_ARG, "t0 goes with a grid")
+    _need_here((pos, "pos"), (t0, "t0"))
+    _need_dtype(torch.int32, (pos, "pos"), (t0, "t0"))
+    gh, gw = grid if grid is not None else (1, 1)
+    return hlta_rope_axes_t((ctypes.c_int * 3)(*pairs), int(halves), int(shared_freq), gh, gw,
+                            base, _addr(pos), _addr(t0))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def hlta_rope_axes(q, k, q_out, k_out, B, Hq, Hk, L, d, spec, inverse=False, stream=None):
+    _need_here((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))
+    ref = q if q is not None else k
+    _need_dtype(ref.dtype, (q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))
+    _check(_lib.hlta_rope_axes(_p(q), _p(k), _p(q_out), _p(k_out), B, Hq, Hk, L, d,
+                               ctypes.byref(spec), 1 if inverse else 0, _dt(ref), _stream(stream)))
+
+
+def hlta_paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens, B, Hkv, L, d, num_pages,
+                      page, max_pages, spec=None, stream=None):
+    named = ((k, "k"), (v, "v"), (k_pages, "k_pages"), (v_pages, "v_pages"))
+    ints = ((table, "table"), (kv_lens, "kv_lens"), (new_lens, "new_lens"))
+    _need_here(*named, *ints)
+    _need_dtype(k.dtype, *named)
+    _need_dtype(_int32(), *ints)
+    _check(_lib.hlta_paged_append(_p(k), _p(v), _p(k_pages), _p(v_pages), _p(table), _p(kv_lens),
+                                  _p(new_lens), B, Hkv, L, d, num_pages, page, max_pages,
+                                  None if spec is None else ctypes.byref(spec), _dt(k),
+                                  _stream(stream)))
+
+
+def _int32():
+    import torch
+    return torch.int32
+
+
+def _float32():
+    import torch
+    return torch.float32
+
+
+def hlta_paged_attn_workspace_bytes(B, Hq, Hkv, L, d, page, max_pages, weights=False,
+                                    dt=HLTA_BF16) -> int:
+    return int(_lib.hlta_paged_attn_workspace_bytes(B, Hq, Hkv, L, d, page, max_pages,
+                                                    1 if weights else 0, dt))
+
+
+def hlta_paged_attn_fwd(q, k_pages, v_pages, table, kv_lens, new_lens, o, lse, w_in, w_out, decay,
+                        B, Hq, Hkv, L, d, num_pages, page, max_pages, N, w, scale, workspace,
+                        stream=None):
+    named = ((q, "q"), (k_pages, "k_pages"), (v_pages, "v_pages"), (o, "o"))
+    ints = ((table, "table"), (kv_lens, "kv_lens"), (new_lens, "new_lens"))
+    floats = ((lse, "lse"), (w_in, "w_in"), (w_out, "w_out"))
+    _need_here(*named, *ints, *floats, (workspace, "workspace"))
+    _need_dtype(q.dtype, *named)
+    _need_dtype(_int32(), *ints)
+    _need_dtype(_float32(), *floats)
+    _check(_lib.hlta_paged_attn_fwd(_p(q), _p(k_pages), _p(v_pages), _p(table), _p(kv_lens),
+                                    _p(new_lens), _p(o), _p(lse), _p(w_in), _p(w_out),
+                                    float(decay), B, Hq, Hkv, L, d, num_pages, page, max_pages, N,
+                                    w, float(scale), _p(workspace),
+                                    workspace.numel() * workspace.element_size(), _dt(q),
+                                    _stream(stream)))
+
+
+def hlta_paged_evict_workspace_bytes(B, Hkv, budget) -> int:
+    return int(_lib.hlta_paged_evict_workspace_bytes(B, Hkv, budget))
+
+
+def hlta_paged_evict(weights, k_pages, v_pages, table, kv_lens, B, Hkv, d, num_pages, page,
+                     max_pages, budget, sink, recent, k_dst, v_dst, dst_table, num_dst, max_dst,
+                     new_lens, kept, w_out, workspace, stream=None):
+    named = ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_dst, "k_dst"), (v_dst, "v_dst"))
+    ints = ((table, "table"), (kv_lens, "kv_lens"), (dst_table, "dst_table"),
+            (new_lens, "new_lens"), (kept, "kept"))
+    floats = ((weights, "weights"), (w_out, "w_out"))
+    _need_here(*named, *ints, *floats, (workspace, "workspace"))
+    _need_dtype(k_pages.dtype, *named)
+    _need_dtype(_int32(), *ints)
+    _need_dtype(_float32(), *floats)
+    _check(_lib.hlta_paged_evict(_p(weights), _p(k_pages), _p(v_pages), _p(table), _p(kv_lens), B,
+                                 Hkv, d, num_pages, page, max_pages, budget, sink, recent,
+                                 _p(k_dst), _p(v_dst), _p(dst_table), num_dst, max_dst,
+                                 _p(new_lens), _p(kept), _p(w_out), _p(workspace),
+                                 workspace.numel() * workspace.element_size(), _dt(k_pages),
+                                 _stream(stream)))
+
+
+def _gdn_step_check(q, k, v, a, b, o, S, S_out, slots, lens):
+    _need_here((q, "q"), (k, "k"), (v, "v"), (a, "a"), (b, "b"), (o, "o"), (S, "S"),
+               (S_out, "S_out"), (slots, "slots"), (lens, "lens"))
+    _need_dtype(q.dtype, (k, "k"), (v, "v"), (o, "o"))
+    _need_dtype(_float32(), (a, "a"), (b, "b"), (S, "S"), (S_out, "S_out"))
+    _need_dtype(_int32(), (slots, "slots"), (lens, "lens"))
+
+
+def hlta_gdn_step(q, k, v, a, b, o, S, S_out, slots, lens, B, H, L, d, num_slots, stream=None):
+    _gdn_step_check(q, k, v, a, b, o, S, S_out, slots, lens)
+    _check(_lib.hlta_gdn_step(_p(q), _p(k), _p(v), _p(a), _p(b), _p(o), _p(S), _p(S_out),
+                              _p(slots), _p(lens), B, H, L, d, num_slots, _dt(q), _stream(stream)))
+
+
+def hlta_gdn_step_raw(q, k, v, x, y, c, o, S, S_out, slots, lens, B, H, L, d, num_slots,
+                      stream=None):
+    _gdn_step_check(q, k, v, x, y, o, S, S_out, slots, lens)
+    _check(_lib.hlta_gdn_step_raw(_p(q), _p(k), _p(v), _p(x), _p(y), float(c), _p(o), _p(S),
+                                  _p(S_out), _p(slots), _p(lens), B, H, L, d, num_slots, _dt(q),
+                                  _stream(stream)))
+
+
 def hlta_device_status(stream=None) -> int:
     code = ctypes.c_uint(0)
     _check(_lib.hlta_device_status(_stream(stream), ctypes.byref(code)))
@@ -479,6 +641,152 @@ def hybrid(q, k, v, a, b, Hs, Hd, Hg, T, N, w_swa, w_dswa, r, S0=None, chunk=64,
     hlta_hybrid_fwd(q, k, v, a, b, o, S0, S_out, B, Hs, Hd, Hg, T, N, d, w_swa, w_dswa, r,
                     chunk, scale, workspace, stream)
     return o, S_out
+
+
+def _on(stream, *tensors):
+    """Tensors allocated here for a call on another stream than the current one: torch's
+    allocator may not hand their memory on before that stream's work is done."""
+    if stream is None:
+        return
+    import torch
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream.cuda_stream == torch.cuda.current_stream().cuda_stream:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def rope_axes(q, k, pairs, grid=None, pos=None, t0=None, base=10000.0, halves=False,
+              shared_freq=False, inverse=False, out=None, stream=None):
+    """q and k ([B, H, L, d], either may be None) rotated by positions on three axes (see
+    hlta_rope_axes); `out` = (q_out, k_out), which may be (q, k) for in place."""
+    import torch
+    ref = q if q is not None else k
+    B, _, L, d = ref.shape
+    Hq, Hk = (0 if t is None else t.shape[1] for t in (q, k))
+    for t, n, H in ((q, "q", Hq), (k, "k", Hk)):
+        _need_shape(t, n, B, H, L, d)
+    _need_shape(pos, "pos", B, L, 3)
+    _need_shape(t0, "t0", B)
+    spec = rope_axes_spec(pairs, grid, pos, t0, base, halves, shared_freq)
+    if out is None:
+        out = tuple(None if t is None else torch.empty_like(t) for t in (q, k))
+        _on(stream, *out)
+    _need_shape(out[0], "q_out", B, Hq, L, d)
+    _need_shape(out[1], "k_out", B, Hk, L, d)
+    hlta_rope_axes(q, k, out[0], out[1], B, Hq, Hk, L, d, spec, inverse, stream)
+    return out
+
+
+def _cache_shape(k_pages, v_pages, table, kv_lens, new_lens=None):
+    pages, H, page, d = k_pages.shape
+    B, width = table.shape
+    _need_shape(v_pages, "v_pages", pages, H, page, d)
+    _need_shape(kv_lens, "kv_lens", B)
+    _need_shape(new_lens, "new_lens", B)
+    return pages, H, page, d, B, width
+
+
+def paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens=None, rope=None, stream=None):
+    """Append a chunk (k, v [B, Hkv, L, d]) to a paged cache (see hlta_paged_append); `rope`: the
+    arguments of rope_axes_spec as a dict, for k to be rotated on the way."""
+    pages, H, page, d, B, width = _cache_shape(k_pages, v_pages, table, kv_lens, new_lens)
+    L = k.shape[2]
+    _need_shape(k, "k", B, H, L, d)
+    _need_shape(v, "v", B, H, L, d)
+    spec = None
+    if rope is not None:
+        _need_shape(rope.get("pos"), "pos", B, L, 3)
+        _need_shape(rope.get("t0"), "t0", B)
+        spec = rope_axes_spec(**rope)
+    hlta_paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens, B, H, L, d, pages, page,
+                      width, spec, stream)
+
+
+def paged_attn(q, k_pages, v_pages, table, kv_lens, new_lens=None, N=1, w=0, scale=0.0, out=None,
+               lse=None, w_in=None, w_out=None, decay=1.0, workspace=None, stream=None):
+    """Attention of a chunk (q [B, Hq, L, d]) over a paged cache it was appended to (see
+    hlta_paged_attn_fwd). Rows behind a rollout's new tokens are left as they are in `out`
+    (zeros when it is allocated here)."""
+    import torch
+    pages, H, page, d, B, width = _cache_shape(k_pages, v_pages, table, kv_lens, new_lens)
+    Hq, L = q.shape[1:3]
+    _need_shape(q, "q", B, Hq, L, d)
+    _need_shape(lse, "lse", B, Hq, L)
+    _need_shape(w_in, "w_in", B, H, width * page)
+    _need_shape(w_out, "w_out", B, H, width * page)
+    if out is None:
+        out = torch.empty_like(q) if new_lens is None else torch.zeros_like(q)
+        _on(stream, out)
+    _need_shape(out, "out", B, Hq, L, d)
+    if workspace is None:
+        workspace = _workspace(hlta_paged_attn_workspace_bytes(B, Hq, H, L, d, page, width,
+                                                               w_out is not None, _dt(q)), q.device)
+        _on(stream, workspace)
+    hlta_paged_attn_fwd(q, k_pages, v_pages, table, kv_lens, new_lens, out, lse, w_in, w_out, decay,
+                        B, Hq, H, L, d, pages, page, width, N, w, scale, workspace, stream)
+    return out
+
+
+def paged_evict(weights, k_pages, v_pages, table, kv_lens, budget, sink, recent, k_dst, v_dst,
+                dst_table, new_lens=None, kept=None, w_out=None, workspace=None, stream=None):
+    """Copy the `budget` positions of largest accumulated weight (the first `sink` and the last
+    `recent` always among them) of every rollout and key head to the destination's pages (see
+    hlta_paged_evict). Returns the new lengths [B] int32."""
+    import torch
+    pages, H, page, d, B, width = _cache_shape(k_pages, v_pages, table, kv_lens, new_lens)
+    num_dst, dwidth = k_dst.shape[0], dst_table.shape[1]
+    _need_shape(weights, "weights", B, H, width * page)
+    _need_shape(k_dst, "k_dst", num_dst, H, page, d)
+    _need_shape(v_dst, "v_dst", num_dst, H, page, d)
+    _need_shape(dst_table, "dst_table", B, dwidth)
+    _need_shape(kept, "kept", B, H, budget)
+    _need_shape(w_out, "w_out", B, H, dwidth * page)
+    if new_lens is None:
+        new_lens = torch.empty_like(kv_lens)
+        _on(stream, new_lens)
+    if workspace is None:
+        workspace = _workspace(hlta_paged_evict_workspace_bytes(B, H, budget), weights.device)
+        _on(stream, workspace)
+    hlta_paged_evict(weights, k_pages, v_pages, table, kv_lens, B, H, d, pages, page, width, budget,
+                     sink, recent, k_dst, v_dst, dst_table, num_dst, dwidth, new_lens, kept, w_out,
+                     workspace, stream)
+    return new_lens
+
+
+def _gdn_step_shapes(q, k, v, a, b, S, slots, lens, out, S_out, stream):
+    import torch
+    B, H, L, d = q.shape
+    for t, n in ((k, "k"), (v, "v"), (out, "out")):
+        _need_shape(t, n, B, H, L, d)
+    for t, n in ((a, "a"), (b, "b")):
+        _need_shape(t, n, B, H, L)
+    _need_shape(S, "S", S.shape[0], H, d, d)
+    _need_shape(S_out, "S_out", *S.shape)
+    _need_shape(slots, "slots", B)
+    _need_shape(lens, "lens", B)
+    if out is None:
+        out = torch.empty_like(q) if slots is None and lens is None else torch.zeros_like(q)
+        _on(stream, out)
+    return (B, H, L, d), out, S if S_out is None else S_out
+
+
+def gdn_step(q, k, v, a, b, S, slots=None, lens=None, out=None, S_out=None, stream=None):
+    """One step of one or a few tokens of the gated delta rule over a pool of states S
+    [slots, H, d, d], updated in place unless S_out is given (see hlta_gdn_step). Returns
+    (o, S_out)."""
+    (B, H, L, d), o, So = _gdn_step_shapes(q, k, v, a, b, S, slots, lens, out, S_out, stream)
+    hlta_gdn_step(q, k, v, a, b, o, S, So, slots, lens, B, H, L, d, S.shape[0], stream)
+    return o, So
+
+
+def gdn_step_raw(q, k, v, x, y, c, S, slots=None, lens=None, out=None, S_out=None, stream=None):
+    """gdn_step from raw q, k and raw gate inputs (see hlta_gdn_step_raw)."""
+    (B, H, L, d), o, So = _gdn_step_shapes(q, k, v, x, y, S, slots, lens, out, S_out, stream)
+    hlta_gdn_step_raw(q, k, v, x, y, c, o, S, So, slots, lens, B, H, L, d, S.shape[0], stream)
+    return o, So
 
 
 class Stream:

@@ -1,0 +1,211 @@
+// Gated delta rule token by token over a pool of states: the recurrent form, for steps of one or
+// a few tokens.
+//
+// Row i of the state only meets itself: with u = S_i . k and the old row,
+//   S_i' = a S_i + (b v_i - a b u) k,     o_i = S_i' . q = a (S_i . q) + (b v_i - a b u) (k . q),
+// so both products of a token read the same old row and are reduced together, and k . q is one
+// number per token. Bound by HBM: 4 d^2 bytes in and as many out per state, against 8 d^2
+// operations per token.
+// d = 128: eight lanes share a row (16 channels each, as four 16-byte words 128 bytes apart, so
+// that a warp's load covers whole 128-byte lines of four rows); a thread keeps the rows' channels
+// in registers for all of the step's tokens, so the state moves once however many tokens there are.
+// Other d (fp32 tensors): a warp walks a row.
+#include "hlta_internal.cuh"
+
+#include <math.h>
+
+namespace hlta {
+namespace {
+
+__device__ __forceinline__ float ldf(const float *p) { return *p; }
+__device__ __forceinline__ float ldf(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void stf(float *p, float v) { *p = v; }
+__device__ __forceinline__ void stf(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float warp_sum(float x)
+{
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The rollout's state slot and token count; false: skipped (padded, out of range, or its slot
+// taken by an earlier rollout). Called by every thread of the block.
+__device__ __forceinline__ bool rollout(const GdnStepArgs &p, int b, long &slot, int &n)
+{
+    slot = p.slots ? p.slots[b] : b;
+    n = p.lens ? p.lens[b] : (int)p.L;
+    if (slot < 0) return false;
+    int bad = slot >= p.num_slots || n < 0 || n > p.L;
+    if (p.slots)
+        for (int i = threadIdx.x; i < b; i += blockDim.x) bad |= p.slots[i] == slot;
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) atomicOr(p.err, DEVERR_TABLE);
+    return !bad;
+}
+
+// gates of a token: given, or a = exp(-c softplus(x)), b = sigmoid(y)
+__device__ __forceinline__ void gates(const GdnStepArgs &p, long at, float &a, float &b)
+{
+    a = p.a[at];
+    b = p.b[at];
+    if (p.raw) {
+        a = expf(-p.raw_c * (fmaxf(a, 0.f) + log1pf(expf(-fabsf(a)))));
+        b = 1.f / (1.f + expf(-b));
+    }
+}
+
+// scale to unit norm; a zero vector stays zero
+__device__ __forceinline__ float unit(float sumsq) { return sumsq > 0.f ? rsqrtf(sumsq) : 0.f; }
+
+constexpr int D = 128, TOK = 4, RPT = 4, NT = 128;      // staged tokens, rows per thread, threads
+constexpr int ROWS = NT / 8 * RPT;                      // rows per block (64)
+
+template <typename E>
+__global__ void __launch_bounds__(NT) gdn_step_kernel(const GdnStepArgs p)
+{
+    __shared__ __align__(16) float qs[TOK][D], ks[TOK][D];
+    __shared__ float as[TOK], bs[TOK], kq[TOK];
+    const int b = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    long slot;
+    int n;
+    if (!rollout(p, b, slot, n)) return;
+    const int sub = threadIdx.x & 7, row0 = blockIdx.x * ROWS + (threadIdx.x >> 3);
+    const long bh = (long)b * p.H + h;
+    const float *S = p.S + (slot * p.H + h) * D * D;
+    float *So = p.S_out + (slot * p.H + h) * D * D;
+    float s[RPT][16];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float4 v = *(const float4 *)(S + (row0 + r * (NT / 8)) * D + x * 32 + sub * 4);
+            s[r][4 * x] = v.x; s[r][4 * x + 1] = v.y; s[r][4 * x + 2] = v.z; s[r][4 * x + 3] = v.w;
+        }
+    for (int t0 = 0; t0 < n; t0 += TOK) {
+        __syncthreads();
+        if (t0 + warp < n) {            // one warp stages a token
+            const long at = (bh * p.L + t0 + warp) * D;
+            float q[4], k[4], qq = 0.f, kk = 0.f, qk = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                q[x] = ldf((const E *)p.q + at + x * 32 + lane);
+                k[x] = ldf((const E *)p.k + at + x * 32 + lane);
+                qq = fmaf(q[x], q[x], qq);
+                kk = fmaf(k[x], k[x], kk);
+                qk = fmaf(q[x], k[x], qk);
+            }
+            qk = warp_sum(qk);
+            float fq = 1.f, fk = 1.f;
+            if (p.raw) {
+                fq = unit(warp_sum(qq));
+                fk = unit(warp_sum(kk));
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                qs[warp][x * 32 + lane] = q[x] * fq;
+                ks[warp][x * 32 + lane] = k[x] * fk;
+            }
+            if (lane == 0) {
+                gates(p, bh * p.L + t0 + warp, as[warp], bs[warp]);
+                kq[warp] = qk * fq * fk;
+            }
+        }
+        __syncthreads();
+        for (int t = t0; t < min(n, t0 + TOK); ++t) {
+            const int j = t - t0;
+            float q[16], k[16];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float4 vq = *(const float4 *)&qs[j][x * 32 + sub * 4], vk = *(const float4 *)&ks[j][x * 32 + sub * 4];
+                q[4 * x] = vq.x; q[4 * x + 1] = vq.y; q[4 * x + 2] = vq.z; q[4 * x + 3] = vq.w;
+                k[4 * x] = vk.x; k[4 * x + 1] = vk.y; k[4 * x + 2] = vk.z; k[4 * x + 3] = vk.w;
+            }
+            const float a = as[j], bb = bs[j], qk = kq[j];
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+                float u = 0.f, w = 0.f;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    u = fmaf(s[r][x], k[x], u);
+                    w = fmaf(s[r][x], q[x], w);
+                }
+#pragma unroll
+                for (int o = 4; o; o >>= 1) {
+                    u += __shfl_xor_sync(0xffffffffu, u, o);
+                    w += __shfl_xor_sync(0xffffffffu, w, o);
+                }
+                const long at = (bh * p.L + t) * D + row0 + r * (NT / 8);
+                const float g = bb * (ldf((const E *)p.v + at) - a * u);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) s[r][x] = fmaf(a, s[r][x], g * k[x]);
+                if (sub == 0) stf((E *)p.o + at, fmaf(a, w, g * qk));
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            *(float4 *)(So + (row0 + r * (NT / 8)) * D + x * 32 + sub * 4) =
+                make_float4(s[r][4 * x], s[r][4 * x + 1], s[r][4 * x + 2], s[r][4 * x + 3]);
+}
+
+// fp32 tensors of any d <= 128: a warp per state row, up to four channels a lane.
+__global__ void __launch_bounds__(NT) gdn_step_any_kernel(const GdnStepArgs p)
+{
+    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31, d = p.d;
+    long slot;
+    int n;
+    if (!rollout(p, b, slot, n)) return;
+    const int row = blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
+    if (row >= d) return;
+    const long bh = (long)b * p.H + h, base = (slot * p.H + h) * d * d + (long)row * d;
+    float s[4];
+    for (int x = 0; x < 4; ++x) s[x] = x * 32 + lane < d ? p.S[base + x * 32 + lane] : 0.f;
+    for (int t = 0; t < n; ++t) {
+        const long at = (bh * p.L + t) * d;
+        float q[4], k[4], qq = 0.f, kk = 0.f, qk = 0.f, u = 0.f, w = 0.f;
+        for (int x = 0; x < 4; ++x) {
+            const bool in = x * 32 + lane < d;
+            q[x] = in ? ((const float *)p.q)[at + x * 32 + lane] : 0.f;
+            k[x] = in ? ((const float *)p.k)[at + x * 32 + lane] : 0.f;
+            qq = fmaf(q[x], q[x], qq);
+            kk = fmaf(k[x], k[x], kk);
+            qk = fmaf(q[x], k[x], qk);
+            u = fmaf(s[x], k[x], u);
+            w = fmaf(s[x], q[x], w);
+        }
+        float fq = 1.f, fk = 1.f, a, bb;
+        if (p.raw) {
+            fq = unit(warp_sum(qq));
+            fk = unit(warp_sum(kk));
+        }
+        u = warp_sum(u) * fk;
+        w = warp_sum(w) * fq;
+        qk = warp_sum(qk) * fq * fk;
+        gates(p, bh * p.L + t, a, bb);
+        const float g = bb * (((const float *)p.v)[at + row] - a * u);
+        for (int x = 0; x < 4; ++x) s[x] = fmaf(a, s[x], g * (k[x] * fk));
+        if (lane == 0) ((float *)p.o)[at + row] = fmaf(a, w, g * qk);
+    }
+    for (int x = 0; x < 4; ++x)
+        if (x * 32 + lane < d) p.S_out[base + x * 32 + lane] = s[x];
+}
+
+}  // namespace
+
+cudaError_t launch_gdn_step(const GdnStepArgs &a, bool bf16, cudaStream_t s)
+{
+    if (a.B == 0 || a.H == 0) return cudaSuccess;
+    if (a.B > 65535 || a.H > 65535) return cudaErrorNotSupported;
+    if (a.d == D) {
+        const dim3 grid(D / ROWS, (unsigned)a.H, (unsigned)a.B);
+        if (bf16) gdn_step_kernel<__nv_bfloat16><<<grid, NT, 0, s>>>(a), note_launch();
+        else gdn_step_kernel<float><<<grid, NT, 0, s>>>(a), note_launch();
+    } else {
+        gdn_step_any_kernel<<<dim3((unsigned)((a.d + NT / 32 - 1) / (NT / 32)), (unsigned)a.H, (unsigned)a.B), NT, 0, s>>>(a), note_launch();
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace hlta

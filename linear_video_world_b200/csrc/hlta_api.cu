@@ -1070,6 +1070,8 @@ hlta_status hlta_device_status(void *stream, unsigned int *code)
     if ((e = cudaMemcpy(ctx->err, &zero, sizeof zero, cudaMemcpyHostToDevice)) != cudaSuccess)
         return cuda_fail(e, "clear device error word");
     if (code) *code = word;
+    if (word == DEVERR_TABLE)
+        return fail(HLTA_ERR_INVALID_ARG, "a page, slot or length given to a kernel was out of range (device error word 0x%x)", word);
     if (word) return fail(HLTA_ERR_TIMEOUT, "a kernel's bounded wait expired (device error word 0x%x)", word);
     return HLTA_OK;
 }

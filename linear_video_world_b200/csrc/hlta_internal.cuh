@@ -206,15 +206,83 @@ cudaError_t launch_frame_advance(int *f, int F, cudaStream_t s);
 cudaError_t launch_rope(void *q, void *k, bool bf16, int B, int Htot, int h0, int Hr, long L,
                         int N, int d, double base, int pos_mode, int sign, cudaStream_t s);
 
+// Rotary positions over several axes (rope_axes.cu); q or k null: skipped.
+cudaError_t launch_rope_axes(const void *q, const void *k, void *q_out, void *k_out, int B, int Hq, int Hk,
+                             long L, int d, const hlta_rope_axes_t *sp, int inverse, bool bf16, cudaStream_t s);
+
+// A paged cache: pages [num_pages][H][1 << page_log2][d], tables as in hlta.h.
+struct PagedKV {
+    void *k, *v;
+    const int *table, *kv_lens;
+    long num_pages;
+    int H, d, page_log2, max_pages;
+    unsigned int *err;
+};
+cudaError_t launch_paged_append(const PagedKV &c, const void *k, const void *v, const int *new_lens, int B, long L,
+                                const hlta_rope_axes_t *sp, bool bf16, cudaStream_t s);
+
+// Attention of a chunk over a paged cache. The G query heads of a key head are consecutive, so
+// their G * L rows ("packed rows", row r: head r / L of the group, token r % L) are consecutive
+// rows of q and o.
+struct PagedAttnArgs {
+    PagedKV c;
+    const void *q;
+    void *o;
+    float *lse;                     // [B][Hq][L]; the launcher's caller points it into the workspace
+                                    // when only the weights need it; null when neither does
+    const float *w_in;
+    float *w_out, decay;
+    const int *new_lens;
+    int B, G;
+    long L;
+    int N, w;
+    float sl2;                      // softmax scale * log2(e)
+    void *ws;
+};
+size_t paged_attn_simt_bytes(int B, int Hq, int Hkv, long L, int d, int max_keys);
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, bool bf16, cudaStream_t s);
+
+struct PagedEvictArgs {
+    PagedKV c;
+    const float *weights;
+    int B, budget, sink, recent;
+    void *k_dst, *v_dst;
+    const int *dst_table;
+    long num_dst;
+    int max_dst;
+    int *new_lens, *kept;
+    float *w_out;
+    void *ws;
+};
+size_t paged_evict_bytes(int B, int H, int budget);
+cudaError_t launch_paged_evict(const PagedEvictArgs &a, bool bf16, cudaStream_t s);
+
+// Gated delta rule token by token over a pool of states (gdn_step.cu).
+struct GdnStepArgs {
+    const void *q, *k, *v;
+    const float *a, *b;             // gates, or the raw gate inputs
+    int raw;
+    float raw_c;
+    void *o;
+    const float *S;
+    float *S_out;
+    const int *slots, *lens;
+    int B, H, d;
+    long L, num_slots;
+    unsigned int *err;
+};
+cudaError_t launch_gdn_step(const GdnStepArgs &a, bool bf16, cudaStream_t s);
+
 // Device error word: kernels OR a code into it when a bounded wait expires (the bits are the
 // HLTA_DEVERR_* values of hlta.h).
 enum : unsigned int {
     DEVERR_ATTN_WAIT = 1u << 0,
     DEVERR_GDN_WAIT = 1u << 1,
     DEVERR_SELFTEST = 1u << 2,
+    DEVERR_TABLE = 1u << 3,
 };
 static_assert(DEVERR_ATTN_WAIT == HLTA_DEVERR_ATTN_WAIT && DEVERR_GDN_WAIT == HLTA_DEVERR_GDN_WAIT &&
-                  DEVERR_SELFTEST == HLTA_DEVERR_SELFTEST,
+                  DEVERR_SELFTEST == HLTA_DEVERR_SELFTEST && DEVERR_TABLE == HLTA_DEVERR_TABLE,
               "device error bits must match hlta.h");
 
 // Counts one kernel launch enqueued by the library (hlta_kernel_launches); every launch site
