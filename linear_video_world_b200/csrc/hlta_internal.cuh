@@ -240,7 +240,10 @@ struct PagedAttnArgs {
     void *ws;
 };
 size_t paged_attn_simt_bytes(int B, int Hq, int Hkv, long L, int d, int max_keys);
-cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, bool bf16, cudaStream_t s);
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s);                 // fp32
+cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, bool bf16, cudaStream_t s);   // after the attention
+size_t paged_attn_tc_bytes();
+cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s);                   // bf16
 
 struct PagedEvictArgs {
     PagedKV c;

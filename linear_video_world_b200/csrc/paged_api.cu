@@ -137,7 +137,7 @@ size_t hlta_paged_attn_workspace_bytes(int B, int Hq, int Hkv, long L, int d, in
         (long)max_pages * page > (1L << 30) || (dt != HLTA_BF16 && dt != HLTA_FP32))
         return 0;
     const size_t lse = weights ? pad((size_t)B * Hq * L * 4) : 0;
-    return lse + pad(paged_attn_simt_bytes(B, Hq, Hkv, L, d, max_pages * page)) + 256;
+    return lse + pad(dt == HLTA_BF16 ? paged_attn_tc_bytes() : paged_attn_simt_bytes(B, Hq, Hkv, L, d, max_pages * page)) + 256;
 }
 
 hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages, const int *table, const int *kv_lens,
@@ -182,7 +182,9 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
     a.N = N; a.w = w;
     a.sl2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d)) * 1.4426950408889634f;
     a.ws = ws;
-    return done(launch_paged_attn_simt(a, dt == HLTA_BF16, (cudaStream_t)stream), "paged attention");
+    cudaError_t e = dt == HLTA_BF16 ? launch_paged_attn_tc(a, (cudaStream_t)stream) : launch_paged_attn_simt(a, (cudaStream_t)stream);
+    if (e == cudaSuccess && w_out) e = launch_paged_weights_simt(a, dt == HLTA_BF16, (cudaStream_t)stream);
+    return done(e, "paged attention");
 }
 
 size_t hlta_paged_evict_workspace_bytes(int B, int Hkv, int budget)

@@ -313,12 +313,18 @@ cudaError_t run(const PagedAttnArgs &a, cudaStream_t s)
         if (blocks > 0x7fffffffL) return cudaErrorNotSupported;
         paged_join_kernel<E><<<(unsigned)blocks, THREADS, 0, s>>>(a, ns, m, l, o), note_launch();
     }
-    if (a.w_out) {
-        const size_t sw = (size_t)(KT * (dp + 4) + QB * dp + THREADS / 32 * KT) * 4;
-        if ((e = cudaFuncSetAttribute(paged_weights_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sw)) != cudaSuccess)
-            return e;
-        paged_weights_kernel<E><<<dim3((unsigned)((keys + KT - 1) / KT), (unsigned)(a.B * a.c.H)), THREADS, sw, s>>>(a), note_launch();
-    }
+    return cudaGetLastError();
+}
+
+template <typename E>
+cudaError_t run_weights(const PagedAttnArgs &a, cudaStream_t s)
+{
+    const int dp = (a.c.d + 3) & ~3, keys = a.c.max_pages << a.c.page_log2;
+    if ((long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
+    const size_t sw = (size_t)(KT * (dp + 4) + QB * dp + THREADS / 32 * KT) * 4;
+    cudaError_t e = cudaFuncSetAttribute(paged_weights_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sw);
+    if (e != cudaSuccess) return e;
+    paged_weights_kernel<E><<<dim3((unsigned)((keys + KT - 1) / KT), (unsigned)(a.B * a.c.H)), THREADS, sw, s>>>(a), note_launch();
     return cudaGetLastError();
 }
 
@@ -331,9 +337,11 @@ size_t paged_attn_simt_bytes(int B, int Hq, int Hkv, long L, int d, int max_keys
     return ns > 1 ? (size_t)ns * rows * (d + 2) * 4 : 0;
 }
 
-cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, bool bf16, cudaStream_t s)
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s) { return run<float>(a, s); }
+
+cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, bool bf16, cudaStream_t s)
 {
-    return bf16 ? run<__nv_bfloat16>(a, s) : run<float>(a, s);
+    return bf16 ? run_weights<__nv_bfloat16>(a, s) : run_weights<float>(a, s);
 }
 
 }  // namespace hlta

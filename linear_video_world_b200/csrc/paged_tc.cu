@@ -1,0 +1,630 @@
+// Attention of a chunk over a paged cache, bf16, head dim 128, on the sm_100a tensor cores.
+//
+// Exact softmax by 128-key tiles with a running maximum and sum. The division of the work over the
+// GPU (gangs over a line of key tiles, pieces joined by a second kernel) is in paged.cuh; a row
+// tile is 256 packed rows (two sub-tiles of 128) of one key head, so the query heads that share a
+// key head share its tiles too.
+// Roles of a block's 11 warps (one block per SM; as in the window attention kernel, with the walk
+// over pages in place of the walk over frames):
+//   warps 0-3 / 4-7  softmax of sub-tile 0 / 1, one thread per row (its tensor-memory lane)
+//   warp 8           producer: per piece Q, then K and V tiles through one ring of three 32 KB slots
+//                    in the order K0, K1, V0, K2, V1, ...; a lane per page of the tile looks the
+//                    page up and copies it by TMA to its rows of the swizzled tile (a page holds
+//                    whole groups of eight rows, so page and tile swizzle alike)
+//   warps 9, 10      issuers of sub-tile 0 / 1: S = Q K^T into tensor memory as soon as the softmax
+//                    has read the previous S into registers, O += P V once P is in shared memory;
+//                    committed in two halves so that the next P's first half can be stored early
+// O is rescaled only when a row's maximum grew by more than 2^8 (numerator and denominator share
+// the stale maximum). P is rounded to bf16 for the tensor cores (half a step, 2^-8 of each weight),
+// the sums are taken in fp32 before that rounding.
+//
+// What the cache holds where no row looks: pages without a visible key are not copied; keys that a
+// row does not see are masked to -inf before the maximum, whatever their score (NaN too), and the
+// values of keys outside the row tile's span are zeroed in shared memory before P V, since a weight
+// of zero times NaN is NaN.
+//
+// Every mbarrier wait is bounded; on expiry the kernel records DEVERR_ATTN_WAIT, every role
+// stops, and the tensor memory is released.
+#include "hlta_internal.cuh"
+#include "paged.cuh"
+#include "sm100_ptx.cuh"
+#include "tc_ptx.cuh"
+
+#include <algorithm>
+#include <math.h>
+
+namespace hlta {
+namespace {
+
+using namespace ptx;
+using namespace paged;
+
+constexpr int BM = 128, QT = 2, ROWS = BM * QT;     // rows per sub-tile, sub-tiles, rows per block
+constexpr int BN = 128, D = 128;                    // keys per tile, head dim
+constexpr int THREADS = 352;
+constexpr int WARP_TMA = 8, WARP_MMA = 9;
+constexpr uint32_t HALF = 128 * 128;                // [128 rows][64 columns] bf16
+constexpr uint32_t TILE = 2 * HALF;
+constexpr int NSLOT = 3;
+constexpr uint32_t SM_Q = 0, SM_SLOT = QT * TILE, SM_P = SM_SLOT + NSLOT * TILE;
+constexpr uint32_t SM_BAR = SM_P + QT * TILE;
+constexpr uint32_t TMEM_COLS = 512;                 // S of sub-tile q at 128 q, O at 256 + 128 q
+enum {
+    B_QFULL, B_QFREE,
+    B_FULL, B_EMPTY = B_FULL + NSLOT,               // per slot
+    B_SFULL = B_EMPTY + NSLOT,                      // per sub-tile from here
+    B_SFREE = B_SFULL + QT, B_PFULL = B_SFREE + QT, B_PVA = B_PFULL + QT, B_PVDONE = B_PVA + QT,
+    B_ODONE = B_PVDONE + QT, B_OFREE = B_ODONE + QT, NBARS = B_OFREE + QT
+};
+constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS;   // the block's start on the line
+constexpr uint32_t SM_TMEM = SM_PLACE + 32, SM_ABORT = SM_TMEM + 4, SM_TOTAL = SM_ABORT + 4;
+constexpr size_t SMEM_BYTES = SM_TOTAL + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
+static_assert(sizeof(Place) <= 32, "place");
+
+struct Params {
+    Line line;
+    PagedKV c;
+    int G, R, nr;                   // query heads a key head; packed rows; row tiles
+    float sl2;
+    __nv_bfloat16 *o;
+    float *lse;
+    float *part;                    // [block][2][32 column quads][256 rows] float4
+    float2 *ml;                     // [block][2][256 rows] (maximum, sum)
+};
+
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+        "mov.b64 pc, {%6, %7};\n\tfma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+        "add.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The span of the live rows among packed rows [r0, r1): tokens of a range that stays inside one
+// head are consecutive, one that runs into the next head covers the first or every token.
+__device__ __forceinline__ Span rows_span(const Params &p, const Roll &ro, int r0, int r1)
+{
+    const int L = p.line.L;
+    r1 = min(r1, p.R);
+    if (r0 >= r1) return Span{0, 0};
+    int i0 = r0 % L, i1 = i0 + (r1 - 1 - r0);
+    if (i1 >= L) {
+        // the range holds the head's last tokens and the next head's first ones
+        i0 = 0;
+        i1 = L - 1;
+    }
+    if (i0 >= ro.n) return Span{0, 0};
+    Span s;
+    s.lo = span_of(ro, i0, p.line.N, p.line.w).lo;
+    s.hi = span_of(ro, min(i1, ro.n - 1), p.line.N, p.line.w).hi;
+    if (s.hi <= s.lo) s.lo = s.hi = 0;
+    return s;
+}
+
+// A block's share of a piece: its row tile, the span of its rows, the key tiles of each sub-tile.
+struct Share {
+    Piece<BN> x;
+    int rt;
+    Span u;                         // span of the row tile
+    int ta, tb;                     // key tiles of the piece that the span touches
+    int a0, b0, a1, b1;             // of which sub-tile 0 / 1 needs [a, b)
+};
+__device__ __forceinline__ bool next_share(const Params &p, Place &c, int member, Share &s)
+{
+    if (!next_piece<BN>(p.line, c, s.x)) return false;
+    s.rt = s.x.pass * p.line.gs + member;
+    const int r0 = s.rt * ROWS;
+    auto clip = [&](const Span &v, int &a, int &b) {
+        a = max(s.x.ta, v.lo / BN);
+        b = min(s.x.tb, (v.hi + BN - 1) / BN);
+        if (v.hi <= v.lo || b < a) a = b = s.x.ta;
+    };
+    const Span v0 = rows_span(p, s.x.x.r, r0, r0 + BM), v1 = rows_span(p, s.x.x.r, r0 + BM, r0 + ROWS);
+    clip(v0, s.a0, s.b0);
+    clip(v1, s.a1, s.b1);
+    const bool e0 = v0.hi > v0.lo, e1 = v1.hi > v1.lo;
+    s.u.lo = e0 && e1 ? min(v0.lo, v1.lo) : e0 ? v0.lo : v1.lo;
+    s.u.hi = max(v0.hi, v1.hi);
+    // the tiles walked: from the first to the last that either sub-tile needs
+    const bool n0 = s.b0 > s.a0, n1 = s.b1 > s.a1;
+    s.ta = n0 && n1 ? min(s.a0, s.a1) : n0 ? s.a0 : s.a1;
+    s.tb = max(n0 ? s.b0 : s.ta, n1 ? s.b1 : s.ta);
+    return true;
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t sbase = smem_u32(smem);
+    auto BAR = [&](int i) { return sbase + SM_BAR + 8u * (uint32_t)i; };
+    volatile int *abort_flag = (volatile int *)(smem + SM_ABORT);
+    uint32_t *tmem_slot = (uint32_t *)(smem + SM_TMEM);
+    Place *place = (Place *)(smem + SM_PLACE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gang = blockIdx.x / p.line.gs, member = blockIdx.x % p.line.gs;
+
+    if (threadIdx.x == 0) {
+        mbar_init(BAR(B_QFULL), 1);
+        mbar_init(BAR(B_QFREE), 2);
+        for (int i = 0; i < NSLOT; ++i) {
+            mbar_init(BAR(B_FULL + i), 1);
+            mbar_init(BAR(B_EMPTY + i), 2);
+        }
+        for (int q = 0; q < QT; ++q) {
+            mbar_init(BAR(B_SFULL + q), 1);
+            mbar_init(BAR(B_SFREE + q), BM);
+            mbar_init(BAR(B_PFULL + q), BM);
+            mbar_init(BAR(B_PVA + q), 1);
+            mbar_init(BAR(B_PVDONE + q), 1);
+            mbar_init(BAR(B_ODONE + q), 1);
+            mbar_init(BAR(B_OFREE + q), BM);
+        }
+        *abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == WARP_TMA) {
+        const Place c = place_of<BN>(p.line, gang);
+        if (lane == 0) *place = c;
+    }
+    if (warp == WARP_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    auto wait_bar = [&](uint32_t bar, uint32_t parity) -> bool {
+        return mbar_try(bar, parity) || mbar_wait(bar, parity, abort_flag, p.c.err, DEVERR_ATTN_WAIT);
+    };
+    Place at = *place;
+    Share s;
+    // A share's ring items: K of its first tile, then K of tile j + 1 and V of tile j in turn: with n
+    // tiles, K(j) is item 2j - 1 (j >= 1), V(j) item 2j + 2, the last V item 2n - 1.
+
+    if (warp == WARP_TMA) {
+        int it = 0, units = 0;
+        bool ok = true;
+        const int psz = 1 << p.c.page_log2, npg = BN >> p.c.page_log2;
+        while (ok && next_share(p, at, member, s)) {
+            if (s.tb <= s.ta) continue;
+            if (s.x.x.r.bad && lane == 0) atomicOr(p.c.err, DEVERR_TABLE);
+            // the page of this lane's part of tile t, or -1 when none of its positions is seen
+            auto page_at = [&](int t) -> int {
+                const int p0 = t * BN + lane * psz;
+                return lane < npg && p0 < s.u.hi && p0 + psz > s.u.lo ? page_of(p.c, s.x.b, max(p0, s.u.lo)) : -1;
+            };
+            auto load = [&](const CUtensorMap *map, int pg) -> bool {
+                const int sl = it % NSLOT;
+                bool w = true;
+                if (lane == 0 && it >= NSLOT) w = wait_bar(BAR(B_EMPTY + sl), (uint32_t)((it / NSLOT) + 1) & 1u);
+                if (!__shfl_sync(0xffffffffu, w, 0)) return false;
+                const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
+                if (lane == 0) mbar_expect_tx(BAR(B_FULL + sl), (uint32_t)__popc(have) * (uint32_t)psz * 256u);
+                __syncwarp();
+                if (pg >= 0) {
+                    const int row = (pg * p.c.H + s.x.h) << p.c.page_log2;
+                    const uint32_t dst = sbase + SM_SLOT + (uint32_t)sl * TILE + (uint32_t)(lane * psz) * 128u;
+                    tma_load_2d(dst, map, 0, row, BAR(B_FULL + sl));
+                    tma_load_2d(dst + HALF, map, 64, row, BAR(B_FULL + sl));
+                }
+                ++it;
+                return true;
+            };
+            int kp = page_at(s.ta), vp;
+            if (units > 0) {
+                bool w = true;
+                if (lane == 0) w = wait_bar(BAR(B_QFREE), (uint32_t)(units - 1) & 1u);
+                if (!(ok = __shfl_sync(0xffffffffu, w, 0))) break;
+            }
+            if (lane == 0) {
+                const int row = (s.x.b * p.c.H + s.x.h) * p.R + s.rt * ROWS;
+                mbar_expect_tx(BAR(B_QFULL), QT * TILE);
+                for (int q = 0; q < QT; ++q)
+                    for (int x = 0; x < 2; ++x)
+                        tma_load_2d(sbase + SM_Q + q * TILE + x * HALF, &tq, 64 * x, row + q * BM, BAR(B_QFULL));
+            }
+            ++units;
+            ok = load(&tk, kp);
+            for (int t = s.ta; ok && t < s.tb; ++t) {
+                vp = kp;
+                if (t + 1 < s.tb) {
+                    kp = page_at(t + 1);
+                    if (!(ok = load(&tk, kp))) break;
+                }
+                ok = load(&tv, vp);
+            }
+        }
+        if (lane == 0 && *abort_flag) {
+            // a bounded wait expired somewhere: let the copies this block issued land
+            const long long t0 = clock64();
+            for (int i = it - 1; i >= 0 && i >= it - NSLOT; --i)
+                while (!mbar_try(BAR(B_FULL + i % NSLOT), (uint32_t)(i / NSLOT) & 1u) && clock64() - t0 < (1LL << 31)) {}
+            if (units > 0)
+                while (!mbar_try(BAR(B_QFULL), (uint32_t)(units - 1) & 1u) && clock64() - t0 < (1LL << 31)) {}
+        }
+    } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
+        if (lane == 0) {
+            const int q = warp - WARP_MMA;
+            constexpr uint32_t IDESC_S = tc::idesc_bf16(BM, BN, false, false), IDESC_O = tc::idesc_bf16(BM, D, false, true);
+            const uint64_t dq = tc::sw128_desc(sbase + SM_Q + q * TILE, 16, 1024);
+            const uint64_t dk0 = tc::sw128_desc(sbase + SM_SLOT, 16, 1024);       // K-major (K)
+            const uint64_t dv0 = tc::sw128_desc(sbase + SM_SLOT, HALF, 1024);     // MN-major (V)
+            const uint64_t dp = tc::sw128_desc(sbase + SM_P + q * TILE, 16, 1024);
+            const uint32_t s_tm = tmem + 128u * q, o_tm = tmem + 256u + 128u * q;
+            int it = 0, ns = 0, npv = 0, units = 0;
+            bool ok = true;
+            while (ok && next_share(p, at, member, s)) {
+                if (s.tb <= s.ta) continue;
+                const int a = q ? s.a1 : s.a0, b = q ? s.b1 : s.b0;
+                const int npv0 = npv;
+                if (!(ok = wait_bar(BAR(B_QFULL), (uint32_t)units & 1u))) break;
+                tc::fence_after_sync();
+                auto ofree = [&]() -> bool { return units < 1 || wait_bar(BAR(B_OFREE + q), (uint32_t)(units - 1) & 1u); };
+                auto do_k = [&](int t) -> bool {
+                    const int sl = it % NSLOT;
+                    if (!wait_bar(BAR(B_FULL + sl), (uint32_t)(it / NSLOT) & 1u)) return false;
+                    if (t >= a && t < b) {
+                        if (ns > 0 && !wait_bar(BAR(B_SFREE + q), (uint32_t)(ns - 1) & 1u)) return false;
+                        tc::fence_after_sync();
+                        const uint64_t dk = dk0 + (uint64_t)((sl * TILE) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                            tc::umma_bf16(s_tm, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
+                        }
+                        tc::umma_commit(BAR(B_SFULL + q));
+                        tc::umma_commit(BAR(B_EMPTY + sl));
+                        ++ns;
+                    } else {
+                        mbar_arrive(BAR(B_EMPTY + sl));
+                    }
+                    ++it;
+                    return true;
+                };
+                auto do_v = [&](int t) -> bool {
+                    const int sl = it % NSLOT;
+                    if (!wait_bar(BAR(B_FULL + sl), (uint32_t)(it / NSLOT) & 1u)) return false;
+                    if (t >= a && t < b) {
+                        if (!wait_bar(BAR(B_PFULL + q), (uint32_t)npv & 1u)) return false;
+                        // the share's first P V overwrites O: the previous epilogue must have read it
+                        if (npv == npv0 && !ofree()) return false;
+                        tc::fence_after_sync();
+                        const uint64_t dv = dv0 + (uint64_t)((sl * TILE) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk) {
+                            const uint64_t poff = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                            tc::umma_bf16(o_tm, dp + poff, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (npv > npv0 || kk > 0) ? 1u : 0u);
+                            if (kk == BN / 32 - 1) tc::umma_commit(BAR(B_PVA + q));
+                        }
+                        tc::umma_commit(BAR(B_PVDONE + q));
+                        tc::umma_commit(BAR(B_EMPTY + sl));
+                        ++npv;
+                    } else {
+                        mbar_arrive(BAR(B_EMPTY + sl));
+                    }
+                    ++it;
+                    return true;
+                };
+                ok = do_k(s.ta);
+                for (int t = s.ta; ok && t < s.tb; ++t) {
+                    if (t + 1 < s.tb) ok = do_k(t + 1);
+                    else tc::umma_commit(BAR(B_QFREE));           // the share's last S was issued
+                    ok = ok && do_v(t);
+                }
+                if (!ok) break;
+                // a share without a P V of this sub-tile still waits for the previous epilogue, so
+                // that its completion never runs two shares ahead of the softmax
+                if (npv == npv0 && !(ok = ofree())) break;
+                tc::umma_commit(BAR(B_ODONE + q));
+                ++units;
+            }
+        }
+    } else {
+        const int q = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t tlane = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t s_tm = tlane + 128u * q, o_tm = tlane + 256u + 128u * q;
+        const uint32_t prow = sbase + SM_P + (uint32_t)q * TILE + (uint32_t)row * 128u;
+        const uint32_t rx = (uint32_t)(row & 7);
+        constexpr float LAZY = 8.f;
+        bool ok = true;
+        int k = 0, units = 0, items = 0, piece = 0;
+        for (; ok && next_share(p, at, member, s); ++piece) {
+            const int r = s.rt * ROWS + q * BM + row, i = r % p.line.L;
+            const bool live = r < p.R && i < s.x.x.r.n;
+            // a row that is none takes the row tile's span: it computes what nobody reads, and its
+            // warp keeps to the unmasked path
+            const Span v = live ? span_of(s.x.x.r, i, p.line.N, p.line.w) : s.u;
+            const int a = q ? s.a1 : s.a0, b = q ? s.b1 : s.b0, n = s.tb - s.ta;
+            float m = -INFINITY, lsum = 0.f;
+            const int k0 = k;
+            for (int t = a; t < b; ++t, ++k) {
+                if (!__all_sync(0xffffffffu, wait_bar(BAR(B_SFULL + q), (uint32_t)k & 1u))) { ok = false; break; }
+                tc::fence_after_sync();
+                uint32_t sa[64], sb[64];
+                tc::tmem_ld64(s_tm, sa);
+                tc::tmem_ld64(s_tm + 64, sb);
+                tc::fence_before_sync();
+                mbar_arrive(BAR(B_SFREE + q));
+                const int p0 = t * BN;
+                if (__any_sync(0xffffffffu, v.lo > p0 || v.hi < p0 + BN)) {
+                    const int lo = v.lo - p0, hi = v.hi - p0;
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) {
+                        if (x < lo || x >= hi) sa[x] = __float_as_uint(-INFINITY);
+                        if (64 + x < lo || 64 + x >= hi) sb[x] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    asm("max.f32 %0, %0, %1, %2;" : "+f"(mx0) : "f"(__uint_as_float(sa[2 * x])), "f"(__uint_as_float(sa[2 * x + 1])));
+                    asm("max.f32 %0, %0, %1, %2;" : "+f"(mx1) : "f"(__uint_as_float(sb[2 * x])), "f"(__uint_as_float(sb[2 * x + 1])));
+                }
+                const float mnew = fmaxf(m, fmaxf(mx0, mx1) * p.sl2);
+                const bool need = mnew > m + LAZY;
+                const float muse = need ? mnew : m;
+                const float alpha = (need && m != -INFINITY) ? tc::ex2(m - mnew) : 1.f;
+                const float negm = muse == -INFINITY ? 0.f : -muse;
+                const float2 sl = make_float2(p.sl2, p.sl2), nm = make_float2(negm, negm);
+                float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[64];
+                auto half = [&](const uint32_t (&sv)[64], int o) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const float2 e = ffma2(make_float2(__uint_as_float(sv[2 * x]), __uint_as_float(sv[2 * x + 1])), sl, nm);
+                        const float2 w = make_float2(tc::ex2(e.x), tc::ex2(e.y));
+                        ps[x & 1] = fadd2(ps[x & 1], w);
+                        pk[o + x] = tc::pack_bf16(w.x, w.y);
+                    }
+                };
+                auto store = [&](int h) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + (uint32_t)h * HALF + ((((uint32_t)c) ^ rx) << 4)),
+                                     "r"(pk[h * 32 + c * 4]), "r"(pk[h * 32 + c * 4 + 1]), "r"(pk[h * 32 + c * 4 + 2]), "r"(pk[h * 32 + c * 4 + 3])
+                                     : "memory");
+                };
+                half(sa, 0);
+                const bool resc = k > k0 && __any_sync(0xffffffffu, need && m != -INFINITY);
+                if (k >= 1 && !__all_sync(0xffffffffu, wait_bar(BAR(B_PVA + q), (uint32_t)(k - 1) & 1u))) { ok = false; break; }
+                if (!resc) store(0);
+                half(sb, 32);
+                if (k >= 1 && !__all_sync(0xffffffffu, wait_bar(BAR(B_PVDONE + q), (uint32_t)(k - 1) & 1u))) { ok = false; break; }
+                tc::fence_after_sync();
+                if (resc) {
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t orow[32];
+                        tc::tmem_ld32(o_tm + cc * 32, orow);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) orow[x] = __float_as_uint(__uint_as_float(orow[x]) * alpha);
+                        tc::tmem_st32(o_tm + cc * 32, orow);
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    store(0);
+                }
+                store(1);
+                lsum = lsum * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
+                m = muse;
+                if (s.u.lo > p0 || s.u.hi < p0 + BN) {
+                    // values outside the row tile's span: zeros (each sub-tile that reads the tile
+                    // writes them before its own P V)
+                    const int j = t - s.ta, item = items + (j + 1 < n ? 2 * j + 2 : 2 * j + 1), sl2 = item % NSLOT;
+                    if (!__all_sync(0xffffffffu, wait_bar(BAR(B_FULL + sl2), (uint32_t)(item / NSLOT) & 1u))) { ok = false; break; }
+                    if (p0 + row < s.u.lo || p0 + row >= s.u.hi) {
+                        const uint32_t vrow = sbase + SM_SLOT + (uint32_t)sl2 * TILE + (uint32_t)row * 128u;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + (c >> 3) * HALF + (c & 7) * 16), "r"(0) : "memory");
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(BAR(B_PFULL + q));
+            }
+            if (!ok) break;
+            const bool worked = n > 0;
+            items += 2 * n;
+            if (worked) {
+                if (!__all_sync(0xffffffffu, wait_bar(BAR(B_ODONE + q), (uint32_t)units & 1u))) { ok = false; break; }
+                tc::fence_after_sync();
+                ++units;
+            }
+            const bool have = k > k0;
+            const long grow = (long)(s.x.b * p.c.H + s.x.h) * p.R + r;
+            if (s.x.whole) {
+                const float inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
+                if (p.lse && live) p.lse[grow] = (m + log2f(lsum)) * 0.69314718055994531f;
+                __nv_bfloat16 *orow = p.o + grow * D;
+#pragma unroll
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t ov[32];
+                    __syncwarp();
+                    if (have) tc::tmem_ld32(o_tm + cc * 32, ov);
+                    if (live) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            w[x] = have ? tc::pack_bf16(__uint_as_float(ov[2 * x]) * inv, __uint_as_float(ov[2 * x + 1]) * inv) : 0u;
+                        uint4 *dst = reinterpret_cast<uint4 *>(orow + cc * 32);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                    }
+                }
+            } else {
+                const int rr = q * BM + row;
+                const long slot = (long)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
+                if (live) p.ml[slot * ROWS + rr] = make_float2(m, lsum);
+                float4 *dst = reinterpret_cast<float4 *>(p.part) + slot * (D / 4) * ROWS + rr;
+                if (have) {
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t ov[32];
+                        __syncwarp();
+                        tc::tmem_ld32(o_tm + cc * 32, ov);
+                        if (live) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                dst[(cc * 8 + x) * ROWS] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]),
+                                                                       __uint_as_float(ov[4 * x + 2]), __uint_as_float(ov[4 * x + 3]));
+                        }
+                    }
+                }
+            }
+            if (worked) {
+                tc::fence_before_sync();
+                mbar_arrive(BAR(B_OFREE + q));
+            }
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == WARP_MMA) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+// Joins the pieces of heads whose keys were cut, in the order of the gangs; rows that see no key
+// get zeros here. A block takes 32 rows (a lane each), a warp 16 channels of them.
+__global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constant__ Params p)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nb = (p.R + 31) / 32;
+    const int bh = blockIdx.x / nb, r = (blockIdx.x % nb) * 32 + lane;
+    const int b = bh / p.c.H, h = bh % p.c.H;
+    const int rt = r / ROWS, pass = rt / p.line.gs, member = rt % p.line.gs, rr = r % ROWS;
+    const Holders g = holders_of<BN>(p.line, pass, b, h);
+    if (g.T > 0 && g.g0 == g.g1) return;
+    const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
+    if (ro.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
+    if (r >= p.R || r % p.line.L >= ro.n) return;
+    float m = -INFINITY, l = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (g.T > 0) {
+        for (int i = g.g0; i <= g.g1; ++i) {
+            const long slot = ((long)i * p.line.gs + member) * 2 + (i == g.g0 ? g.slot0 : 0);
+            m = fmaxf(m, p.ml[slot * ROWS + rr].x);
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        for (int i = g.g0; i <= g.g1; ++i) {
+            const long slot = ((long)i * p.line.gs + member) * 2 + (i == g.g0 ? g.slot0 : 0);
+            const float2 ml = p.ml[slot * ROWS + rr];
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;       // none of the piece's keys: no output written
+            const float f = exp2f(ml.x - base);
+            l = fmaf(ml.y, f, l);
+            const float4 *src = reinterpret_cast<const float4 *>(p.part) + slot * (D / 4) * ROWS + rr;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float4 v = src[(warp * 4 + x) * ROWS];
+                acc[x].x = fmaf(v.x, f, acc[x].x);
+                acc[x].y = fmaf(v.y, f, acc[x].y);
+                acc[x].z = fmaf(v.z, f, acc[x].z);
+                acc[x].w = fmaf(v.w, f, acc[x].w);
+            }
+        }
+    }
+    const long row = (long)bh * p.R + r;
+    const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+    uint32_t w[8];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        w[2 * x] = tc::pack_bf16(acc[x].x * inv, acc[x].y * inv);
+        w[2 * x + 1] = tc::pack_bf16(acc[x].z * inv, acc[x].w * inv);
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(p.o + row * D + warp * 16);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (p.lse && warp == 0) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
+}
+
+int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 148;
+    }
+    return n;
+}
+
+// Blocks per gang for nr row tiles on `sms` SMs: as many as waste the fewest block-passes, the
+// largest of equals (more blocks that meet in L2).
+int gang_size(int nr, int sms)
+{
+    int best = 1;
+    double top = 0;
+    for (int g = 1; g <= std::min(nr, sms); ++g) {
+        const int passes = (nr + g - 1) / g;
+        const double use = (double)nr / ((double)passes * g) * ((double)(sms / g) * g / sms);
+        if (use >= top - 1e-9) {
+            top = std::max(top, use);
+            best = g;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+size_t paged_attn_tc_bytes() { return (size_t)sm_count() * 2 * ROWS * (D * 4 + 8); }
+
+cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
+{
+    const long R = a.G * a.L;
+    const long q_rows = (long)a.B * a.c.H * R, kv_rows = a.c.num_pages * a.c.H << a.c.page_log2;
+    if (R == 0 || a.B == 0) return cudaSuccess;
+    if (q_rows + ROWS >= (1L << 31) || kv_rows + BN >= (1L << 31)) return cudaErrorNotSupported;
+    const int psz = 1 << a.c.page_log2;
+    CUtensorMap mq, mk, mv;
+    cudaError_t e;
+    if ((e = make_tmap_2d_bf16(&mq, a.q, q_rows, D, 64, BM, true)) != cudaSuccess) return e;
+    if ((e = make_tmap_2d_bf16(&mk, a.c.k, kv_rows, D, 64, (uint32_t)psz, true)) != cudaSuccess) return e;
+    if ((e = make_tmap_2d_bf16(&mv, a.c.v, kv_rows, D, 64, (uint32_t)psz, true)) != cudaSuccess) return e;
+    const int sms = sm_count();
+    Params p;
+    p.c = a.c;
+    p.G = a.G;
+    p.R = (int)R;
+    p.nr = (int)((R + ROWS - 1) / ROWS);
+    p.line.B = a.B; p.line.H = a.c.H; p.line.L = (int)a.L; p.line.N = a.N; p.line.w = a.w;
+    p.line.cap = a.c.max_pages << a.c.page_log2;
+    p.line.kv_lens = a.c.kv_lens; p.line.new_lens = a.new_lens;
+    p.line.gs = gang_size(p.nr, sms);
+    p.line.ngang = sms / p.line.gs;
+    p.line.passes = (p.nr + p.line.gs - 1) / p.line.gs;
+    p.sl2 = a.sl2;
+    p.o = (__nv_bfloat16 *)a.o;
+    p.lse = a.lse;
+    p.part = (float *)a.ws;
+    p.ml = (float2 *)((char *)a.ws + (size_t)sms * 2 * ROWS * D * 4);
+    if ((e = cudaFuncSetAttribute(paged_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess) return e;
+    paged_attn_tc_kernel<<<p.line.gs * p.line.ngang, THREADS, SMEM_BYTES, s>>>(mq, mk, mv, p), note_launch();
+    const long blocks = (long)a.B * a.c.H * ((R + 31) / 32);
+    if (blocks > 0x7fffffffL) return cudaErrorNotSupported;
+    paged_join_tc_kernel<<<(unsigned)blocks, 256, 0, s>>>(p), note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace hlta
