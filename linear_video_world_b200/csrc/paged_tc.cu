@@ -4,16 +4,28 @@
 // GPU (gangs over a line of key tiles, pieces joined by a second kernel) is in paged.cuh; a row
 // tile is 256 packed rows (two sub-tiles of 128) of one key head, so the query heads that share a
 // key head share its tiles too.
-// Roles of a block's 11 warps (one block per SM; as in the window attention kernel, with the walk
-// over pages in place of the walk over frames):
+// Roles of a block's 12 warps (one block per SM):
 //   warps 0-3 / 4-7  softmax of sub-tile 0 / 1, one thread per row (its tensor-memory lane)
-//   warp 8           producer: per piece Q, then K and V tiles through one ring of three 32 KB slots
-//                    in the order K0, K1, V0, K2, V1, ...; a lane per page of the tile looks the
-//                    page up and copies it by TMA to its rows of the swizzled tile (a page holds
-//                    whole groups of eight rows, so page and tile swizzle alike)
-//   warps 9, 10      issuers of sub-tile 0 / 1: S = Q K^T into tensor memory as soon as the softmax
-//                    has read the previous S into registers, O += P V once P is in shared memory;
-//                    committed in two halves so that the next P's first half can be stored early
+//   warp 8           producer: per share Q, then K and V tiles through one ring of five 32 KB slots
+//                    in the order K0, V0, K1, V1, ...; a lane per page of the tile looks the page up
+//                    and copies it by TMA to its rows of the swizzled tile (a page holds whole
+//                    groups of eight rows, so page and tile swizzle alike)
+//   warps 9, 10      issuers of sub-tile 0 / 1
+//   warp 11          completes the warpgroup that gives registers to the softmax warps
+// Per sub-tile and tile: S = Q K^T into 128 columns of tensor memory; the softmax reads them into
+// registers, and writes P as bf16 over the first 64 of the same columns, in two halves; O += P V
+// with P from tensor memory (an operand that costs no shared-memory reads), then S of the next
+// tile, issued behind it in the same order, overwrites P. The completion of S therefore also says
+// that the previous P V is done, and O may be rescaled. One sub-tile's products run while the
+// other's softmax does.
+// Why P is not in shared memory: a 128 x 128 x 16 product from shared memory reads 8 KB for 32
+// cycles of math, twice what shared memory delivers. With P there too, a pair of sub-tiles moves
+// 384 KB per 128 keys (operands, P's stores, the copies in), 3072 cycles at 128 B per cycle;
+// this way it moves 256 KB. The exponentials take 2048 cycles (16 per cycle).
+// The softmax keeps a row's 128 scores in registers: 168 registers a thread (what 384 threads may
+// have) spilled, and with all of the SM's memory given to shared memory a spilled register comes
+// back from L2. The last warpgroup gives its registers to the other two (56 / 224), and the share's
+// bookkeeping is worked out twice instead of being kept across the tiles.
 // O is rescaled only when a row's maximum grew by more than 2^8 (numerator and denominator share
 // the stale maximum). P is rounded to bf16 for the tensor cores (half a step, 2^-8 of each weight),
 // the sums are taken in fp32 before that rounding.
@@ -41,23 +53,23 @@ using namespace paged;
 
 constexpr int BM = 128, QT = 2, ROWS = BM * QT;     // rows per sub-tile, sub-tiles, rows per block
 constexpr int BN = 128, D = 128;                    // keys per tile, head dim
-constexpr int THREADS = 352;
+constexpr int THREADS = 384;                        // 8 softmax warps, producer, two issuers, one that only pads
+                                                    // the last warpgroup (registers move between warpgroups)
 constexpr int WARP_TMA = 8, WARP_MMA = 9;
 constexpr uint32_t HALF = 128 * 128;                // [128 rows][64 columns] bf16
 constexpr uint32_t TILE = 2 * HALF;
-constexpr int NSLOT = 3;
-constexpr uint32_t SM_Q = 0, SM_SLOT = QT * TILE, SM_P = SM_SLOT + NSLOT * TILE;
-constexpr uint32_t SM_BAR = SM_P + QT * TILE;
-constexpr uint32_t TMEM_COLS = 512;                 // S of sub-tile q at 128 q, O at 256 + 128 q
+constexpr int NSLOT = 5;
+constexpr uint32_t SM_Q = 0, SM_SLOT = QT * TILE, SM_BAR = SM_SLOT + NSLOT * TILE;
+constexpr uint32_t TMEM_COLS = 512;                 // S (and P over it) of sub-tile q at 128 q, O at 256 + 128 q
 enum {
     B_QFULL, B_QFREE,
     B_FULL, B_EMPTY = B_FULL + NSLOT,               // per slot
     B_SFULL = B_EMPTY + NSLOT,                      // per sub-tile from here
-    B_SFREE = B_SFULL + QT, B_PFULL = B_SFREE + QT, B_PVA = B_PFULL + QT, B_PVDONE = B_PVA + QT,
-    B_ODONE = B_PVDONE + QT, B_OFREE = B_ODONE + QT, NBARS = B_OFREE + QT
+    B_PA = B_SFULL + QT, B_PB = B_PA + QT,          // the halves of P
+    B_ODONE = B_PB + QT, B_OFREE = B_ODONE + QT, NBARS = B_OFREE + QT
 };
-constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS;   // the block's start on the line
-constexpr uint32_t SM_TMEM = SM_PLACE + 32, SM_ABORT = SM_TMEM + 4, SM_TOTAL = SM_ABORT + 4;
+constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS;   // the block's start on the line, then each softmax warp's place
+constexpr uint32_t SM_TMEM = SM_PLACE + 9 * 32, SM_ABORT = SM_TMEM + 4, SM_TOTAL = SM_ABORT + 4;
 constexpr size_t SMEM_BYTES = SM_TOTAL + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
 static_assert(sizeof(Place) <= 32, "place");
@@ -90,6 +102,23 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+
+// The bounded wait of sm100_ptx.cuh, inlined: a kernel that moves registers between its warpgroups
+// may not call functions.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned int *err)
+{
+    if (mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > (1LL << 32)) {
+            *abort_flag = 1;
+            atomicOr(err, DEVERR_ATTN_WAIT);
+            return false;
+        }
+    }
 }
 
 // The span of the live rows among packed rows [r0, r1): tokens of a range that stays inside one
@@ -154,7 +183,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     auto BAR = [&](int i) { return sbase + SM_BAR + 8u * (uint32_t)i; };
     volatile int *abort_flag = (volatile int *)(smem + SM_ABORT);
     uint32_t *tmem_slot = (uint32_t *)(smem + SM_TMEM);
-    Place *place = (Place *)(smem + SM_PLACE);
+    auto place = [&](int i) { return (Place *)(smem + SM_PLACE + 32 * i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gang = blockIdx.x / p.line.gs, member = blockIdx.x % p.line.gs;
 
@@ -167,10 +196,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         }
         for (int q = 0; q < QT; ++q) {
             mbar_init(BAR(B_SFULL + q), 1);
-            mbar_init(BAR(B_SFREE + q), BM);
-            mbar_init(BAR(B_PFULL + q), BM);
-            mbar_init(BAR(B_PVA + q), 1);
-            mbar_init(BAR(B_PVDONE + q), 1);
+            mbar_init(BAR(B_PA + q), BM);
+            mbar_init(BAR(B_PB + q), BM);
             mbar_init(BAR(B_ODONE + q), 1);
             mbar_init(BAR(B_OFREE + q), BM);
         }
@@ -179,7 +206,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     }
     if (warp == WARP_TMA) {
         const Place c = place_of<BN>(p.line, gang);
-        if (lane == 0) *place = c;
+        if (lane < 9) *place(lane) = c;
     }
     if (warp == WARP_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(TMEM_COLS)
@@ -191,263 +218,260 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     auto wait_bar = [&](uint32_t bar, uint32_t parity) -> bool {
-        return mbar_try(bar, parity) || mbar_wait(bar, parity, abort_flag, p.c.err, DEVERR_ATTN_WAIT);
+        return wait_inline(bar, parity, abort_flag, p.c.err);
     };
-    Place at = *place;
-    Share s;
-    // A share's ring items: K of its first tile, then K of tile j + 1 and V of tile j in turn: with n
-    // tiles, K(j) is item 2j - 1 (j >= 1), V(j) item 2j + 2, the last V item 2n - 1.
+    // A share's ring items: K and V of its tiles in turn: K(j) is item 2j, V(j) item 2j + 1.
 
-    if (warp == WARP_TMA) {
-        int it = 0, units = 0;
-        bool ok = true;
-        const int psz = 1 << p.c.page_log2, npg = BN >> p.c.page_log2;
-        while (ok && next_share(p, at, member, s)) {
-            if (s.tb <= s.ta) continue;
-            if (s.x.x.r.bad && lane == 0) atomicOr(p.c.err, DEVERR_TABLE);
-            // the page of this lane's part of tile t, or -1 when none of its positions is seen
-            auto page_at = [&](int t) -> int {
-                const int p0 = t * BN + lane * psz;
-                return lane < npg && p0 < s.u.hi && p0 + psz > s.u.lo ? page_of(p.c, s.x.b, max(p0, s.u.lo)) : -1;
-            };
-            auto load = [&](const CUtensorMap *map, int pg) -> bool {
-                const int sl = it % NSLOT;
-                bool w = true;
-                if (lane == 0 && it >= NSLOT) w = wait_bar(BAR(B_EMPTY + sl), (uint32_t)((it / NSLOT) + 1) & 1u);
-                if (!__shfl_sync(0xffffffffu, w, 0)) return false;
-                const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
-                if (lane == 0) mbar_expect_tx(BAR(B_FULL + sl), (uint32_t)__popc(have) * (uint32_t)psz * 256u);
-                __syncwarp();
-                if (pg >= 0) {
-                    const int row = (pg * p.c.H + s.x.h) << p.c.page_log2;
-                    const uint32_t dst = sbase + SM_SLOT + (uint32_t)sl * TILE + (uint32_t)(lane * psz) * 128u;
-                    tma_load_2d(dst, map, 0, row, BAR(B_FULL + sl));
-                    tma_load_2d(dst + HALF, map, 64, row, BAR(B_FULL + sl));
-                }
-                ++it;
-                return true;
-            };
-            int kp = page_at(s.ta), vp;
-            if (units > 0) {
-                bool w = true;
-                if (lane == 0) w = wait_bar(BAR(B_QFREE), (uint32_t)(units - 1) & 1u);
-                if (!(ok = __shfl_sync(0xffffffffu, w, 0))) break;
-            }
-            if (lane == 0) {
-                const int row = (s.x.b * p.c.H + s.x.h) * p.R + s.rt * ROWS;
-                mbar_expect_tx(BAR(B_QFULL), QT * TILE);
-                for (int q = 0; q < QT; ++q)
-                    for (int x = 0; x < 2; ++x)
-                        tma_load_2d(sbase + SM_Q + q * TILE + x * HALF, &tq, 64 * x, row + q * BM, BAR(B_QFULL));
-            }
-            ++units;
-            ok = load(&tk, kp);
-            for (int t = s.ta; ok && t < s.tb; ++t) {
-                vp = kp;
-                if (t + 1 < s.tb) {
-                    kp = page_at(t + 1);
-                    if (!(ok = load(&tk, kp))) break;
-                }
-                ok = load(&tv, vp);
-            }
-        }
-        if (lane == 0 && *abort_flag) {
-            // a bounded wait expired somewhere: let the copies this block issued land
-            const long long t0 = clock64();
-            for (int i = it - 1; i >= 0 && i >= it - NSLOT; --i)
-                while (!mbar_try(BAR(B_FULL + i % NSLOT), (uint32_t)(i / NSLOT) & 1u) && clock64() - t0 < (1LL << 31)) {}
-            if (units > 0)
-                while (!mbar_try(BAR(B_QFULL), (uint32_t)(units - 1) & 1u) && clock64() - t0 < (1LL << 31)) {}
-        }
-    } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
-        if (lane == 0) {
-            const int q = warp - WARP_MMA;
-            constexpr uint32_t IDESC_S = tc::idesc_bf16(BM, BN, false, false), IDESC_O = tc::idesc_bf16(BM, D, false, true);
-            const uint64_t dq = tc::sw128_desc(sbase + SM_Q + q * TILE, 16, 1024);
-            const uint64_t dk0 = tc::sw128_desc(sbase + SM_SLOT, 16, 1024);       // K-major (K)
-            const uint64_t dv0 = tc::sw128_desc(sbase + SM_SLOT, HALF, 1024);     // MN-major (V)
-            const uint64_t dp = tc::sw128_desc(sbase + SM_P + q * TILE, 16, 1024);
-            const uint32_t s_tm = tmem + 128u * q, o_tm = tmem + 256u + 128u * q;
-            int it = 0, ns = 0, npv = 0, units = 0;
+    if (warp >= WARP_TMA) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == WARP_TMA) {
+            Place at = *place(0);
+            Share s;
+            int it = 0, units = 0;
             bool ok = true;
+            const int psz = 1 << p.c.page_log2, npg = BN >> p.c.page_log2;
             while (ok && next_share(p, at, member, s)) {
                 if (s.tb <= s.ta) continue;
-                const int a = q ? s.a1 : s.a0, b = q ? s.b1 : s.b0;
-                const int npv0 = npv;
-                if (!(ok = wait_bar(BAR(B_QFULL), (uint32_t)units & 1u))) break;
-                tc::fence_after_sync();
-                auto ofree = [&]() -> bool { return units < 1 || wait_bar(BAR(B_OFREE + q), (uint32_t)(units - 1) & 1u); };
-                auto do_k = [&](int t) -> bool {
+                if (s.x.x.r.bad && lane == 0) atomicOr(p.c.err, DEVERR_TABLE);
+                // the page of this lane's part of tile t, or -1 when none of its positions is seen
+                auto page_at = [&](int t) -> int {
+                    const int p0 = t * BN + lane * psz;
+                    return lane < npg && p0 < s.u.hi && p0 + psz > s.u.lo ? page_of(p.c, s.x.b, max(p0, s.u.lo)) : -1;
+                };
+                auto load = [&](const CUtensorMap *map, int pg) -> bool {
                     const int sl = it % NSLOT;
-                    if (!wait_bar(BAR(B_FULL + sl), (uint32_t)(it / NSLOT) & 1u)) return false;
-                    if (t >= a && t < b) {
-                        if (ns > 0 && !wait_bar(BAR(B_SFREE + q), (uint32_t)(ns - 1) & 1u)) return false;
-                        tc::fence_after_sync();
-                        const uint64_t dk = dk0 + (uint64_t)((sl * TILE) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                            tc::umma_bf16(s_tm, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
-                        }
-                        tc::umma_commit(BAR(B_SFULL + q));
-                        tc::umma_commit(BAR(B_EMPTY + sl));
-                        ++ns;
-                    } else {
-                        mbar_arrive(BAR(B_EMPTY + sl));
+                    bool w = true;
+                    if (lane == 0 && it >= NSLOT) w = wait_bar(BAR(B_EMPTY + sl), (uint32_t)((it / NSLOT) + 1) & 1u);
+                    if (!__shfl_sync(0xffffffffu, w, 0)) return false;
+                    const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
+                    if (lane == 0) mbar_expect_tx(BAR(B_FULL + sl), (uint32_t)__popc(have) * (uint32_t)psz * 256u);
+                    __syncwarp();
+                    if (pg >= 0) {
+                        const int row = (pg * p.c.H + s.x.h) << p.c.page_log2;
+                        const uint32_t dst = sbase + SM_SLOT + (uint32_t)sl * TILE + (uint32_t)(lane * psz) * 128u;
+                        tma_load_2d(dst, map, 0, row, BAR(B_FULL + sl));
+                        tma_load_2d(dst + HALF, map, 64, row, BAR(B_FULL + sl));
                     }
                     ++it;
                     return true;
                 };
-                auto do_v = [&](int t) -> bool {
-                    const int sl = it % NSLOT;
-                    if (!wait_bar(BAR(B_FULL + sl), (uint32_t)(it / NSLOT) & 1u)) return false;
-                    if (t >= a && t < b) {
-                        if (!wait_bar(BAR(B_PFULL + q), (uint32_t)npv & 1u)) return false;
-                        // the share's first P V overwrites O: the previous epilogue must have read it
-                        if (npv == npv0 && !ofree()) return false;
-                        tc::fence_after_sync();
-                        const uint64_t dv = dv0 + (uint64_t)((sl * TILE) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk) {
-                            const uint64_t poff = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                            tc::umma_bf16(o_tm, dp + poff, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (npv > npv0 || kk > 0) ? 1u : 0u);
-                            if (kk == BN / 32 - 1) tc::umma_commit(BAR(B_PVA + q));
-                        }
-                        tc::umma_commit(BAR(B_PVDONE + q));
-                        tc::umma_commit(BAR(B_EMPTY + sl));
-                        ++npv;
-                    } else {
-                        mbar_arrive(BAR(B_EMPTY + sl));
-                    }
-                    ++it;
-                    return true;
-                };
-                ok = do_k(s.ta);
-                for (int t = s.ta; ok && t < s.tb; ++t) {
-                    if (t + 1 < s.tb) ok = do_k(t + 1);
-                    else tc::umma_commit(BAR(B_QFREE));           // the share's last S was issued
-                    ok = ok && do_v(t);
+                int pg = page_at(s.ta);
+                if (units > 0) {
+                    bool w = true;
+                    if (lane == 0) w = wait_bar(BAR(B_QFREE), (uint32_t)(units - 1) & 1u);
+                    if (!(ok = __shfl_sync(0xffffffffu, w, 0))) break;
                 }
-                if (!ok) break;
-                // a share without a P V of this sub-tile still waits for the previous epilogue, so
-                // that its completion never runs two shares ahead of the softmax
-                if (npv == npv0 && !(ok = ofree())) break;
-                tc::umma_commit(BAR(B_ODONE + q));
+                if (lane == 0) {
+                    const int row = (s.x.b * p.c.H + s.x.h) * p.R + s.rt * ROWS;
+                    mbar_expect_tx(BAR(B_QFULL), QT * TILE);
+                    for (int q = 0; q < QT; ++q)
+                        for (int x = 0; x < 2; ++x)
+                            tma_load_2d(sbase + SM_Q + q * TILE + x * HALF, &tq, 64 * x, row + q * BM, BAR(B_QFULL));
+                }
                 ++units;
+                for (int t = s.ta; ok && t < s.tb; ++t) {
+                    const int next = t + 1 < s.tb ? page_at(t + 1) : -1;      // looked up ahead of the waits
+                    ok = load(&tk, pg) && load(&tv, pg);
+                    pg = next;
+                }
+            }
+            if (lane == 0 && *abort_flag) {
+                // a bounded wait expired somewhere: let the copies this block issued land
+                const long long t0 = clock64();
+                for (int i = it - 1; i >= 0 && i >= it - NSLOT; --i)
+                    while (!mbar_try(BAR(B_FULL + i % NSLOT), (uint32_t)(i / NSLOT) & 1u) && clock64() - t0 < (1LL << 31)) {}
+                if (units > 0)
+                    while (!mbar_try(BAR(B_QFULL), (uint32_t)(units - 1) & 1u) && clock64() - t0 < (1LL << 31)) {}
+            }
+        } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
+            if (lane == 0) {
+                const int q = warp - WARP_MMA;
+                constexpr uint32_t IDESC_S = tc::idesc_bf16(BM, BN, false, false), IDESC_O = tc::idesc_bf16(BM, D, false, true);
+                const uint64_t dq = tc::sw128_desc(sbase + SM_Q + q * TILE, 16, 1024);
+                const uint64_t dk0 = tc::sw128_desc(sbase + SM_SLOT, 16, 1024);       // K-major (K)
+                const uint64_t dv0 = tc::sw128_desc(sbase + SM_SLOT, HALF, 1024);     // MN-major (V)
+                const uint32_t s_tm = tmem + 128u * q, o_tm = tmem + 256u + 128u * q;
+                Place at = *place(0);
+                Share s;
+                int it = 0, np = 0, units = 0;
+                bool ok = true;
+                while (ok && next_share(p, at, member, s)) {
+                    if (s.tb <= s.ta) continue;
+                    const int a = q ? s.a1 : s.a0, b = q ? s.b1 : s.b0;
+                    const int np0 = np;
+                    if (!(ok = wait_bar(BAR(B_QFULL), (uint32_t)units & 1u))) break;
+                    tc::fence_after_sync();
+                    auto ofree = [&]() -> bool { return units < 1 || wait_bar(BAR(B_OFREE + q), (uint32_t)(units - 1) & 1u); };
+                    auto do_k = [&](int t) -> bool {
+                        const int sl = it % NSLOT;
+                        if (!wait_bar(BAR(B_FULL + sl), (uint32_t)(it / NSLOT) & 1u)) return false;
+                        if (t >= a && t < b) {
+                            tc::fence_after_sync();
+                            const uint64_t dk = dk0 + (uint64_t)((sl * TILE) >> 4);
+    #pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint64_t off = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                                tc::umma_bf16(s_tm, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
+                            }
+                            tc::umma_commit(BAR(B_SFULL + q));
+                            tc::umma_commit(BAR(B_EMPTY + sl));
+                        } else {
+                            mbar_arrive(BAR(B_EMPTY + sl));
+                        }
+                        if (t + 1 == s.tb) tc::umma_commit(BAR(B_QFREE));         // the share's last S was issued
+                        ++it;
+                        return true;
+                    };
+                    auto do_v = [&](int t) -> bool {
+                        const int sl = it % NSLOT;
+                        if (!wait_bar(BAR(B_FULL + sl), (uint32_t)(it / NSLOT) & 1u)) return false;
+                        if (t >= a && t < b) {
+                            const uint64_t dv = dv0 + (uint64_t)((sl * TILE) >> 4);
+                            // the share's first P V overwrites O: the previous epilogue must have read it
+                            if (np == np0 && !ofree()) return false;
+    #pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (!wait_bar(BAR((h ? B_PB : B_PA) + q), (uint32_t)np & 1u)) return false;
+                                tc::fence_after_sync();
+    #pragma unroll
+                                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                                    tc::umma_bf16_ts(o_tm, s_tm + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (np > np0 || kk > 0) ? 1u : 0u);
+                            }
+                            tc::umma_commit(BAR(B_EMPTY + sl));
+                            ++np;
+                        } else {
+                            mbar_arrive(BAR(B_EMPTY + sl));
+                        }
+                        ++it;
+                        return true;
+                    };
+                    for (int t = s.ta; ok && t < s.tb; ++t) ok = (t > s.ta || do_k(t)) && do_v(t) && (t + 1 >= s.tb || do_k(t + 1));
+                    if (!ok) break;
+                    // a share without a P V of this sub-tile still waits for the previous epilogue, so
+                    // that its completion never runs two shares ahead of the softmax
+                    if (np == np0 && !(ok = ofree())) break;
+                    tc::umma_commit(BAR(B_ODONE + q));
+                    ++units;
+                }
             }
         }
     } else {
-        const int q = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-        const uint32_t tlane = tmem + ((uint32_t)(quad * 32) << 16);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int q = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_tm = tlane + 128u * q, o_tm = tlane + 256u + 128u * q;
-        const uint32_t prow = sbase + SM_P + (uint32_t)q * TILE + (uint32_t)row * 128u;
-        const uint32_t rx = (uint32_t)(row & 7);
         constexpr float LAZY = 8.f;
         bool ok = true;
-        int k = 0, units = 0, items = 0, piece = 0;
-        for (; ok && next_share(p, at, member, s); ++piece) {
-            const int r = s.rt * ROWS + q * BM + row, i = r % p.line.L;
-            const bool live = r < p.R && i < s.x.x.r.n;
-            // a row that is none takes the row tile's span: it computes what nobody reads, and its
-            // warp keeps to the unmasked path
-            const Span v = live ? span_of(s.x.x.r, i, p.line.N, p.line.w) : s.u;
-            const int a = q ? s.a1 : s.a0, b = q ? s.b1 : s.b0, n = s.tb - s.ta;
+        int k = 0, units = 0, items = 0;
+        for (int piece = 0; ok; ++piece) {
+            int a, b, n, ta, ulo, uhi, vlo, vhi;
+            {
+                Place at = *place(1 + warp);
+                Share s;
+                if (!next_share(p, at, member, s)) break;
+                const int r = s.rt * ROWS + q * BM + row, i = r % p.line.L;
+                // a row that is none takes the row tile's span: it computes what nobody reads, and
+                // its warp keeps to the unmasked path
+                const Span v = r < p.R && i < s.x.x.r.n ? span_of(s.x.x.r, i, p.line.N, p.line.w) : s.u;
+                a = q ? s.a1 : s.a0;
+                b = q ? s.b1 : s.b0;
+                ta = s.ta;
+                n = s.tb - s.ta;
+                ulo = s.u.lo; uhi = s.u.hi;
+                vlo = v.lo; vhi = v.hi;
+            }
+            __syncwarp();
             float m = -INFINITY, lsum = 0.f;
             const int k0 = k;
             for (int t = a; t < b; ++t, ++k) {
                 if (!__all_sync(0xffffffffu, wait_bar(BAR(B_SFULL + q), (uint32_t)k & 1u))) { ok = false; break; }
                 tc::fence_after_sync();
-                uint32_t sa[64], sb[64];
-                tc::tmem_ld64(s_tm, sa);
-                tc::tmem_ld64(s_tm + 64, sb);
-                tc::fence_before_sync();
-                mbar_arrive(BAR(B_SFREE + q));
-                const int p0 = t * BN;
-                if (__any_sync(0xffffffffu, v.lo > p0 || v.hi < p0 + BN)) {
-                    const int lo = v.lo - p0, hi = v.hi - p0;
+                uint32_t sv[4][32];
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) {
-                        if (x < lo || x >= hi) sa[x] = __float_as_uint(-INFINITY);
-                        if (64 + x < lo || 64 + x >= hi) sb[x] = __float_as_uint(-INFINITY);
+                for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_tm + 32u * c, sv[c]);
+                const int p0 = t * BN;
+                if (__any_sync(0xffffffffu, vlo > p0 || vhi < p0 + BN)) {
+                    const int lo = vlo - p0, hi = vhi - p0;
+#pragma unroll
+                    for (int x = 0; x < BN; ++x)
+                        if (x < lo || x >= hi) sv[x >> 5][x & 31] = __float_as_uint(-INFINITY);
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[c]) : "f"(__uint_as_float(sv[c][2 * x])), "f"(__uint_as_float(sv[c][2 * x + 1])));
+                const float mnew = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl2);
+                const bool need = mnew > m + LAZY;
+                const float alpha = (need && m != -INFINITY) ? tc::ex2(m - mnew) : 1.f;
+                if (__any_sync(0xffffffffu, need && m != -INFINITY)) {
+                    // S is there, so the previous P V is done
+#pragma unroll
+                    for (int cc = 0; cc < D / 16; ++cc) {
+                        uint32_t orow[16];
+                        tc::tmem_ld16(o_tm + cc * 16, orow);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) orow[x] = __float_as_uint(__uint_as_float(orow[x]) * alpha);
+                        tc::tmem_st16(o_tm + cc * 16, orow);
                     }
                 }
-                float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    asm("max.f32 %0, %0, %1, %2;" : "+f"(mx0) : "f"(__uint_as_float(sa[2 * x])), "f"(__uint_as_float(sa[2 * x + 1])));
-                    asm("max.f32 %0, %0, %1, %2;" : "+f"(mx1) : "f"(__uint_as_float(sb[2 * x])), "f"(__uint_as_float(sb[2 * x + 1])));
-                }
-                const float mnew = fmaxf(m, fmaxf(mx0, mx1) * p.sl2);
-                const bool need = mnew > m + LAZY;
-                const float muse = need ? mnew : m;
-                const float alpha = (need && m != -INFINITY) ? tc::ex2(m - mnew) : 1.f;
-                const float negm = muse == -INFINITY ? 0.f : -muse;
+                if (need) m = mnew;
+                const float negm = m == -INFINITY ? 0.f : -m;
                 const float2 sl = make_float2(p.sl2, p.sl2), nm = make_float2(negm, negm);
                 float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                uint32_t pk[64];
-                auto half = [&](const uint32_t (&sv)[64], int o) {
+                auto quarter = [&](const uint32_t (&x4)[32], uint32_t dst) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const float2 e = ffma2(make_float2(__uint_as_float(sv[2 * x]), __uint_as_float(sv[2 * x + 1])), sl, nm);
+                    for (int x = 0; x < 16; ++x) {
+                        const float2 e = ffma2(make_float2(__uint_as_float(x4[2 * x]), __uint_as_float(x4[2 * x + 1])), sl, nm);
                         const float2 w = make_float2(tc::ex2(e.x), tc::ex2(e.y));
                         ps[x & 1] = fadd2(ps[x & 1], w);
-                        pk[o + x] = tc::pack_bf16(w.x, w.y);
+                        pk[x] = tc::pack_bf16(w.x, w.y);
                     }
+                    tc::tmem_st16(dst, pk);
                 };
-                auto store = [&](int h) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + (uint32_t)h * HALF + ((((uint32_t)c) ^ rx) << 4)),
-                                     "r"(pk[h * 32 + c * 4]), "r"(pk[h * 32 + c * 4 + 1]), "r"(pk[h * 32 + c * 4 + 2]), "r"(pk[h * 32 + c * 4 + 3])
-                                     : "memory");
-                };
-                half(sa, 0);
-                const bool resc = k > k0 && __any_sync(0xffffffffu, need && m != -INFINITY);
-                if (k >= 1 && !__all_sync(0xffffffffu, wait_bar(BAR(B_PVA + q), (uint32_t)(k - 1) & 1u))) { ok = false; break; }
-                if (!resc) store(0);
-                half(sb, 32);
-                if (k >= 1 && !__all_sync(0xffffffffu, wait_bar(BAR(B_PVDONE + q), (uint32_t)(k - 1) & 1u))) { ok = false; break; }
-                tc::fence_after_sync();
-                if (resc) {
-#pragma unroll
-                    for (int cc = 0; cc < D / 32; ++cc) {
-                        uint32_t orow[32];
-                        tc::tmem_ld32(o_tm + cc * 32, orow);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) orow[x] = __float_as_uint(__uint_as_float(orow[x]) * alpha);
-                        tc::tmem_st32(o_tm + cc * 32, orow);
-                    }
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    store(0);
-                }
-                store(1);
-                lsum = lsum * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
-                m = muse;
-                if (s.u.lo > p0 || s.u.hi < p0 + BN) {
+                if (ulo > p0 || uhi < p0 + BN) {
                     // values outside the row tile's span: zeros (each sub-tile that reads the tile
                     // writes them before its own P V)
-                    const int j = t - s.ta, item = items + (j + 1 < n ? 2 * j + 2 : 2 * j + 1), sl2 = item % NSLOT;
-                    if (!__all_sync(0xffffffffu, wait_bar(BAR(B_FULL + sl2), (uint32_t)(item / NSLOT) & 1u))) { ok = false; break; }
-                    if (p0 + row < s.u.lo || p0 + row >= s.u.hi) {
-                        const uint32_t vrow = sbase + SM_SLOT + (uint32_t)sl2 * TILE + (uint32_t)row * 128u;
+                    const int item = items + 2 * (t - ta) + 1, vs = item % NSLOT;
+                    if (!__all_sync(0xffffffffu, wait_bar(BAR(B_FULL + vs), (uint32_t)(item / NSLOT) & 1u))) { ok = false; break; }
+                    if (p0 + row < ulo || p0 + row >= uhi) {
+                        const uint32_t vrow = sbase + SM_SLOT + (uint32_t)vs * TILE + (uint32_t)row * 128u;
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + (c >> 3) * HALF + (c & 7) * 16), "r"(0) : "memory");
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(BAR(B_PFULL + q));
+                quarter(sv[0], s_tm);
+                quarter(sv[1], s_tm + 16);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                mbar_arrive(BAR(B_PA + q));
+                quarter(sv[2], s_tm + 32);
+                quarter(sv[3], s_tm + 48);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                mbar_arrive(BAR(B_PB + q));
+                lsum = lsum * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
             }
             if (!ok) break;
-            const bool worked = n > 0;
             items += 2 * n;
-            if (worked) {
+            if (n > 0) {
                 if (!__all_sync(0xffffffffu, wait_bar(BAR(B_ODONE + q), (uint32_t)units & 1u))) { ok = false; break; }
                 tc::fence_after_sync();
                 ++units;
             }
             const bool have = k > k0;
+            Place at = *place(1 + warp);
+            Share s;
+            next_share(p, at, member, s);
+            __syncwarp();
+            if (lane == 0) *place(1 + warp) = at;
+            __syncwarp();
+            const int r = s.rt * ROWS + q * BM + row;
+            const bool live = r < p.R && r % p.line.L < s.x.x.r.n;
             const long grow = (long)(s.x.b * p.c.H + s.x.h) * p.R + r;
             if (s.x.whole) {
                 const float inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
@@ -488,7 +512,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                     }
                 }
             }
-            if (worked) {
+            if (n > 0) {
                 tc::fence_before_sync();
                 mbar_arrive(BAR(B_OFREE + q));
             }
