@@ -157,6 +157,7 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
     if (misaligned4(new_lens) || misaligned4(lse) || misaligned4(w_in) || misaligned4(w_out))
         return FAIL("lengths, lse and weights must be 4-byte aligned");
     if (w_in && !w_out) return FAIL("w_in without w_out");
+    if (!isfinite(scale)) return FAIL("scale must be finite (got %g)", (double)scale);
     if (w_out && !isfinite(decay)) return FAIL("decay must be finite (got %g)", (double)decay);
     const size_t nw = (size_t)B * Hkv * max_pages * page * 4;
     if (w_in && w_in != w_out && overlap(w_in, nw, w_out, nw)) return FAIL("w_out overlaps w_in");

@@ -4,28 +4,30 @@
 // GPU (gangs over a line of key tiles, pieces joined by a second kernel) is in paged.cuh; a row
 // tile is 256 packed rows (two sub-tiles of 128) of one key head, so the query heads that share a
 // key head share its tiles too.
-// Roles of a block's 12 warps (one block per SM):
-//   warps 0-3 / 4-7  softmax of sub-tile 0 / 1, one thread per row (its tensor-memory lane)
-//   warp 8           producer: per share Q, then K and V tiles through one ring of five 32 KB slots
+// Roles of a block's 20 warps (one block per SM):
+//   warps 0-7 / 8-15 softmax of sub-tile 0 / 1: two threads per row (its tensor-memory lane), one for
+//                    keys 0-63 of a tile, one for keys 64-127
+//   warp 16          producer: per share Q, then K and V tiles through one ring of five 32 KB slots
 //                    in the order K0, V0, K1, V1, ...; a lane per page of the tile looks the page up
 //                    and copies it by TMA to its rows of the swizzled tile (a page holds whole
 //                    groups of eight rows, so page and tile swizzle alike)
-//   warps 9, 10      issuers of sub-tile 0 / 1
-//   warp 11          completes the warpgroup that gives registers to the softmax warps
+//   warp 17          issuer of the products, the sub-tiles in turn
+//   warps 18, 19     complete the warpgroup that gives registers to the softmax warps
 // Per sub-tile and tile: S = Q K^T into 128 columns of tensor memory; the softmax reads them into
-// registers, and writes P as bf16 over the first 64 of the same columns, in two halves; O += P V
+// registers, and writes P as bf16 over the first 64 of the same columns, each half as soon as it is
+// done; O += P V
 // with P from tensor memory (an operand that costs no shared-memory reads), then S of the next
 // tile, issued behind it in the same order, overwrites P. The completion of S therefore also says
-// that the previous P V is done, and O may be rescaled. One sub-tile's products run while the
-// other's softmax does.
+// that the previous P V is done, and O may be rescaled. One thread issues for both sub-tiles, P V
+// and next S of one and then of the other: with a thread each, their products interleaved and both
+// softmaxes then ran, and waited, at the same time (5700 cycles per tile).
 // Why P is not in shared memory: a 128 x 128 x 16 product from shared memory reads 8 KB for 32
 // cycles of math, twice what shared memory delivers. With P there too, a pair of sub-tiles moves
 // 384 KB per 128 keys (operands, P's stores, the copies in), 3072 cycles at 128 B per cycle;
 // this way it moves 256 KB. The exponentials take 2048 cycles (16 per cycle).
-// The softmax keeps a row's 128 scores in registers: 168 registers a thread (what 384 threads may
-// have) spilled, and with all of the SM's memory given to shared memory a spilled register comes
-// back from L2. The last warpgroup gives its registers to the other two (56 / 224), and the share's
-// bookkeeping is worked out twice instead of being kept across the tiles.
+// The softmax keeps its scores in registers. With a thread per row (128 scores) the two warps per
+// scheduler spent most of a tile waiting for their own results: 2.6 us per tile of 2 x 128 rows; two
+// threads per row (64 scores, the maxima exchanged through shared memory) give four.
 // O is rescaled only when a row's maximum grew by more than 2^8 (numerator and denominator share
 // the stale maximum). P is rounded to bf16 for the tensor cores (half a step, 2^-8 of each weight),
 // the sums are taken in fp32 before that rounding.
@@ -53,9 +55,8 @@ using namespace paged;
 
 constexpr int BM = 128, QT = 2, ROWS = BM * QT;     // rows per sub-tile, sub-tiles, rows per block
 constexpr int BN = 128, D = 128;                    // keys per tile, head dim
-constexpr int THREADS = 384;                        // 8 softmax warps, producer, two issuers, one that only pads
-                                                    // the last warpgroup (registers move between warpgroups)
-constexpr int WARP_TMA = 8, WARP_MMA = 9;
+constexpr int THREADS = 640;
+constexpr int WARP_TMA = 16, WARP_MMA = 17;
 constexpr uint32_t HALF = 128 * 128;                // [128 rows][64 columns] bf16
 constexpr uint32_t TILE = 2 * HALF;
 constexpr int NSLOT = 5;
@@ -68,9 +69,11 @@ enum {
     B_PA = B_SFULL + QT, B_PB = B_PA + QT,          // the halves of P
     B_ODONE = B_PB + QT, B_OFREE = B_ODONE + QT, NBARS = B_OFREE + QT
 };
-constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS;   // the block's start on the line, then each softmax warp's place
-constexpr uint32_t SM_TMEM = SM_PLACE + 9 * 32, SM_ABORT = SM_TMEM + 4, SM_TOTAL = SM_ABORT + 4;
-constexpr size_t SMEM_BYTES = SM_TOTAL + 1024;
+constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS;   // the block's start on the line; the softmax warps' places
+constexpr uint32_t SM_MAX = SM_PLACE + 17 * 32;     // row maxima: [sub-tile][half][row] fp32
+constexpr uint32_t SM_OK = SM_MAX + QT * 2 * BM * 4;    // per softmax warp: no wait expired
+constexpr uint32_t SM_TMEM = SM_OK + 64, SM_ABORT = SM_TMEM + 4;
+constexpr size_t SMEM_BYTES = SM_ABORT + 4;
 static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
 static_assert(sizeof(Place) <= 32, "place");
 
@@ -102,6 +105,17 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+
+// 8 consecutive fp32 columns, load and wait in one statement
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&x)[8])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+        : "r"(taddr)
+        : "memory");
 }
 
 // The bounded wait of sm100_ptx.cuh, inlined: a kernel that moves registers between its warpgroups
@@ -177,8 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ Params p)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];   // the swizzled tiles repeat every 1024 bytes
     const uint32_t sbase = smem_u32(smem);
     auto BAR = [&](int i) { return sbase + SM_BAR + 8u * (uint32_t)i; };
     volatile int *abort_flag = (volatile int *)(smem + SM_ABORT);
@@ -187,26 +200,30 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gang = blockIdx.x / p.line.gs, member = blockIdx.x % p.line.gs;
 
+    if (sbase & 1023u) {                    // not seen: the attribute asks for it
+        if (threadIdx.x == 0) atomicOr(p.c.err, DEVERR_ATTN_WAIT);
+        return;
+    }
     if (threadIdx.x == 0) {
         mbar_init(BAR(B_QFULL), 1);
-        mbar_init(BAR(B_QFREE), 2);
+        mbar_init(BAR(B_QFREE), 1);
         for (int i = 0; i < NSLOT; ++i) {
             mbar_init(BAR(B_FULL + i), 1);
-            mbar_init(BAR(B_EMPTY + i), 2);
+            mbar_init(BAR(B_EMPTY + i), 1);
         }
         for (int q = 0; q < QT; ++q) {
             mbar_init(BAR(B_SFULL + q), 1);
             mbar_init(BAR(B_PA + q), BM);
             mbar_init(BAR(B_PB + q), BM);
             mbar_init(BAR(B_ODONE + q), 1);
-            mbar_init(BAR(B_OFREE + q), BM);
+            mbar_init(BAR(B_OFREE + q), 2 * BM);
         }
         *abort_flag = 0;
         mbar_init_fence();
     }
     if (warp == WARP_TMA) {
         const Place c = place_of<BN>(p.line, gang);
-        if (lane < 9) *place(lane) = c;
+        if (lane < 17) *place(lane) = c;
     }
     if (warp == WARP_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(TMEM_COLS)
@@ -223,7 +240,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     // A share's ring items: K and V of its tiles in turn: K(j) is item 2j, V(j) item 2j + 1.
 
     if (warp >= WARP_TMA) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == WARP_TMA) {
             Place at = *place(0);
             Share s;
@@ -283,88 +300,103 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                 if (units > 0)
                     while (!mbar_try(BAR(B_QFULL), (uint32_t)(units - 1) & 1u) && clock64() - t0 < (1LL << 31)) {}
             }
-        } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
+        } else if (warp == WARP_MMA) {
             if (lane == 0) {
-                const int q = warp - WARP_MMA;
                 constexpr uint32_t IDESC_S = tc::idesc_bf16(BM, BN, false, false), IDESC_O = tc::idesc_bf16(BM, D, false, true);
-                const uint64_t dq = tc::sw128_desc(sbase + SM_Q + q * TILE, 16, 1024);
+                const uint64_t dq0 = tc::sw128_desc(sbase + SM_Q, 16, 1024);
                 const uint64_t dk0 = tc::sw128_desc(sbase + SM_SLOT, 16, 1024);       // K-major (K)
                 const uint64_t dv0 = tc::sw128_desc(sbase + SM_SLOT, HALF, 1024);     // MN-major (V)
-                const uint32_t s_tm = tmem + 128u * q, o_tm = tmem + 256u + 128u * q;
                 Place at = *place(0);
                 Share s;
-                int it = 0, np = 0, units = 0;
+                int it = 0, np[QT] = {0, 0}, units = 0;
                 bool ok = true;
+                auto full = [&](int i) -> bool { return wait_bar(BAR(B_FULL + i % NSLOT), (uint32_t)(i / NSLOT) & 1u); };
                 while (ok && next_share(p, at, member, s)) {
                     if (s.tb <= s.ta) continue;
-                    const int a = q ? s.a1 : s.a0, b = q ? s.b1 : s.b0;
-                    const int np0 = np;
+                    const int first[QT] = {np[0], np[1]};
                     if (!(ok = wait_bar(BAR(B_QFULL), (uint32_t)units & 1u))) break;
-                    tc::fence_after_sync();
-                    auto ofree = [&]() -> bool { return units < 1 || wait_bar(BAR(B_OFREE + q), (uint32_t)(units - 1) & 1u); };
-                    auto do_k = [&](int t) -> bool {
-                        const int sl = it % NSLOT;
-                        if (!wait_bar(BAR(B_FULL + sl), (uint32_t)(it / NSLOT) & 1u)) return false;
-                        if (t >= a && t < b) {
+                    auto ofree = [&](int q) -> bool { return units < 1 || wait_bar(BAR(B_OFREE + q), (uint32_t)(units - 1) & 1u); };
+                    auto needs = [&](int q, int t) -> bool { return q ? t >= s.a1 && t < s.b1 : t >= s.a0 && t < s.b0; };
+                    // S of sub-tile q with the K tile in ring item `item`
+                    auto do_s = [&](int q, int item) {
+                        const uint64_t dk = dk0 + (uint64_t)(((item % NSLOT) * TILE) >> 4), dq = dq0 + (uint64_t)((q * TILE) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                            tc::umma_bf16(tmem + 128u * q, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
+                        }
+                        tc::umma_commit(BAR(B_SFULL + q));
+                    };
+                    // O += P V of sub-tile q with the V tile in ring item `item`
+                    auto do_pv = [&](int q, int item) -> bool {
+                        const uint64_t dv = dv0 + (uint64_t)(((item % NSLOT) * TILE) >> 4);
+                        // the share's first P V overwrites O: the previous epilogue must have read it
+                        if (np[q] == first[q] && !ofree(q)) return false;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!wait_bar(BAR((h ? B_PB : B_PA) + q), (uint32_t)np[q] & 1u)) return false;
                             tc::fence_after_sync();
-                            const uint64_t dk = dk0 + (uint64_t)((sl * TILE) >> 4);
-    #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint64_t off = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                                tc::umma_bf16(s_tm, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
-                            }
-                            tc::umma_commit(BAR(B_SFULL + q));
-                            tc::umma_commit(BAR(B_EMPTY + sl));
-                        } else {
-                            mbar_arrive(BAR(B_EMPTY + sl));
+#pragma unroll
+                            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                                tc::umma_bf16_ts(tmem + 256u + 128u * q, tmem + 128u * q + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O,
+                                                 (np[q] > first[q] || kk > 0) ? 1u : 0u);
                         }
-                        if (t + 1 == s.tb) tc::umma_commit(BAR(B_QFREE));         // the share's last S was issued
-                        ++it;
+                        ++np[q];
                         return true;
                     };
-                    auto do_v = [&](int t) -> bool {
-                        const int sl = it % NSLOT;
-                        if (!wait_bar(BAR(B_FULL + sl), (uint32_t)(it / NSLOT) & 1u)) return false;
-                        if (t >= a && t < b) {
-                            const uint64_t dv = dv0 + (uint64_t)((sl * TILE) >> 4);
-                            // the share's first P V overwrites O: the previous epilogue must have read it
-                            if (np == np0 && !ofree()) return false;
-    #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (!wait_bar(BAR((h ? B_PB : B_PA) + q), (uint32_t)np & 1u)) return false;
-                                tc::fence_after_sync();
-    #pragma unroll
-                                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                                    tc::umma_bf16_ts(o_tm, s_tm + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (np > np0 || kk > 0) ? 1u : 0u);
-                            }
-                            tc::umma_commit(BAR(B_EMPTY + sl));
-                            ++np;
-                        } else {
-                            mbar_arrive(BAR(B_EMPTY + sl));
+                    if (!(ok = full(it))) break;
+                    tc::fence_after_sync();
+                    for (int q = 0; q < QT; ++q)
+                        if (needs(q, s.ta)) do_s(q, it);
+                    tc::umma_commit(BAR(B_EMPTY + it % NSLOT));
+                    ++it;
+                    if (s.ta + 1 == s.tb) tc::umma_commit(BAR(B_QFREE));
+                    // V of tile t is item `it`, K of the next one item it + 1. A sub-tile's P V and next S
+                    // go together, then the other sub-tile's: while one has its products the other has
+                    // the exponential unit, instead of both waiting for both.
+                    for (int t = s.ta; ok && t < s.tb; ++t) {
+                        const bool more = t + 1 < s.tb;
+                        if (!(ok = full(it) && (!more || full(it + 1)))) break;
+                        tc::fence_after_sync();
+                        for (int q = 0; ok && q < QT; ++q) {
+                            if (needs(q, t)) ok = do_pv(q, it);
+                            if (ok && more && needs(q, t + 1)) do_s(q, it + 1);
                         }
+                        if (!ok) break;
+                        tc::umma_commit(BAR(B_EMPTY + it % NSLOT));
                         ++it;
-                        return true;
-                    };
-                    for (int t = s.ta; ok && t < s.tb; ++t) ok = (t > s.ta || do_k(t)) && do_v(t) && (t + 1 >= s.tb || do_k(t + 1));
+                        if (more) {
+                            tc::umma_commit(BAR(B_EMPTY + it % NSLOT));
+                            ++it;
+                            if (t + 2 == s.tb) tc::umma_commit(BAR(B_QFREE));     // the share's last S was issued
+                        }
+                    }
                     if (!ok) break;
-                    // a share without a P V of this sub-tile still waits for the previous epilogue, so
-                    // that its completion never runs two shares ahead of the softmax
-                    if (np == np0 && !(ok = ofree())) break;
-                    tc::umma_commit(BAR(B_ODONE + q));
+                    for (int q = 0; ok && q < QT; ++q) {
+                        // a share without a P V of a sub-tile still waits for its previous epilogue, so that
+                        // its completion never runs two shares ahead of the softmax
+                        if (np[q] == first[q]) ok = ofree(q);
+                        if (ok) tc::umma_commit(BAR(B_ODONE + q));
+                    }
                     ++units;
                 }
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        const int q = warp >> 2, row = (warp & 3) * 32 + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int q = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
         const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t s_tm = tlane + 128u * q, o_tm = tlane + 256u + 128u * q;
+        const uint32_t s_tm = tlane + 128u * q, o_tm = tlane + 256u + 128u * q + 64u * half;
+        volatile float *mx_own = (volatile float *)(smem + SM_MAX) + (q * 2 + half) * BM + row;
+        volatile float *mx_other = (volatile float *)(smem + SM_MAX) + (q * 2 + (half ^ 1)) * BM + row;
+        const int pair_bar = 1 + q * 4 + (warp & 3);        // named barrier of the two warps of these rows
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
         constexpr float LAZY = 8.f;
         bool ok = true;
+        volatile int *ok_own = (volatile int *)(smem + SM_OK) + warp, *ok_other = (volatile int *)(smem + SM_OK) + (warp ^ 4);
         int k = 0, units = 0, items = 0;
-        for (int piece = 0; ok; ++piece) {
-            int a, b, n, ta, ulo, uhi, vlo, vhi;
+        for (int piece = 0;; ++piece) {
+            int a, b, v_item, ulo, uhi, vlo, vhi;
             {
                 Place at = *place(1 + warp);
                 Share s;
@@ -375,8 +407,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                 const Span v = r < p.R && i < s.x.x.r.n ? span_of(s.x.x.r, i, p.line.N, p.line.w) : s.u;
                 a = q ? s.a1 : s.a0;
                 b = q ? s.b1 : s.b0;
-                ta = s.ta;
-                n = s.tb - s.ta;
+                v_item = items - 2 * s.ta + 1;
                 ulo = s.u.lo; uhi = s.u.hi;
                 vlo = v.lo; vhi = v.hi;
             }
@@ -384,132 +415,133 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             float m = -INFINITY, lsum = 0.f;
             const int k0 = k;
             for (int t = a; t < b; ++t, ++k) {
-                if (!__all_sync(0xffffffffu, wait_bar(BAR(B_SFULL + q), (uint32_t)k & 1u))) { ok = false; break; }
+                ok = __all_sync(0xffffffffu, ok && wait_bar(BAR(B_SFULL + q), (uint32_t)k & 1u));
                 tc::fence_after_sync();
-                uint32_t sv[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_tm + 32u * c, sv[c]);
-                const int p0 = t * BN;
-                if (__any_sync(0xffffffffu, vlo > p0 || vhi < p0 + BN)) {
+                uint32_t sv[64];
+                tc::tmem_ld64(s_tm + 64u * half, sv);
+                const int p0 = t * BN + 64 * half;
+                if (__any_sync(0xffffffffu, vlo > p0 || vhi < p0 + 64)) {
                     const int lo = vlo - p0, hi = vhi - p0;
 #pragma unroll
-                    for (int x = 0; x < BN; ++x)
-                        if (x < lo || x >= hi) sv[x >> 5][x & 31] = __float_as_uint(-INFINITY);
+                    for (int x = 0; x < 64; ++x)
+                        if (x < lo || x >= hi) sv[x] = __float_as_uint(-INFINITY);
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < 16; ++x)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[c]) : "f"(__uint_as_float(sv[c][2 * x])), "f"(__uint_as_float(sv[c][2 * x + 1])));
-                const float mnew = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl2);
+                for (int x = 0; x < 32; ++x)
+                    asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[x & 3]) : "f"(__uint_as_float(sv[2 * x])), "f"(__uint_as_float(sv[2 * x + 1])));
+                const float own = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl2;
+                // both warps have read S before either writes P over it; both give up when one did (a
+                // maximum is never NaN)
+                *mx_own = ok ? own : NAN;
+                tc::fence_before_sync();
+                pair_sync();
+                tc::fence_after_sync();
+                const float other = *mx_other;
+                ok = ok && other == other;
+                if (!ok) break;
+                const float mnew = fmaxf(m, fmaxf(own, other));
                 const bool need = mnew > m + LAZY;
                 const float alpha = (need && m != -INFINITY) ? tc::ex2(m - mnew) : 1.f;
                 if (__any_sync(0xffffffffu, need && m != -INFINITY)) {
-                    // S is there, so the previous P V is done
+                    // S is there, so the previous P V is done; each warp rescales half the channels
 #pragma unroll
-                    for (int cc = 0; cc < D / 16; ++cc) {
-                        uint32_t orow[16];
-                        tc::tmem_ld16(o_tm + cc * 16, orow);
+                    for (int cc = 0; cc < 8; ++cc) {
+                        uint32_t orow[8];
+                        tmem_ld8(o_tm + cc * 8, orow);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) orow[x] = __float_as_uint(__uint_as_float(orow[x]) * alpha);
-                        tc::tmem_st16(o_tm + cc * 16, orow);
+                        for (int x = 0; x < 8; ++x) orow[x] = __float_as_uint(__uint_as_float(orow[x]) * alpha);
+                        tc::tmem_st8(o_tm + cc * 8, orow);
                     }
                 }
                 if (need) m = mnew;
                 const float negm = m == -INFINITY ? 0.f : -m;
                 const float2 sl = make_float2(p.sl2, p.sl2), nm = make_float2(negm, negm);
                 float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                auto quarter = [&](const uint32_t (&x4)[32], uint32_t dst) {
-                    uint32_t pk[16];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const float2 e = ffma2(make_float2(__uint_as_float(x4[2 * x]), __uint_as_float(x4[2 * x + 1])), sl, nm);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float2 e = ffma2(make_float2(__uint_as_float(sv[16 * c + 2 * x]), __uint_as_float(sv[16 * c + 2 * x + 1])), sl, nm);
                         const float2 w = make_float2(tc::ex2(e.x), tc::ex2(e.y));
                         ps[x & 1] = fadd2(ps[x & 1], w);
                         pk[x] = tc::pack_bf16(w.x, w.y);
                     }
-                    tc::tmem_st16(dst, pk);
-                };
-                if (ulo > p0 || uhi < p0 + BN) {
-                    // values outside the row tile's span: zeros (each sub-tile that reads the tile
-                    // writes them before its own P V)
-                    const int item = items + 2 * (t - ta) + 1, vs = item % NSLOT;
-                    if (!__all_sync(0xffffffffu, wait_bar(BAR(B_FULL + vs), (uint32_t)(item / NSLOT) & 1u))) { ok = false; break; }
-                    if (p0 + row < ulo || p0 + row >= uhi) {
-                        const uint32_t vrow = sbase + SM_SLOT + (uint32_t)vs * TILE + (uint32_t)row * 128u;
+                    tc::tmem_st8(s_tm + 32u * half + 8u * c, pk);
+                }
+                if (ulo > t * BN || uhi < (t + 1) * BN) {
+                    // values outside the row tile's span: zeros, this half's keys (each sub-tile that
+                    // reads the tile writes them before its own P V)
+                    const int item = v_item + 2 * t, vs = item % NSLOT;
+                    ok = wait_bar(BAR(B_FULL + vs), (uint32_t)(item / NSLOT) & 1u);
+                    const int key = 64 * half + (row & 63);
+                    if (ok && (t * BN + key < ulo || t * BN + key >= uhi)) {
+                        const uint32_t vrow = sbase + SM_SLOT + (uint32_t)vs * TILE + (uint32_t)(row >> 6) * HALF + (uint32_t)key * 128u;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + (c >> 3) * HALF + (c & 7) * 16), "r"(0) : "memory");
+                        for (int c = 0; c < 8; ++c)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + c * 16), "r"(0) : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                quarter(sv[0], s_tm);
-                quarter(sv[1], s_tm + 16);
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
-                mbar_arrive(BAR(B_PA + q));
-                quarter(sv[2], s_tm + 32);
-                quarter(sv[3], s_tm + 48);
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                mbar_arrive(BAR(B_PB + q));
+                mbar_arrive(BAR((half ? B_PB : B_PA) + q));
                 lsum = lsum * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
             }
-            if (!ok) break;
-            items += 2 * n;
-            if (n > 0) {
-                if (!__all_sync(0xffffffffu, wait_bar(BAR(B_ODONE + q), (uint32_t)units & 1u))) { ok = false; break; }
-                tc::fence_after_sync();
-                ++units;
-            }
-            const bool have = k > k0;
             Place at = *place(1 + warp);
             Share s;
             next_share(p, at, member, s);
+            const int n = s.tb - s.ta;
             __syncwarp();
             if (lane == 0) *place(1 + warp) = at;
-            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok && (n == 0 || wait_bar(BAR(B_ODONE + q), (uint32_t)units & 1u)));
+            // the row's sum is the sum of its two threads' (lower half of the keys first)
+            *mx_own = lsum;
+            if (lane == 0) *ok_own = ok;
+            pair_sync();
+            const float l_other = *mx_other;
+            ok = ok && *ok_other;
+            pair_sync();
+            if (!ok) break;
+            tc::fence_after_sync();
+            lsum = half ? l_other + lsum : lsum + l_other;
+            items += 2 * n;
+            if (n > 0) ++units;
+            const bool have = k > k0;
             const int r = s.rt * ROWS + q * BM + row;
             const bool live = r < p.R && r % p.line.L < s.x.x.r.n;
             const long grow = (long)(s.x.b * p.c.H + s.x.h) * p.R + r;
+            const int rr = q * BM + row;
+            const long slot = (long)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
+            float inv = 1.f;
             if (s.x.whole) {
-                const float inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
-                if (p.lse && live) p.lse[grow] = (m + log2f(lsum)) * 0.69314718055994531f;
-                __nv_bfloat16 *orow = p.o + grow * D;
+                inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
+                if (p.lse && live && half == 0) p.lse[grow] = (m + log2f(lsum)) * 0.69314718055994531f;
+            } else if (live && half == 0) {
+                p.ml[slot * ROWS + rr] = make_float2(m, lsum);
+            }
 #pragma unroll
-                for (int cc = 0; cc < D / 32; ++cc) {
-                    uint32_t ov[32];
-                    __syncwarp();
-                    if (have) tc::tmem_ld32(o_tm + cc * 32, ov);
-                    if (live) {
-                        uint32_t w[16];
+            for (int cc = 0; cc < 4; ++cc) {
+                uint32_t ov[16];
+                __syncwarp();
+                if (have) tc::tmem_ld16(o_tm + cc * 16, ov);
+                if (!live) continue;
+                if (s.x.whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + grow * D + 64 * half + cc * 16);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            w[x] = have ? tc::pack_bf16(__uint_as_float(ov[2 * x]) * inv, __uint_as_float(ov[2 * x + 1]) * inv) : 0u;
-                        uint4 *dst = reinterpret_cast<uint4 *>(orow + cc * 32);
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t w[4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                        for (int y = 0; y < 4; ++y)
+                            w[y] = have ? tc::pack_bf16(__uint_as_float(ov[8 * x + 2 * y]) * inv, __uint_as_float(ov[8 * x + 2 * y + 1]) * inv) : 0u;
+                        dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                }
-            } else {
-                const int rr = q * BM + row;
-                const long slot = (long)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
-                if (live) p.ml[slot * ROWS + rr] = make_float2(m, lsum);
-                float4 *dst = reinterpret_cast<float4 *>(p.part) + slot * (D / 4) * ROWS + rr;
-                if (have) {
+                } else if (have) {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part) + (slot * (D / 4) + 16 * half + 4 * cc) * ROWS + rr;
 #pragma unroll
-                    for (int cc = 0; cc < D / 32; ++cc) {
-                        uint32_t ov[32];
-                        __syncwarp();
-                        tc::tmem_ld32(o_tm + cc * 32, ov);
-                        if (live) {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                dst[(cc * 8 + x) * ROWS] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]),
-                                                                       __uint_as_float(ov[4 * x + 2]), __uint_as_float(ov[4 * x + 3]));
-                        }
-                    }
+                    for (int x = 0; x < 4; ++x)
+                        dst[x * ROWS] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]), __uint_as_float(ov[4 * x + 3]));
                 }
             }
             if (n > 0) {

@@ -74,7 +74,7 @@ def test_paged_attn(h):
     cases = [(c, BAD) for c in CACHE if c.get("max_pages") != 1 << 27] + [(dict(max_pages=1 << 27), BAD)]
     cases += [(dict(q=None), BAD), (dict(o=None), BAD), (dict(o=_p(0)), BAD), (dict(q=ODD), BAD), (dict(o=ODD), BAD), (dict(Hq=9), BAD), (dict(Hq=0), BAD),
               (dict(H=0), BAD), (dict(L=-1), BAD), (dict(N=0), BAD), (dict(w=-1), BAD), (dict(w_out=None), BAD), (dict(decay=F(float("nan"))), BAD),
-              (dict(decay=F(float("inf"))), BAD), (dict(w_in=ctypes.c_void_p((1 << 32) * 8 + 16)), BAD), (dict(lse=ctypes.c_void_p(3)), BAD),
+              (dict(decay=F(float("inf"))), BAD), (dict(scale=F(float("inf"))), BAD), (dict(scale=F(float("nan"))), BAD), (dict(w_in=ctypes.c_void_p((1 << 32) * 8 + 16)), BAD), (dict(lse=ctypes.c_void_p(3)), BAD),
               (dict(w_out=ctypes.c_void_p(1 << 34 | 2)), BAD), (dict(new=ctypes.c_void_p(5)), BAD), (dict(ws=None), BAD), (dict(wsb=ws - 1), BAD),
               (dict(ws=ctypes.c_void_p((1 << 40) + 16)), BAD), (dict(dt=3), BAD), (dict(d=64), NO), (dict(d=0), BAD), (dict(Hq=4 * 129), NO),
               (dict(B=0), ok), (dict(L=0, w_in=None, w_out=None), ok)]
