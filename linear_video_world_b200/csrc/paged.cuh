@@ -100,7 +100,7 @@ __device__ __forceinline__ long long tiles_before(const Line &p, int b)
 // A place on the line: the next key tile `t` of key head h of rollout b in pass `pass`.
 struct Place {
     int pass, b, h, t;
-    long long left;                 // tiles left of the range
+    int left;                       // tiles left of the range
 };
 
 // Start of gang g's range (one warp; all lanes get it).
@@ -115,7 +115,7 @@ __device__ __forceinline__ Place place_of(const Line &p, int g)
     c.pass = c.b = c.h = c.t = 0;
     if (g >= ng) return c;
     const long long a = W * g / ng;
-    c.left = W * (g + 1) / ng - a;
+    c.left = (int)(W * (g + 1) / ng - a);
     c.pass = (int)(a / per);
     long long x = a - per * c.pass;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -165,7 +165,7 @@ __device__ __forceinline__ bool next_piece(const Line &p, Place &c, Piece<TK> &o
     o.pass = c.pass;
     o.b = c.b;
     o.h = c.h;
-    const int take = (int)(c.left < (long long)(o.x.T - c.t) ? c.left : (long long)(o.x.T - c.t));
+    const int take = min(c.left, o.x.T - c.t);
     o.ta = o.x.t0 + c.t;
     o.tb = o.ta + take;
     o.whole = take == o.x.T;

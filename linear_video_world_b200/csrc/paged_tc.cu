@@ -4,30 +4,24 @@
 // GPU (gangs over a line of key tiles, pieces joined by a second kernel) is in paged.cuh; a row
 // tile is 256 packed rows (two sub-tiles of 128) of one key head, so the query heads that share a
 // key head share its tiles too.
-// Roles of a block's 20 warps (one block per SM):
-//   warps 0-7 / 8-15 softmax of sub-tile 0 / 1: two threads per row (its tensor-memory lane), one for
-//                    keys 0-63 of a tile, one for keys 64-127
-//   warp 16          producer: per share Q, then K and V tiles through one ring of five 32 KB slots
-//                    in the order K0, V0, K1, V1, ...; a lane per page of the tile looks the page up
-//                    and copies it by TMA to its rows of the swizzled tile (a page holds whole
-//                    groups of eight rows, so page and tile swizzle alike)
-//   warp 17          issuer of the products, the sub-tiles in turn
-//   warps 18, 19     complete the warpgroup that gives registers to the softmax warps
-// Per sub-tile and tile: S = Q K^T into 128 columns of tensor memory; the softmax reads them into
-// registers, and writes P as bf16 over the first 64 of the same columns, each half as soon as it is
-// done; O += P V
-// with P from tensor memory (an operand that costs no shared-memory reads), then S of the next
-// tile, issued behind it in the same order, overwrites P. The completion of S therefore also says
-// that the previous P V is done, and O may be rescaled. One thread issues for both sub-tiles, P V
-// and next S of one and then of the other: with a thread each, their products interleaved and both
-// softmaxes then ran, and waited, at the same time (5700 cycles per tile).
-// Why P is not in shared memory: a 128 x 128 x 16 product from shared memory reads 8 KB for 32
-// cycles of math, twice what shared memory delivers. With P there too, a pair of sub-tiles moves
-// 384 KB per 128 keys (operands, P's stores, the copies in), 3072 cycles at 128 B per cycle;
-// this way it moves 256 KB. The exponentials take 2048 cycles (16 per cycle).
-// The softmax keeps its scores in registers. With a thread per row (128 scores) the two warps per
-// scheduler spent most of a tile waiting for their own results: 2.6 us per tile of 2 x 128 rows; two
-// threads per row (64 scores, the maxima exchanged through shared memory) give four.
+// Roles of a block's 12 warps (one block per SM):
+//   warps 0-3 / 4-7  softmax of sub-tile 0 / 1, one thread per row (its tensor-memory lane)
+//   warp 8           producer: per share Q, then K and V tiles through one ring of three 32 KB slots
+//                    in the order K0, K1, V0, K2, V1, ...; a lane per page of the tile looks the
+//                    page up and copies it by TMA to its rows of the swizzled tile (a page holds
+//                    whole groups of eight rows, so page and tile swizzle alike)
+//   warp 9           issuer of the products, the sub-tiles in turn
+//   warps 10, 11     complete the warpgroup that gives registers to the softmax warps
+// S = Q K^T goes to tensor memory, the softmax reads a row's 128 scores into registers and frees it
+// at once, so S of the next tile is done while P of this one is formed; P goes to shared memory,
+// stored in two halves, each as soon as the previous P V has read that half.
+// What bounds it: per tile of 2 x 128 rows the products take 2051 cycles (64 per 128 x 128 x 16,
+// measured, from shared or tensor memory alike; a product of 64 keys takes 62, so tiles are not
+// halved), the exponentials 2048 (16 a cycle). So neither may wait for the other.
+// The softmax has to stay in registers: 168 a thread (what 384 threads may have) spilled, and with
+// all of the SM's memory given to shared memory a spilled register comes back from L2. The last
+// warpgroup gives its registers to the other two (96 / 200), and the share's bookkeeping is worked
+// out twice instead of being kept across the tiles.
 // O is rescaled only when a row's maximum grew by more than 2^8 (numerator and denominator share
 // the stale maximum). P is rounded to bf16 for the tensor cores (half a step, 2^-8 of each weight),
 // the sums are taken in fp32 before that rounding.
@@ -55,24 +49,23 @@ using namespace paged;
 
 constexpr int BM = 128, QT = 2, ROWS = BM * QT;     // rows per sub-tile, sub-tiles, rows per block
 constexpr int BN = 128, D = 128;                    // keys per tile, head dim
-constexpr int THREADS = 640;
-constexpr int WARP_TMA = 16, WARP_MMA = 17;
+constexpr int THREADS = 384;
+constexpr int WARP_TMA = 8, WARP_MMA = 9;
 constexpr uint32_t HALF = 128 * 128;                // [128 rows][64 columns] bf16
 constexpr uint32_t TILE = 2 * HALF;
-constexpr int NSLOT = 5;
-constexpr uint32_t SM_Q = 0, SM_SLOT = QT * TILE, SM_BAR = SM_SLOT + NSLOT * TILE;
-constexpr uint32_t TMEM_COLS = 512;                 // S (and P over it) of sub-tile q at 128 q, O at 256 + 128 q
+constexpr int NSLOT = 3;
+constexpr uint32_t SM_Q = 0, SM_SLOT = QT * TILE, SM_P = SM_SLOT + NSLOT * TILE, SM_BAR = SM_P + QT * TILE;
+constexpr uint32_t TMEM_COLS = 512;                 // S of sub-tile q at 128 q, O at 256 + 128 q
 enum {
     B_QFULL, B_QFREE,
     B_FULL, B_EMPTY = B_FULL + NSLOT,               // per slot
     B_SFULL = B_EMPTY + NSLOT,                      // per sub-tile from here
-    B_PA = B_SFULL + QT, B_PB = B_PA + QT,          // the halves of P
-    B_ODONE = B_PB + QT, B_OFREE = B_ODONE + QT, NBARS = B_OFREE + QT
+    B_SFREE = B_SFULL + QT, B_PFULL = B_SFREE + QT,
+    B_PVA = B_PFULL + QT, B_PVDONE = B_PVA + QT,    // P V: its first half, all of it
+    B_ODONE = B_PVDONE + QT, B_OFREE = B_ODONE + QT, NBARS = B_OFREE + QT
 };
 constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS;   // the block's start on the line; the softmax warps' places
-constexpr uint32_t SM_MAX = SM_PLACE + 17 * 32;     // row maxima: [sub-tile][half][row] fp32
-constexpr uint32_t SM_OK = SM_MAX + QT * 2 * BM * 4;    // per softmax warp: no wait expired
-constexpr uint32_t SM_TMEM = SM_OK + 64, SM_ABORT = SM_TMEM + 4;
+constexpr uint32_t SM_TMEM = SM_PLACE + 9 * 32, SM_ABORT = SM_TMEM + 4;
 constexpr size_t SMEM_BYTES = SM_ABORT + 4;
 static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
 static_assert(sizeof(Place) <= 32, "place");
@@ -107,14 +100,23 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
     return d;
 }
 
-// 8 consecutive fp32 columns, load and wait in one statement
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&x)[8])
+// 128 consecutive fp32 columns: both loads in flight before the wait
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&x)[128])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
-        : "r"(taddr)
+        : TC_REGS32(x), TC_REGS32((x + 32)), TC_REGS32((x + 64)), TC_REGS32((x + 96))
+        : "r"(taddr), "r"(taddr + 64u)
         : "memory");
 }
 
@@ -213,17 +215,19 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         }
         for (int q = 0; q < QT; ++q) {
             mbar_init(BAR(B_SFULL + q), 1);
-            mbar_init(BAR(B_PA + q), BM);
-            mbar_init(BAR(B_PB + q), BM);
+            mbar_init(BAR(B_SFREE + q), BM);
+            mbar_init(BAR(B_PFULL + q), BM);
+            mbar_init(BAR(B_PVA + q), 1);
+            mbar_init(BAR(B_PVDONE + q), 1);
             mbar_init(BAR(B_ODONE + q), 1);
-            mbar_init(BAR(B_OFREE + q), 2 * BM);
+            mbar_init(BAR(B_OFREE + q), BM);
         }
         *abort_flag = 0;
         mbar_init_fence();
     }
     if (warp == WARP_TMA) {
         const Place c = place_of<BN>(p.line, gang);
-        if (lane < 17) *place(lane) = c;
+        if (lane < 9) *place(lane) = c;
     }
     if (warp == WARP_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(TMEM_COLS)
@@ -237,10 +241,11 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     auto wait_bar = [&](uint32_t bar, uint32_t parity) -> bool {
         return wait_inline(bar, parity, abort_flag, p.c.err);
     };
-    // A share's ring items: K and V of its tiles in turn: K(j) is item 2j, V(j) item 2j + 1.
+    // A share's ring items: K of its first tile, then K of tile j + 1 and V of tile j in turn. With n
+    // tiles, K(j) is item 2j - 1 (j >= 1), V(j) item 2j + 2, the last V item 2n - 1.
 
     if (warp >= WARP_TMA) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == WARP_TMA) {
             Place at = *place(0);
             Share s;
@@ -286,10 +291,14 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                             tma_load_2d(sbase + SM_Q + q * TILE + x * HALF, &tq, 64 * x, row + q * BM, BAR(B_QFULL));
                 }
                 ++units;
+                ok = load(&tk, pg);
                 for (int t = s.ta; ok && t < s.tb; ++t) {
-                    const int next = t + 1 < s.tb ? page_at(t + 1) : -1;      // looked up ahead of the waits
-                    ok = load(&tk, pg) && load(&tv, pg);
-                    pg = next;
+                    const int v_pg = pg;                          // K and V share pages
+                    if (t + 1 < s.tb) {
+                        pg = page_at(t + 1);
+                        if (!(ok = load(&tk, pg))) break;
+                    }
+                    ok = load(&tv, v_pg);
                 }
             }
             if (lane == 0 && *abort_flag) {
@@ -306,71 +315,76 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                 const uint64_t dq0 = tc::sw128_desc(sbase + SM_Q, 16, 1024);
                 const uint64_t dk0 = tc::sw128_desc(sbase + SM_SLOT, 16, 1024);       // K-major (K)
                 const uint64_t dv0 = tc::sw128_desc(sbase + SM_SLOT, HALF, 1024);     // MN-major (V)
+                const uint64_t dp0 = tc::sw128_desc(sbase + SM_P, 16, 1024);
                 Place at = *place(0);
                 Share s;
-                int it = 0, np[QT] = {0, 0}, units = 0;
+                int slot = 0, ns[QT] = {0, 0}, np[QT] = {0, 0}, units = 0;
+                uint32_t lap = 0;                                     // parity of the ring's lap
                 bool ok = true;
-                auto full = [&](int i) -> bool { return wait_bar(BAR(B_FULL + i % NSLOT), (uint32_t)(i / NSLOT) & 1u); };
+                // the next ring item is there; and behind it
+                auto item = [&]() -> bool { return wait_bar(BAR(B_FULL + slot), lap); };
+                auto item_done = [&] {
+                    tc::umma_commit(BAR(B_EMPTY + slot));
+                    if (++slot == NSLOT) {
+                        slot = 0;
+                        lap ^= 1u;
+                    }
+                };
                 while (ok && next_share(p, at, member, s)) {
                     if (s.tb <= s.ta) continue;
                     const int first[QT] = {np[0], np[1]};
                     if (!(ok = wait_bar(BAR(B_QFULL), (uint32_t)units & 1u))) break;
                     auto ofree = [&](int q) -> bool { return units < 1 || wait_bar(BAR(B_OFREE + q), (uint32_t)(units - 1) & 1u); };
                     auto needs = [&](int q, int t) -> bool { return q ? t >= s.a1 && t < s.b1 : t >= s.a0 && t < s.b0; };
-                    // S of sub-tile q with the K tile in ring item `item`
-                    auto do_s = [&](int q, int item) {
-                        const uint64_t dk = dk0 + (uint64_t)(((item % NSLOT) * TILE) >> 4), dq = dq0 + (uint64_t)((q * TILE) >> 4);
+                    // S of tile t, once the softmax has read the previous S
+                    auto do_s = [&](int t) -> bool {
+                        if (!item()) return false;
+                        const uint64_t dk = dk0 + (uint64_t)((slot * TILE) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                            tc::umma_bf16(tmem + 128u * q, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
-                        }
-                        tc::umma_commit(BAR(B_SFULL + q));
-                    };
-                    // O += P V of sub-tile q with the V tile in ring item `item`
-                    auto do_pv = [&](int q, int item) -> bool {
-                        const uint64_t dv = dv0 + (uint64_t)(((item % NSLOT) * TILE) >> 4);
-                        // the share's first P V overwrites O: the previous epilogue must have read it
-                        if (np[q] == first[q] && !ofree(q)) return false;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!wait_bar(BAR((h ? B_PB : B_PA) + q), (uint32_t)np[q] & 1u)) return false;
+                        for (int q = 0; q < QT; ++q) {
+                            if (!needs(q, t)) continue;
+                            if (ns[q] > 0 && !wait_bar(BAR(B_SFREE + q), (uint32_t)(ns[q] - 1) & 1u)) return false;
                             tc::fence_after_sync();
+                            const uint64_t dq = dq0 + (uint64_t)((q * TILE) >> 4);
 #pragma unroll
-                            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                                tc::umma_bf16_ts(tmem + 256u + 128u * q, tmem + 128u * q + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O,
-                                                 (np[q] > first[q] || kk > 0) ? 1u : 0u);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint64_t off = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                                tc::umma_bf16(tmem + 128u * q, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
+                            }
+                            tc::umma_commit(BAR(B_SFULL + q));
+                            ++ns[q];
                         }
-                        ++np[q];
+                        item_done();
+                        if (t + 1 == s.tb) tc::umma_commit(BAR(B_QFREE));             // the share's last S was issued
                         return true;
                     };
-                    if (!(ok = full(it))) break;
-                    tc::fence_after_sync();
-                    for (int q = 0; q < QT; ++q)
-                        if (needs(q, s.ta)) do_s(q, it);
-                    tc::umma_commit(BAR(B_EMPTY + it % NSLOT));
-                    ++it;
-                    if (s.ta + 1 == s.tb) tc::umma_commit(BAR(B_QFREE));
-                    // V of tile t is item `it`, K of the next one item it + 1. A sub-tile's P V and next S
-                    // go together, then the other sub-tile's: while one has its products the other has
-                    // the exponential unit, instead of both waiting for both.
-                    for (int t = s.ta; ok && t < s.tb; ++t) {
-                        const bool more = t + 1 < s.tb;
-                        if (!(ok = full(it) && (!more || full(it + 1)))) break;
-                        tc::fence_after_sync();
-                        for (int q = 0; ok && q < QT; ++q) {
-                            if (needs(q, t)) ok = do_pv(q, it);
-                            if (ok && more && needs(q, t + 1)) do_s(q, it + 1);
+                    // O += P V of tile t, committed in two halves
+                    auto do_pv = [&](int t) -> bool {
+                        if (!item()) return false;
+                        const uint64_t dv = dv0 + (uint64_t)((slot * TILE) >> 4);
+#pragma unroll
+                        for (int q = 0; q < QT; ++q) {
+                            if (!needs(q, t)) continue;
+                            // the share's first P V overwrites O: the previous epilogue must have read it
+                            if (np[q] == first[q] && !ofree(q)) return false;
+                            if (!wait_bar(BAR(B_PFULL + q), (uint32_t)np[q] & 1u)) return false;
+                            tc::fence_after_sync();
+                            const uint64_t dp = dp0 + (uint64_t)((q * TILE) >> 4);
+                            const uint32_t acc = np[q] > first[q] ? 1u : 0u;
+#pragma unroll
+                            for (int kk = 0; kk < BN / 16; ++kk) {
+                                tc::umma_bf16(tmem + 256u + 128u * q, dp + ((uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4),
+                                              dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, kk > 0 ? 1u : acc);
+                                if (kk == BN / 32 - 1) tc::umma_commit(BAR(B_PVA + q));
+                            }
+                            tc::umma_commit(BAR(B_PVDONE + q));
+                            ++np[q];
                         }
-                        if (!ok) break;
-                        tc::umma_commit(BAR(B_EMPTY + it % NSLOT));
-                        ++it;
-                        if (more) {
-                            tc::umma_commit(BAR(B_EMPTY + it % NSLOT));
-                            ++it;
-                            if (t + 2 == s.tb) tc::umma_commit(BAR(B_QFREE));     // the share's last S was issued
-                        }
-                    }
+                        item_done();
+                        return true;
+                    };
+                    ok = do_s(s.ta);
+                    for (int t = s.ta; ok && t < s.tb; ++t) ok = (t + 1 >= s.tb || do_s(t + 1)) && do_pv(t);
                     if (!ok) break;
                     for (int q = 0; ok && q < QT; ++q) {
                         // a share without a P V of a sub-tile still waits for its previous epilogue, so that
@@ -383,20 +397,17 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        const int q = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        const int q = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t s_tm = tlane + 128u * q, o_tm = tlane + 256u + 128u * q + 64u * half;
-        volatile float *mx_own = (volatile float *)(smem + SM_MAX) + (q * 2 + half) * BM + row;
-        volatile float *mx_other = (volatile float *)(smem + SM_MAX) + (q * 2 + (half ^ 1)) * BM + row;
-        const int pair_bar = 1 + q * 4 + (warp & 3);        // named barrier of the two warps of these rows
-        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
+        const uint32_t s_tm = tlane + 128u * q, o_tm = tlane + 256u + 128u * q;
+        const uint32_t prow = sbase + SM_P + (uint32_t)q * TILE + (uint32_t)row * 128u;
+        const uint32_t rx = (uint32_t)(row & 7);
         constexpr float LAZY = 8.f;
         bool ok = true;
-        volatile int *ok_own = (volatile int *)(smem + SM_OK) + warp, *ok_other = (volatile int *)(smem + SM_OK) + (warp ^ 4);
         int k = 0, units = 0, items = 0;
         for (int piece = 0;; ++piece) {
-            int a, b, v_item, ulo, uhi, vlo, vhi;
+            int a, b, ta, tb, ulo, uhi, vlo, vhi;
             {
                 Place at = *place(1 + warp);
                 Share s;
@@ -407,7 +418,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                 const Span v = r < p.R && i < s.x.x.r.n ? span_of(s.x.x.r, i, p.line.N, p.line.w) : s.u;
                 a = q ? s.a1 : s.a0;
                 b = q ? s.b1 : s.b0;
-                v_item = items - 2 * s.ta + 1;
+                ta = s.ta;
+                tb = s.tb;
                 ulo = s.u.lo; uhi = s.u.hi;
                 vlo = v.lo; vhi = v.hi;
             }
@@ -415,99 +427,98 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             float m = -INFINITY, lsum = 0.f;
             const int k0 = k;
             for (int t = a; t < b; ++t, ++k) {
-                ok = __all_sync(0xffffffffu, ok && wait_bar(BAR(B_SFULL + q), (uint32_t)k & 1u));
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(BAR(B_SFULL + q), (uint32_t)k & 1u)))) break;
                 tc::fence_after_sync();
-                uint32_t sv[64];
-                tc::tmem_ld64(s_tm + 64u * half, sv);
-                const int p0 = t * BN + 64 * half;
-                if (__any_sync(0xffffffffu, vlo > p0 || vhi < p0 + 64)) {
+                uint32_t sv[128];
+                tmem_ld128(s_tm, sv);
+                tc::fence_before_sync();
+                mbar_arrive(BAR(B_SFREE + q));
+                const int p0 = t * BN;
+                if (__any_sync(0xffffffffu, vlo > p0 || vhi < p0 + BN)) {
                     const int lo = vlo - p0, hi = vhi - p0;
 #pragma unroll
-                    for (int x = 0; x < 64; ++x)
+                    for (int x = 0; x < BN; ++x)
                         if (x < lo || x >= hi) sv[x] = __float_as_uint(-INFINITY);
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
+                for (int x = 0; x < BN / 2; ++x)
                     asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[x & 3]) : "f"(__uint_as_float(sv[2 * x])), "f"(__uint_as_float(sv[2 * x + 1])));
-                const float own = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl2;
-                // both warps have read S before either writes P over it; both give up when one did (a
-                // maximum is never NaN)
-                *mx_own = ok ? own : NAN;
-                tc::fence_before_sync();
-                pair_sync();
-                tc::fence_after_sync();
-                const float other = *mx_other;
-                ok = ok && other == other;
-                if (!ok) break;
-                const float mnew = fmaxf(m, fmaxf(own, other));
+                const float mnew = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl2);
                 const bool need = mnew > m + LAZY;
                 const float alpha = (need && m != -INFINITY) ? tc::ex2(m - mnew) : 1.f;
-                if (__any_sync(0xffffffffu, need && m != -INFINITY)) {
-                    // S is there, so the previous P V is done; each warp rescales half the channels
-#pragma unroll
-                    for (int cc = 0; cc < 8; ++cc) {
-                        uint32_t orow[8];
-                        tmem_ld8(o_tm + cc * 8, orow);
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) orow[x] = __float_as_uint(__uint_as_float(orow[x]) * alpha);
-                        tc::tmem_st8(o_tm + cc * 8, orow);
-                    }
-                }
+                const bool resc = __any_sync(0xffffffffu, need && m != -INFINITY);
                 if (need) m = mnew;
                 const float negm = m == -INFINITY ? 0.f : -m;
                 const float2 sl = make_float2(p.sl2, p.sl2), nm = make_float2(negm, negm);
                 float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[32];
+                // P of 64 keys into registers; stored when the previous P V is done with that half
+                auto half = [&](int h) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[8];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const float2 e = ffma2(make_float2(__uint_as_float(sv[16 * c + 2 * x]), __uint_as_float(sv[16 * c + 2 * x + 1])), sl, nm);
+                    for (int x = 0; x < 32; ++x) {
+                        const float2 e = ffma2(make_float2(__uint_as_float(sv[64 * h + 2 * x]), __uint_as_float(sv[64 * h + 2 * x + 1])), sl, nm);
                         const float2 w = make_float2(tc::ex2(e.x), tc::ex2(e.y));
                         ps[x & 1] = fadd2(ps[x & 1], w);
                         pk[x] = tc::pack_bf16(w.x, w.y);
                     }
-                    tc::tmem_st8(s_tm + 32u * half + 8u * c, pk);
-                }
-                if (ulo > t * BN || uhi < (t + 1) * BN) {
-                    // values outside the row tile's span: zeros, this half's keys (each sub-tile that
-                    // reads the tile writes them before its own P V)
-                    const int item = v_item + 2 * t, vs = item % NSLOT;
-                    ok = wait_bar(BAR(B_FULL + vs), (uint32_t)(item / NSLOT) & 1u);
-                    const int key = 64 * half + (row & 63);
-                    if (ok && (t * BN + key < ulo || t * BN + key >= uhi)) {
-                        const uint32_t vrow = sbase + SM_SLOT + (uint32_t)vs * TILE + (uint32_t)(row >> 6) * HALF + (uint32_t)key * 128u;
+                };
+                auto store = [&](int h) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + c * 16), "r"(0) : "memory");
+                    for (int c = 0; c < 8; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + (uint32_t)h * HALF + ((((uint32_t)c) ^ rx) << 4)),
+                                     "r"(pk[c * 4]), "r"(pk[c * 4 + 1]), "r"(pk[c * 4 + 2]), "r"(pk[c * 4 + 3])
+                                     : "memory");
+                };
+                half(0);
+                if (k >= 1 && !(ok = __all_sync(0xffffffffu, wait_bar(BAR(B_PVA + q), (uint32_t)(k - 1) & 1u)))) break;
+                store(0);
+                half(1);
+                if (k >= 1 && !(ok = __all_sync(0xffffffffu, wait_bar(BAR(B_PVDONE + q), (uint32_t)(k - 1) & 1u)))) break;
+                store(1);
+                if (resc) {
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t orow[32];
+                        tc::tmem_ld32(o_tm + cc * 32, orow);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) orow[x] = __float_as_uint(__uint_as_float(orow[x]) * alpha);
+                        tc::tmem_st32(o_tm + cc * 32, orow);
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                mbar_arrive(BAR((half ? B_PB : B_PA) + q));
+                if (ulo > p0 || uhi < p0 + BN) {
+                    // values outside the row tile's span: zeros (each sub-tile that reads the tile
+                    // writes them before its own P V)
+                    const int item = items + (t + 1 < tb ? 2 * (t - ta) + 2 : 2 * (t - ta) + 1), vs = item % NSLOT;
+                    if (!(ok = __all_sync(0xffffffffu, wait_bar(BAR(B_FULL + vs), (uint32_t)(item / NSLOT) & 1u)))) break;
+                    if (p0 + row < ulo || p0 + row >= uhi) {
+                        const uint32_t vrow = sbase + SM_SLOT + (uint32_t)vs * TILE + (uint32_t)row * 128u;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + (c >> 3) * HALF + (c & 7) * 16), "r"(0) : "memory");
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(BAR(B_PFULL + q));
                 lsum = lsum * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
             }
+            if (!ok) break;
             Place at = *place(1 + warp);
             Share s;
             next_share(p, at, member, s);
             const int n = s.tb - s.ta;
             __syncwarp();
             if (lane == 0) *place(1 + warp) = at;
-            ok = __all_sync(0xffffffffu, ok && (n == 0 || wait_bar(BAR(B_ODONE + q), (uint32_t)units & 1u)));
-            // the row's sum is the sum of its two threads' (lower half of the keys first)
-            *mx_own = lsum;
-            if (lane == 0) *ok_own = ok;
-            pair_sync();
-            const float l_other = *mx_other;
-            ok = ok && *ok_other;
-            pair_sync();
-            if (!ok) break;
-            tc::fence_after_sync();
-            lsum = half ? l_other + lsum : lsum + l_other;
+            __syncwarp();
+            if (n > 0) {
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(BAR(B_ODONE + q), (uint32_t)units & 1u)))) break;
+                tc::fence_after_sync();
+                ++units;
+            }
             items += 2 * n;
-            if (n > 0) ++units;
             const bool have = k > k0;
             const int r = s.rt * ROWS + q * BM + row;
             const bool live = r < p.R && r % p.line.L < s.x.x.r.n;
@@ -517,20 +528,20 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             float inv = 1.f;
             if (s.x.whole) {
                 inv = lsum > 0.f ? 1.f / lsum : lsum == lsum ? 0.f : lsum;
-                if (p.lse && live && half == 0) p.lse[grow] = (m + log2f(lsum)) * 0.69314718055994531f;
-            } else if (live && half == 0) {
+                if (p.lse && live) p.lse[grow] = (m + log2f(lsum)) * 0.69314718055994531f;
+            } else if (live) {
                 p.ml[slot * ROWS + rr] = make_float2(m, lsum);
             }
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-                uint32_t ov[16];
+            for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t ov[32];
                 __syncwarp();
-                if (have) tc::tmem_ld16(o_tm + cc * 16, ov);
+                if (have) tc::tmem_ld32(o_tm + cc * 32, ov);
                 if (!live) continue;
                 if (s.x.whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + grow * D + 64 * half + cc * 16);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + grow * D + cc * 32);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    for (int x = 0; x < 4; ++x) {
                         uint32_t w[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
@@ -538,9 +549,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                         dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else if (have) {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part) + (slot * (D / 4) + 16 * half + 4 * cc) * ROWS + rr;
+                    float4 *dst = reinterpret_cast<float4 *>(p.part) + (slot * (D / 4) + 8 * cc) * ROWS + rr;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < 8; ++x)
                         dst[x * ROWS] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]), __uint_as_float(ov[4 * x + 3]));
                 }
             }
