@@ -10,8 +10,9 @@
 //                    in the order K0, K1, V0, K2, V1, ...; a lane per page of the tile looks the
 //                    page up and copies it by TMA to its rows of the swizzled tile (a page holds
 //                    whole groups of eight rows, so page and tile swizzle alike)
-//   warp 9           issuer of the products, the sub-tiles in turn
-//   warps 10, 11     complete the warpgroup that gives registers to the softmax warps
+//   warps 9, 10      issuers of the products of sub-tile 0 / 1 (one thread for both left the tensor
+//                    cores idle between its groups of products: 1.09 PFLOP/s in place of 1.17)
+//   warp 11          completes the warpgroup that gives registers to the softmax warps
 // S = Q K^T goes to tensor memory, the softmax reads a row's 128 scores into registers and frees it
 // at once, so S of the next tile is done while P of this one is formed; P goes to shared memory,
 // stored in two halves, each as soon as the previous P V has read that half.
@@ -208,10 +209,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     }
     if (threadIdx.x == 0) {
         mbar_init(BAR(B_QFULL), 1);
-        mbar_init(BAR(B_QFREE), 1);
+        mbar_init(BAR(B_QFREE), 2);
         for (int i = 0; i < NSLOT; ++i) {
             mbar_init(BAR(B_FULL + i), 1);
-            mbar_init(BAR(B_EMPTY + i), 1);
+            mbar_init(BAR(B_EMPTY + i), 2);
         }
         for (int q = 0; q < QT; ++q) {
             mbar_init(BAR(B_SFULL + q), 1);
@@ -309,89 +310,97 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                 if (units > 0)
                     while (!mbar_try(BAR(B_QFULL), (uint32_t)(units - 1) & 1u) && clock64() - t0 < (1LL << 31)) {}
             }
-        } else if (warp == WARP_MMA) {
+        } else if (warp < WARP_MMA + QT) {
             if (lane == 0) {
+                const int q = warp - WARP_MMA;
                 constexpr uint32_t IDESC_S = tc::idesc_bf16(BM, BN, false, false), IDESC_O = tc::idesc_bf16(BM, D, false, true);
-                const uint64_t dq0 = tc::sw128_desc(sbase + SM_Q, 16, 1024);
+                const uint64_t dq = tc::sw128_desc(sbase + SM_Q + q * TILE, 16, 1024);
                 const uint64_t dk0 = tc::sw128_desc(sbase + SM_SLOT, 16, 1024);       // K-major (K)
                 const uint64_t dv0 = tc::sw128_desc(sbase + SM_SLOT, HALF, 1024);     // MN-major (V)
-                const uint64_t dp0 = tc::sw128_desc(sbase + SM_P, 16, 1024);
+                const uint64_t dp = tc::sw128_desc(sbase + SM_P + q * TILE, 16, 1024);
+                const uint32_t s_tm = tmem + 128u * q, o_tm = tmem + 256u + 128u * q;
+                const uint32_t sfull = BAR(B_SFULL + q), sfree = BAR(B_SFREE + q), pfull = BAR(B_PFULL + q), pva = BAR(B_PVA + q),
+                               pvdone = BAR(B_PVDONE + q), ofree = BAR(B_OFREE + q);
                 Place at = *place(0);
-                Share s;
-                int slot = 0, ns[QT] = {0, 0}, np[QT] = {0, 0}, units = 0;
-                uint32_t lap = 0;                                     // parity of the ring's lap
+                uint32_t slot = 0, lap = 0;                           // the next ring item, the parity of its lap
+                uint32_t s_par = 0, p_par = 0;                        // parities of the next S, the next P
+                bool any_s = false;                                   // an S was issued before
+                int units = 0;
                 bool ok = true;
-                // the next ring item is there; and behind it
-                auto item = [&]() -> bool { return wait_bar(BAR(B_FULL + slot), lap); };
-                auto item_done = [&] {
-                    tc::umma_commit(BAR(B_EMPTY + slot));
+                auto item = [&]() -> bool { return wait_bar(BAR(B_FULL) + 8u * slot, lap); };
+                auto next_item = [&] {
                     if (++slot == NSLOT) {
                         slot = 0;
                         lap ^= 1u;
                     }
                 };
-                while (ok && next_share(p, at, member, s)) {
-                    if (s.tb <= s.ta) continue;
-                    const int first[QT] = {np[0], np[1]};
+                while (ok) {
+                    int a, b, ta, tb;
+                    {
+                        Share s;
+                        if (!next_share(p, at, member, s)) break;
+                        a = q ? s.a1 : s.a0;
+                        b = q ? s.b1 : s.b0;
+                        ta = s.ta;
+                        tb = s.tb;
+                    }
+                    if (tb <= ta) continue;
                     if (!(ok = wait_bar(BAR(B_QFULL), (uint32_t)units & 1u))) break;
-                    auto ofree = [&](int q) -> bool { return units < 1 || wait_bar(BAR(B_OFREE + q), (uint32_t)(units - 1) & 1u); };
-                    auto needs = [&](int q, int t) -> bool { return q ? t >= s.a1 && t < s.b1 : t >= s.a0 && t < s.b0; };
                     // S of tile t, once the softmax has read the previous S
                     auto do_s = [&](int t) -> bool {
                         if (!item()) return false;
-                        const uint64_t dk = dk0 + (uint64_t)((slot * TILE) >> 4);
-#pragma unroll
-                        for (int q = 0; q < QT; ++q) {
-                            if (!needs(q, t)) continue;
-                            if (ns[q] > 0 && !wait_bar(BAR(B_SFREE + q), (uint32_t)(ns[q] - 1) & 1u)) return false;
+                        if (t >= a && t < b) {
+                            if (any_s && !wait_bar(sfree, s_par ^ 1u)) return false;
                             tc::fence_after_sync();
-                            const uint64_t dq = dq0 + (uint64_t)((q * TILE) >> 4);
+                            const uint64_t dk = dk0 + (uint64_t)(slot * (TILE >> 4));
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint64_t off = (uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                                tc::umma_bf16(tmem + 128u * q, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
+                                tc::umma_bf16(s_tm, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
                             }
-                            tc::umma_commit(BAR(B_SFULL + q));
-                            ++ns[q];
+                            tc::umma_commit(sfull);
+                            tc::umma_commit(BAR(B_EMPTY) + 8u * slot);
+                            any_s = true;
+                            s_par ^= 1u;
+                        } else {
+                            mbar_arrive(BAR(B_EMPTY) + 8u * slot);
                         }
-                        item_done();
-                        if (t + 1 == s.tb) tc::umma_commit(BAR(B_QFREE));             // the share's last S was issued
+                        next_item();
+                        if (t + 1 == tb) tc::umma_commit(BAR(B_QFREE));               // the share's last S was issued
                         return true;
                     };
                     // O += P V of tile t, committed in two halves
                     auto do_pv = [&](int t) -> bool {
                         if (!item()) return false;
-                        const uint64_t dv = dv0 + (uint64_t)((slot * TILE) >> 4);
-#pragma unroll
-                        for (int q = 0; q < QT; ++q) {
-                            if (!needs(q, t)) continue;
+                        if (t >= a && t < b) {
+                            if (!wait_bar(pfull, p_par)) return false;
                             // the share's first P V overwrites O: the previous epilogue must have read it
-                            if (np[q] == first[q] && !ofree(q)) return false;
-                            if (!wait_bar(BAR(B_PFULL + q), (uint32_t)np[q] & 1u)) return false;
+                            if (t == a && units > 0 && !wait_bar(ofree, (uint32_t)(units - 1) & 1u)) return false;
                             tc::fence_after_sync();
-                            const uint64_t dp = dp0 + (uint64_t)((q * TILE) >> 4);
-                            const uint32_t acc = np[q] > first[q] ? 1u : 0u;
+                            const uint64_t dv = dv0 + (uint64_t)(slot * (TILE >> 4));
+                            const uint32_t acc = t > a ? 1u : 0u;
 #pragma unroll
                             for (int kk = 0; kk < BN / 16; ++kk) {
-                                tc::umma_bf16(tmem + 256u + 128u * q, dp + ((uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4),
-                                              dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, kk > 0 ? 1u : acc);
-                                if (kk == BN / 32 - 1) tc::umma_commit(BAR(B_PVA + q));
+                                tc::umma_bf16(o_tm, dp + ((uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4), dv + (uint64_t)((kk * 2048) >> 4), IDESC_O,
+                                              kk > 0 ? 1u : acc);
+                                if (kk == BN / 32 - 1) tc::umma_commit(pva);
                             }
-                            tc::umma_commit(BAR(B_PVDONE + q));
-                            ++np[q];
+                            tc::umma_commit(pvdone);
+                            tc::umma_commit(BAR(B_EMPTY) + 8u * slot);
+                            p_par ^= 1u;
+                        } else {
+                            mbar_arrive(BAR(B_EMPTY) + 8u * slot);
                         }
-                        item_done();
+                        next_item();
                         return true;
                     };
-                    ok = do_s(s.ta);
-                    for (int t = s.ta; ok && t < s.tb; ++t) ok = (t + 1 >= s.tb || do_s(t + 1)) && do_pv(t);
+                    ok = do_s(ta);
+                    for (int t = ta; ok && t < tb; ++t) ok = (t + 1 >= tb || do_s(t + 1)) && do_pv(t);
                     if (!ok) break;
-                    for (int q = 0; ok && q < QT; ++q) {
-                        // a share without a P V of a sub-tile still waits for its previous epilogue, so that
-                        // its completion never runs two shares ahead of the softmax
-                        if (np[q] == first[q]) ok = ofree(q);
-                        if (ok) tc::umma_commit(BAR(B_ODONE + q));
-                    }
+                    // a share without a P V of this sub-tile still waits for its previous epilogue, so that
+                    // its completion never runs two shares ahead of the softmax
+                    if (a >= b && units > 0 && !(ok = wait_bar(ofree, (uint32_t)(units - 1) & 1u))) break;
+                    tc::umma_commit(BAR(B_ODONE + q));
                     ++units;
                 }
             }
