@@ -1,0 +1,504 @@
+// Attention of a few tokens over a paged cache (at most 16 packed rows of a key head), bf16, head
+// dim 128, with the accumulated attention weights.
+//
+// Bound by HBM: every key and value is read once, 512 bytes for at most 16 rows. The division of
+// the work is that of paged.cuh with single blocks as gangs, two blocks per SM: an equal number of
+// 64-key tiles for every block whatever the rollouts' lengths. One warp of a block copies tiles
+// (K and V of 64 keys, 32 KB) into a ring of three by TMA, a lane per page; 192 KB in flight per SM
+// cover the latency several times. Four warps take 16 keys of a tile each and never wait for one
+// another: S = Q K^T of 16 x 16 by warp-level products (the rows fill one m16 tile, a tcgen05 product
+// would be 7/8 padding), running maximum and sum per warp, O += P V with V's fragments through
+// transposing loads. At the end of a piece the warps' results are joined through shared memory; a
+// piece that is a whole head is stored, others go to the workspace.
+// Weights: their scale is known only at the end, so the scaled scores are stored (4 bytes per row
+// and key next to the 512 that are read) and a second kernel turns them into weights while it joins
+// the pieces; reading K again instead would add half of the traffic.
+//
+// What the cache holds where no row looks: as in the chunk kernel, scores are masked before use and
+// values outside the span of the rows are zeroed in shared memory.
+#include "hlta_internal.cuh"
+#include "paged.cuh"
+#include "sm100_ptx.cuh"
+#include "tc_ptx.cuh"
+
+#include <algorithm>
+#include <math.h>
+
+namespace hlta {
+namespace {
+
+using namespace ptx;
+using namespace paged;
+
+constexpr int MROWS = 16, BN = 64, D = 128;
+constexpr int CW = 4, THREADS = 32 * (CW + 1);          // consumer warps; and the producer
+constexpr int NSLOT = 3;
+constexpr uint32_t HALF = BN * 128, KT = 2 * HALF, TILE = 2 * KT;    // [64 keys][64 columns]; K; K and V
+constexpr uint32_t SM_MERGE = NSLOT * TILE;                          // two warps' O in fragment order
+constexpr uint32_t SM_ML = SM_MERGE + 2 * 64 * 32 * 4;               // [warp][row] (maximum, sum)
+constexpr uint32_t SM_OK = SM_ML + CW * MROWS * 8, SM_BAR = SM_OK + 16, SM_PLACE = SM_BAR + 16 * NSLOT;
+constexpr uint32_t SM_ABORT = SM_PLACE + 32;
+constexpr size_t SMEM_BYTES = SM_ABORT + 16;
+static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two blocks per SM");
+constexpr int KEYS = 2048;                              // keys per block of the second kernel
+
+struct Params {
+    Line line;
+    PagedKV c;
+    int G, R;
+    float sl2;
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *o;
+    float *lse;
+    float *part;                    // [block][2][64 registers][32 lanes]
+    float2 *ml;                     // [block][2][16 rows]
+    float *scores;                  // [b][h][R][cap], log2 units; null without weights
+    float2 *whole;                  // [b][h][16 rows] (maximum, sum) of heads that one block had whole
+    const float *w_in;
+    float *w_out, decay;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float quad_max(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x)
+{
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+// factors that bring two (maximum, unnormalised) pairs to the larger maximum
+__device__ __forceinline__ float2 rebase(float m0, float m1, float &m)
+{
+    m = fmaxf(m0, m1);
+    const float base = m == -INFINITY ? 0.f : m;
+    return make_float2(tc::ex2(m0 - base), tc::ex2(m1 - base));
+}
+
+__global__ void __launch_bounds__(THREADS, 2)
+paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const __grid_constant__ Params p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    volatile int *abort_flag = (volatile int *)(smem + SM_ABORT);
+    auto FULL = [&](int i) { return sbase + SM_BAR + 16u * (uint32_t)i; };
+    auto EMPTY = [&](int i) { return sbase + SM_BAR + 16u * (uint32_t)i + 8u; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;");      // the second kernel may be set up meanwhile
+    if (sbase & 1023u) {                    // not seen: the attribute asks for it
+        if (threadIdx.x == 0) atomicOr(p.c.err, DEVERR_ATTN_WAIT);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NSLOT; ++i) {
+            mbar_init(FULL(i), 1);
+            mbar_init(EMPTY(i), CW);
+        }
+        *abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == CW) {
+        const Place c = place_of<BN>(p.line, blockIdx.x);
+        if (lane == 0) *(Place *)(smem + SM_PLACE) = c;
+    }
+    __syncthreads();
+    Place at = *(Place *)(smem + SM_PLACE);
+    auto wait_bar = [&](uint32_t bar, uint32_t parity) -> bool {
+        return mbar_try(bar, parity) || mbar_wait(bar, parity, abort_flag, p.c.err, DEVERR_ATTN_WAIT);
+    };
+    Piece<BN> x;
+    int slot = 0;
+    uint32_t lap = 0;
+    auto next_slot = [&] {
+        if (++slot == NSLOT) {
+            slot = 0;
+            lap ^= 1u;
+        }
+    };
+    // the span of the chunk's live rows: every tile of the line lies in it
+    auto span_all = [&](const Roll &r) {
+        return Span{span_of(r, 0, p.line.N, p.line.w).lo, span_of(r, r.n - 1, p.line.N, p.line.w).hi};
+    };
+
+    if (warp == CW) {
+        const int psz = 1 << p.c.page_log2, box = min(psz, BN), nbox = BN / box;
+        bool ok = true;
+        long issued = 0;
+        while (ok && next_piece<BN>(p.line, at, x)) {
+            if (x.x.r.bad && lane == 0) atomicOr(p.c.err, DEVERR_TABLE);
+            const Span u = span_all(x.x.r);
+            // the first row of this lane's part of tile t, or -1 when none of its positions is seen
+            auto row_at = [&](int t) -> int {
+                const int p0 = t * BN + lane * box;
+                if (lane >= nbox || t >= x.tb || p0 >= u.hi || p0 + box <= u.lo) return -1;
+                return ((page_of(p.c, x.b, max(p0, u.lo)) * p.c.H + x.h) << p.c.page_log2) + (p0 & (psz - 1));
+            };
+            int row = row_at(x.ta);
+            for (int t = x.ta; t < x.tb; ++t) {
+                const int next = row_at(t + 1);             // looked up ahead of the wait
+                bool w = true;
+                if (lane == 0 && issued >= NSLOT) w = wait_bar(EMPTY(slot), lap ^ 1u);
+                if (!(ok = __shfl_sync(0xffffffffu, w, 0))) break;
+                const unsigned have = __ballot_sync(0xffffffffu, row >= 0);
+                if (lane == 0) mbar_expect_tx(FULL(slot), (uint32_t)__popc(have) * (uint32_t)box * 512u);
+                __syncwarp();
+                if (row >= 0) {
+                    const uint32_t dst = sbase + (uint32_t)slot * TILE + (uint32_t)(lane * box) * 128u;
+                    tma_load_2d(dst, &tk, 0, row, FULL(slot));
+                    tma_load_2d(dst + HALF, &tk, 64, row, FULL(slot));
+                    tma_load_2d(dst + KT, &tv, 0, row, FULL(slot));
+                    tma_load_2d(dst + KT + HALF, &tv, 64, row, FULL(slot));
+                }
+                ++issued;
+                next_slot();
+                row = next;
+            }
+        }
+        if (lane == 0 && *abort_flag) {
+            // a bounded wait expired: let the copies this block issued land
+            const long long t0 = clock64();
+            for (long i = issued - 1; i >= 0 && i >= issued - NSLOT; --i)
+                while (!mbar_try(FULL((int)(i % NSLOT)), (uint32_t)(i / NSLOT) & 1u) && clock64() - t0 < (1LL << 31)) {}
+        }
+        return;
+    }
+
+    // ------------------------------- consumers -------------------------------------------------
+    const int g = lane >> 2, c = lane & 3;
+    const int key0 = warp * 16;             // this warp's keys of a tile
+    float *merge = (float *)(smem + SM_MERGE);
+    float2 *sml = (float2 *)(smem + SM_ML);
+    volatile int *sok = (volatile int *)(smem + SM_OK);
+    // addresses of the fragments inside a tile: K as [key][channel] (no transposition), V transposed
+    const int km = lane >> 3, kr = lane & 7;
+    const int kkey = key0 + (km >> 1) * 8 + kr, vkey = key0 + (km & 1) * 8 + kr;
+    auto k_addr = [&](uint32_t base, int kk) {
+        const int col = 16 * kk + (km & 1) * 8;
+        return base + (uint32_t)(col >> 6) * HALF + (uint32_t)kkey * 128u + ((((uint32_t)(col & 63) >> 3) ^ (uint32_t)(kkey & 7)) << 4);
+    };
+    auto v_addr = [&](uint32_t base, int n2) {
+        const int col = 16 * n2 + (km >> 1) * 8;
+        return base + KT + (uint32_t)(col >> 6) * HALF + (uint32_t)vkey * 128u + ((((uint32_t)(col & 63) >> 3) ^ (uint32_t)(vkey & 7)) << 4);
+    };
+    bool ok = true;
+    for (int piece = 0; next_piece<BN>(p.line, at, x); ++piece) {
+        const Span u = span_all(x.x.r);
+        Span v[2];
+        bool live[2];
+        const long row0 = (long)(x.b * p.c.H + x.h) * p.R;
+        uint32_t qa[8][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = g + 8 * j, i = r % p.line.L;
+            live[j] = r < p.R && i < x.x.r.n;
+            v[j] = live[j] ? span_of(x.x.r, i, p.line.N, p.line.w) : Span{0, 0};
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t *s = reinterpret_cast<const uint32_t *>(p.q + (row0 + r) * D + 16 * kk + 2 * c);
+                qa[kk][j] = live[j] ? s[0] : 0u;
+                qa[kk][2 + j] = live[j] ? s[4] : 0u;
+            }
+        }
+        float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
+        for (int t = x.ta; ok && t < x.tb; ++t) {
+            if (!(ok = __all_sync(0xffffffffu, wait_bar(FULL(slot), lap)))) break;
+            const uint32_t base = sbase + (uint32_t)slot * TILE;
+            float s[2][4] = {};
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                uint32_t b[4];
+                ldsm4(k_addr(base, kk), b);
+                mma16816(s[0], qa[kk], b[0], b[1]);
+                mma16816(s[1], qa[kk], b[2], b[3]);
+            }
+            const int p0 = t * BN + key0;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int pos = p0 + 8 * n + 2 * c;
+                    float &a = s[n][2 * j], &d = s[n][2 * j + 1];
+                    a = pos >= v[j].lo && pos < v[j].hi ? a * p.sl2 : -INFINITY;
+                    d = pos + 1 >= v[j].lo && pos + 1 < v[j].hi ? d * p.sl2 : -INFINITY;
+                    // positions are even and the rows' capacity too, so a pair stays in its row
+                    if (p.scores && live[j] && pos < x.x.r.kv)
+                        *reinterpret_cast<float2 *>(p.scores + (row0 + g + 8 * j) * p.line.cap + pos) = make_float2(a, d);
+                }
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float mn = fmaxf(m[j], quad_max(fmaxf(fmaxf(s[0][2 * j], s[0][2 * j + 1]), fmaxf(s[1][2 * j], s[1][2 * j + 1]))));
+                const float mb = mn == -INFINITY ? 0.f : mn;
+                f[j] = tc::ex2(m[j] - mb);
+                m[j] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    s[n][2 * j] = tc::ex2(s[n][2 * j] - mb);
+                    s[n][2 * j + 1] = tc::ex2(s[n][2 * j + 1] - mb);
+                    sum += s[n][2 * j] + s[n][2 * j + 1];
+                }
+                l[j] = fmaf(l[j], f[j], sum);
+            }
+            if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[n][j] *= f[j >> 1];
+            }
+            const bool edge = u.lo > p0 || u.hi < p0 + 16;
+            if (edge) {
+                // values outside the span: zeros (16 rows of 256 bytes, 128 bytes a lane)
+                const int key = key0 + (lane & 15), pos = t * BN + key;
+                if (pos < u.lo || pos >= u.hi) {
+                    const uint32_t a = base + KT + (uint32_t)(lane >> 4) * HALF + (uint32_t)key * 128u;
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a + 16 * y), "r"(0) : "memory");
+                }
+                __syncwarp();
+            }
+            // P as the left operand: the scores' layout is already that of its fragment
+            const uint32_t pa[4] = {tc::pack_bf16(s[0][0], s[0][1]), tc::pack_bf16(s[0][2], s[0][3]), tc::pack_bf16(s[1][0], s[1][1]),
+                                    tc::pack_bf16(s[1][2], s[1][3])};
+#pragma unroll
+            for (int n2 = 0; n2 < 8; ++n2) {
+                uint32_t b[4];
+                ldsm4t(v_addr(base, n2), b);
+                mma16816(o[2 * n2], pa, b[0], b[1]);
+                mma16816(o[2 * n2 + 1], pa, b[2], b[3]);
+            }
+            if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(EMPTY(slot));
+            next_slot();
+        }
+        // join the four warps: 2 and 3 into 0 and 1, then 1 into 0
+        l[0] = quad_sum(l[0]);
+        l[1] = quad_sum(l[1]);
+        auto put = [&](int buf) {
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) merge[(buf * 64 + n * 4 + j) * 32 + lane] = o[n][j];
+            if (c == 0) {
+                sml[warp * MROWS + g] = make_float2(m[0], l[0]);
+                sml[warp * MROWS + g + 8] = make_float2(m[1], l[1]);
+            }
+        };
+        auto take = [&](int buf, int from) {
+            float2 f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 y = sml[from * MROWS + g + 8 * j];
+                float mm;
+                f[j] = rebase(m[j], y.x, mm);
+                m[j] = mm;
+                l[j] = l[j] * f[j].x + y.y * f[j].y;
+            }
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][j] = o[n][j] * f[j >> 1].x + merge[(buf * 64 + n * 4 + j) * 32 + lane] * f[j >> 1].y;
+        };
+        if (warp >= 2) put(warp - 2);
+        if (lane == 0) sok[warp] = ok;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        ok = sok[0] && sok[1] && sok[2] && sok[3];
+        if (!ok) break;                     // all four together
+        if (warp < 2) take(warp, warp + 2);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (warp == 1) put(0);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (warp == 0) {
+            take(0, 1);
+            if (x.whole) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!live[j]) continue;
+                    const long row = row0 + g + 8 * j;
+                    const float inv = l[j] > 0.f ? 1.f / l[j] : l[j] == l[j] ? 0.f : l[j];
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+                        *reinterpret_cast<uint32_t *>(p.o + row * D + 8 * n + 2 * c) = tc::pack_bf16(o[n][2 * j] * inv, o[n][2 * j + 1] * inv);
+                    if (p.lse && c == 0) p.lse[row] = (m[j] + log2f(l[j])) * 0.69314718055994531f;
+                    if (p.scores && c == 0) p.whole[(long)(x.b * p.c.H + x.h) * MROWS + g + 8 * j] = make_float2(m[j], l[j]);
+                }
+            } else {
+                const long sl = (long)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) p.part[(sl * 64 + n * 4 + j) * 32 + lane] = o[n][j];
+                if (c == 0) {
+                    p.ml[sl * MROWS + g] = make_float2(m[0], l[0]);
+                    p.ml[sl * MROWS + g + 8] = make_float2(m[1], l[1]);
+                }
+            }
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+}
+
+// Joins the pieces of heads whose keys were cut, in the order of the blocks, and turns the scores
+// into weights. Block (x, b * H + h): keys x * KEYS ... of that head; block x = 0 also joins.
+__global__ void __launch_bounds__(128) paged_token_join_kernel(const __grid_constant__ Params p)
+{
+    __shared__ float2 s_ml[MROWS];          // a row's maximum, and one over its sum
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y % p.c.H, b = blockIdx.y / p.c.H;
+    const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
+    const int k0 = blockIdx.x * KEYS;
+    if (blockIdx.x > 0 && k0 >= ro.kv) return;
+    const Holders hd = holders_of<BN>(p.line, 0, b, h);
+    const bool cut = hd.T > 0 && hd.g0 != hd.g1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the first kernel's results from here on
+    if (blockIdx.x == 0 && ro.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
+    const long row0 = (long)blockIdx.y * p.R;
+    const int g = lane >> 2, c = lane & 3;
+    if (hd.T == 0 || cut) {
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[4][4] = {};
+        for (int i = hd.g0; cut && i <= hd.g1; ++i) {
+            const long sl = (long)i * 2 + (i == hd.g0 ? hd.slot0 : 0);
+            m[0] = fmaxf(m[0], p.ml[sl * MROWS + g].x);
+            m[1] = fmaxf(m[1], p.ml[sl * MROWS + g + 8].x);
+        }
+#pragma unroll 4
+        for (int i = hd.g0; cut && i <= hd.g1; ++i) {
+            const long sl = (long)i * 2 + (i == hd.g0 ? hd.slot0 : 0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 y = p.ml[sl * MROWS + g + 8 * j];
+                const float f = tc::ex2(y.x - (m[j] == -INFINITY ? 0.f : m[j]));
+                l[j] = fmaf(y.y, f, l[j]);
+                if (blockIdx.x == 0)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            o[n][2 * j + e] = fmaf(p.part[(sl * 64 + (warp * 4 + n) * 4 + 2 * j + e) * 32 + lane], f, o[n][2 * j + e]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = g + 8 * j;
+            if (warp == 0 && c == 0) s_ml[r] = make_float2(m[j], 1.f / l[j]);
+            if (blockIdx.x > 0 || r >= p.R || r % p.line.L >= ro.n) continue;
+            const float inv = l[j] > 0.f ? 1.f / l[j] : l[j] == l[j] ? 0.f : l[j];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                *reinterpret_cast<uint32_t *>(p.o + (row0 + r) * D + 8 * (warp * 4 + n) + 2 * c) = tc::pack_bf16(o[n][2 * j] * inv, o[n][2 * j + 1] * inv);
+            if (p.lse && warp == 0 && c == 0) p.lse[row0 + r] = (m[j] + log2f(l[j])) * 0.69314718055994531f;
+        }
+    } else if (p.w_out && threadIdx.x < p.R) {
+        const float2 y = p.whole[(long)blockIdx.y * MROWS + threadIdx.x];
+        s_ml[threadIdx.x] = make_float2(y.x, 1.f / y.y);
+    }
+    if (!p.w_out) return;
+    __syncthreads();
+    const Span u = ro.n > 0 ? Span{span_of(ro, 0, p.line.N, p.line.w).lo, span_of(ro, ro.n - 1, p.line.N, p.line.w).hi} : Span{0, 0};
+    for (int k = k0 + threadIdx.x; k < min(k0 + KEYS, ro.kv); k += 128) {
+        float t = 0.f;
+        if (k >= u.lo && k < u.hi)
+            for (int r = 0; r < p.R; ++r) {
+                if (r % p.line.L >= ro.n) continue;
+                const float s = p.scores[(row0 + r) * p.line.cap + k];
+                // a row that does not see the key stored -inf (a row that sees none: no NaN from -inf + inf)
+                if (s != -INFINITY) t = fmaf(tc::ex2(s - s_ml[r].x), s_ml[r].y, t);
+            }
+        const long at = (long)blockIdx.y * p.line.cap + k;
+        if (p.w_in && k < ro.h) t = fmaf(p.decay, p.w_in[at], t);
+        p.w_out[at] = t;
+    }
+}
+
+int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 148;
+    }
+    return n;
+}
+size_t part_bytes() { return (size_t)sm_count() * 4 * (64 * 32 * 4 + MROWS * 8); }
+
+}  // namespace
+
+// The scores kept for the weights grow with rollouts x rows x capacity: past 1 GiB the chunk kernel
+// and a second pass over K serve instead.
+bool paged_token_fits(int B, int H, int G, long L, int cap, bool weights)
+{
+    return G * L <= MROWS && (!weights || (double)B * H * G * L * cap * 4 <= (double)(1L << 30));
+}
+
+size_t paged_token_bytes(int B, int H, int G, long L, int cap, bool weights)
+{
+    return part_bytes() + (weights ? (size_t)B * H * (G * L * (size_t)cap * 4 + MROWS * 8) : 0);
+}
+
+cudaError_t launch_paged_token(const PagedAttnArgs &a, cudaStream_t s)
+{
+    const long kv_rows = a.c.num_pages * a.c.H << a.c.page_log2;
+    if (kv_rows + BN >= (1L << 31) || (long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
+    const uint32_t box = (uint32_t)std::min(1 << a.c.page_log2, BN);
+    CUtensorMap mk, mv;
+    cudaError_t e;
+    if ((e = make_tmap_2d_bf16(&mk, a.c.k, kv_rows, D, 64, box, true)) != cudaSuccess) return e;
+    if ((e = make_tmap_2d_bf16(&mv, a.c.v, kv_rows, D, 64, box, true)) != cudaSuccess) return e;
+    const int sms = sm_count();
+    Params p;
+    p.c = a.c;
+    p.G = a.G;
+    p.R = (int)(a.G * a.L);
+    p.line.B = a.B; p.line.H = a.c.H; p.line.L = (int)a.L; p.line.N = a.N; p.line.w = a.w;
+    p.line.cap = a.c.max_pages << a.c.page_log2;
+    p.line.kv_lens = a.c.kv_lens; p.line.new_lens = a.new_lens;
+    p.line.gs = 1; p.line.passes = 1;
+    // no more blocks than the longest rollouts have tiles
+    const long most = (long)a.B * a.c.H * ((p.line.cap + BN - 1) / BN);
+    p.line.ngang = (int)std::min<long>(2L * sms, most);
+    p.sl2 = a.sl2;
+    p.q = (const __nv_bfloat16 *)a.q;
+    p.o = (__nv_bfloat16 *)a.o;
+    p.lse = a.lse;
+    p.part = (float *)a.ws;
+    p.ml = (float2 *)((char *)a.ws + (size_t)sms * 4 * 64 * 32 * 4);
+    p.whole = (float2 *)((char *)a.ws + part_bytes());
+    p.scores = a.w_out ? (float *)(p.whole + (size_t)a.B * a.c.H * MROWS) : nullptr;
+    p.w_in = a.w_in; p.w_out = a.w_out; p.decay = a.decay;
+    if ((e = cudaFuncSetAttribute(paged_token_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess) return e;
+    paged_token_kernel<<<p.line.ngang, THREADS, SMEM_BYTES, s>>>(mk, mv, p), note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.w_out ? (p.line.cap + KEYS - 1) / KEYS : 1), (unsigned)(a.B * a.c.H));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_token_join_kernel, p), note_launch();
+    return e;
+}
+
+}  // namespace hlta
