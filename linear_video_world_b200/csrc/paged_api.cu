@@ -189,7 +189,8 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
         a.ws = ws + pad((size_t)B * Hq * L * 4);
     }
     cudaError_t e = dt == HLTA_BF16 ? launch_paged_attn_tc(a, (cudaStream_t)stream) : launch_paged_attn_simt(a, (cudaStream_t)stream);
-    if (e == cudaSuccess && w_out) e = launch_paged_weights_simt(a, dt == HLTA_BF16, (cudaStream_t)stream);
+    if (e == cudaSuccess && w_out)
+        e = dt == HLTA_BF16 ? launch_paged_weights_tc(a, (cudaStream_t)stream) : launch_paged_weights_simt(a, (cudaStream_t)stream);
     return done(e, "paged attention");
 }
 

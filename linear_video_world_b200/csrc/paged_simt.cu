@@ -339,9 +339,6 @@ size_t paged_attn_simt_bytes(int B, int Hq, int Hkv, long L, int d, int max_keys
 
 cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s) { return run<float>(a, s); }
 
-cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, bool bf16, cudaStream_t s)
-{
-    return bf16 ? run_weights<__nv_bfloat16>(a, s) : run_weights<float>(a, s);
-}
+cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, cudaStream_t s) { return run_weights<float>(a, s); }
 
 }  // namespace hlta
