@@ -313,19 +313,6 @@ def hlta_gdn_chunk_bwd(q, k, v, a, b, S0, dO, dS_final, dq, dk, dv, da, db, dS0,
                                    _stream(stream)))
 
 
-def _need_here(*named):
-    """Tensors of the serving calls: contiguous, on the current device (their kernels are
-    launched there)."""
-    import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for t, n in named:
-        if t is None:
-            continue
-        _need(t, n)
-        if t.device.index != dev:
-            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} is on {t.device}, the current device is cuda:{dev}")
-
-
 def _need_dtype(dtype, *named):
     for t, n in named:
         if t is not None and t.dtype != dtype:
@@ -333,49 +320,56 @@ def _need_dtype(dtype, *named):
 
 
 def _need_shape(t, n, *shape):
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {list(shape)} (got {list(t.shape)})")
+
+
+def _device():
+    """The current CUDA device, -1 without one (a host tensor's device index, too, is refused)."""
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _addresses(dev, *named):
+    """Addresses of the serving calls' tensors (None: a null pointer), each contiguous and on
+    device `dev`, where their kernels are launched."""
+    out = []
+    for t, n in named:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev or not t.is_contiguous():
+            if not t.is_cuda or not t.is_contiguous():
+                raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be a contiguous CUDA tensor")
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} is on {t.device}, the current device is cuda:{dev}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _stream_address(stream):
+    import torch
+    if stream is None:
+        # the address alone: a Stream object costs as much as a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def rope_axes_spec(pairs, grid=None, pos=None, t0=None, base=10000.0, halves=False,
                    shared_freq=False):
     """hlta_rope_axes_t from its parts: pairs = (time, height, width); grid = (height, width) of
     a frame, or pos [B, L, 3] int32; t0 [B] int32, the first frame's index of each rollout."""
-    import torch
     if (grid is None) == (pos is None):
         raise HltaError(HLTA_ERR_INVALID_ARG, "give either a grid or positions")
     if pos is not None and t0 is not None:
         raise HltaError(HLTA_ERR_INVALID_ARG, "t0 goes with a grid")
-    _need_here((pos, "pos"), (t0, "t0"))
-    _need_dtype(torch.int32, (pos, "pos"), (t0, "t0"))
-    gh, gw = grid if grid is not None else (1, 1)
-    return hlta_rope_axes_t((ctypes.c_int * 3)(*pairs), int(halves), int(shared_freq), gh, gw,
-                            base, _addr(pos), _addr(t0))
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def hlta_rope_axes(q, k, q_out, k_out, B, Hq, Hk, L, d, spec, inverse=False, stream=None):
-    _need_here((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))
-    ref = q if q is not None else k
-    _need_dtype(ref.dtype, (q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))
-    _check(_lib.hlta_rope_axes(_p(q), _p(k), _p(q_out), _p(k_out), B, Hq, Hk, L, d,
-                               ctypes.byref(spec), 1 if inverse else 0, _dt(ref), _stream(stream)))
-
-
-def hlta_paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens, B, Hkv, L, d, num_pages,
-                      page, max_pages, spec=None, stream=None):
-    named = ((k, "k"), (v, "v"), (k_pages, "k_pages"), (v_pages, "v_pages"))
-    ints = ((table, "table"), (kv_lens, "kv_lens"), (new_lens, "new_lens"))
-    _need_here(*named, *ints)
-    _need_dtype(k.dtype, *named)
-    _need_dtype(_int32(), *ints)
-    _check(_lib.hlta_paged_append(_p(k), _p(v), _p(k_pages), _p(v_pages), _p(table), _p(kv_lens),
-                                  _p(new_lens), B, Hkv, L, d, num_pages, page, max_pages,
-                                  None if spec is None else ctypes.byref(spec), _dt(k),
-                                  _stream(stream)))
+    spec = hlta_rope_axes_t()
+    spec.pairs[:] = pairs
+    spec.layout, spec.shared_freq, spec.base = halves, shared_freq, base
+    spec.grid_h, spec.grid_w = grid if grid is not None else (1, 1)
+    if pos is not None or t0 is not None:
+        _need_dtype(_int32(), (pos, "pos"), (t0, "t0"))
+        spec.pos, spec.t0 = _addresses(_device(), (pos, "pos"), (t0, "t0"))
+    return spec
 
 
 def _int32():
@@ -386,6 +380,26 @@ def _int32():
 def _float32():
     import torch
     return torch.float32
+
+
+def hlta_rope_axes(q, k, q_out, k_out, B, Hq, Hk, L, d, spec, inverse=False, stream=None):
+    named = ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))
+    ref = q if q is not None else k
+    _need_dtype(ref.dtype, *named)
+    _check(_lib.hlta_rope_axes(*_addresses(_device(), *named), B, Hq, Hk, L, d,
+                               ctypes.byref(spec), 1 if inverse else 0, _dt(ref),
+                               _stream_address(stream)))
+
+
+def hlta_paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens, B, Hkv, L, d, num_pages,
+                      page, max_pages, spec=None, stream=None):
+    named = ((k, "k"), (v, "v"), (k_pages, "k_pages"), (v_pages, "v_pages"))
+    ints = ((table, "table"), (kv_lens, "kv_lens"), (new_lens, "new_lens"))
+    _need_dtype(k.dtype, *named)
+    _need_dtype(_int32(), *ints)
+    _check(_lib.hlta_paged_append(*_addresses(_device(), *named, *ints), B, Hkv, L, d, num_pages,
+                                  page, max_pages, None if spec is None else ctypes.byref(spec),
+                                  _dt(k), _stream_address(stream)))
 
 
 def hlta_paged_attn_workspace_bytes(B, Hq, Hkv, L, d, page, max_pages, weights=False,
@@ -400,16 +414,15 @@ def hlta_paged_attn_fwd(q, k_pages, v_pages, table, kv_lens, new_lens, o, lse, w
     named = ((q, "q"), (k_pages, "k_pages"), (v_pages, "v_pages"), (o, "o"))
     ints = ((table, "table"), (kv_lens, "kv_lens"), (new_lens, "new_lens"))
     floats = ((lse, "lse"), (w_in, "w_in"), (w_out, "w_out"))
-    _need_here(*named, *ints, *floats, (workspace, "workspace"))
     _need_dtype(q.dtype, *named)
     _need_dtype(_int32(), *ints)
     _need_dtype(_float32(), *floats)
-    _check(_lib.hlta_paged_attn_fwd(_p(q), _p(k_pages), _p(v_pages), _p(table), _p(kv_lens),
-                                    _p(new_lens), _p(o), _p(lse), _p(w_in), _p(w_out),
-                                    float(decay), B, Hq, Hkv, L, d, num_pages, page, max_pages, N,
-                                    w, float(scale), _p(workspace),
+    pq, pk, pv, po, pt, pl, pn, ps, pi, pw, ws = _addresses(_device(), *named, *ints, *floats,
+                                                            (workspace, "workspace"))
+    _check(_lib.hlta_paged_attn_fwd(pq, pk, pv, pt, pl, pn, po, ps, pi, pw, decay, B, Hq, Hkv, L,
+                                    d, num_pages, page, max_pages, N, w, scale, ws,
                                     workspace.numel() * workspace.element_size(), _dt(q),
-                                    _stream(stream)))
+                                    _stream_address(stream)))
 
 
 def hlta_paged_evict_workspace_bytes(B, Hkv, budget) -> int:
@@ -423,38 +436,35 @@ def hlta_paged_evict(weights, k_pages, v_pages, table, kv_lens, B, Hkv, d, num_p
     ints = ((table, "table"), (kv_lens, "kv_lens"), (dst_table, "dst_table"),
             (new_lens, "new_lens"), (kept, "kept"))
     floats = ((weights, "weights"), (w_out, "w_out"))
-    _need_here(*named, *ints, *floats, (workspace, "workspace"))
     _need_dtype(k_pages.dtype, *named)
     _need_dtype(_int32(), *ints)
     _need_dtype(_float32(), *floats)
-    _check(_lib.hlta_paged_evict(_p(weights), _p(k_pages), _p(v_pages), _p(table), _p(kv_lens), B,
-                                 Hkv, d, num_pages, page, max_pages, budget, sink, recent,
-                                 _p(k_dst), _p(v_dst), _p(dst_table), num_dst, max_dst,
-                                 _p(new_lens), _p(kept), _p(w_out), _p(workspace),
+    pk, pv, dk, dv, pt, pl, dt, pn, pi, pw, po, ws = _addresses(
+        _device(), *named, *ints, *floats, (workspace, "workspace"))
+    _check(_lib.hlta_paged_evict(pw, pk, pv, pt, pl, B, Hkv, d, num_pages, page, max_pages, budget,
+                                 sink, recent, dk, dv, dt, num_dst, max_dst, pn, pi, po, ws,
                                  workspace.numel() * workspace.element_size(), _dt(k_pages),
-                                 _stream(stream)))
+                                 _stream_address(stream)))
 
 
-def _gdn_step_check(q, k, v, a, b, o, S, S_out, slots, lens):
-    _need_here((q, "q"), (k, "k"), (v, "v"), (a, "a"), (b, "b"), (o, "o"), (S, "S"),
-               (S_out, "S_out"), (slots, "slots"), (lens, "lens"))
+def _gdn_step_args(q, k, v, a, b, o, S, S_out, slots, lens):
     _need_dtype(q.dtype, (k, "k"), (v, "v"), (o, "o"))
     _need_dtype(_float32(), (a, "a"), (b, "b"), (S, "S"), (S_out, "S_out"))
     _need_dtype(_int32(), (slots, "slots"), (lens, "lens"))
+    return _addresses(_device(), (q, "q"), (k, "k"), (v, "v"), (a, "a"), (b, "b"), (o, "o"),
+                      (S, "S"), (S_out, "S_out"), (slots, "slots"), (lens, "lens"))
 
 
 def hlta_gdn_step(q, k, v, a, b, o, S, S_out, slots, lens, B, H, L, d, num_slots, stream=None):
-    _gdn_step_check(q, k, v, a, b, o, S, S_out, slots, lens)
-    _check(_lib.hlta_gdn_step(_p(q), _p(k), _p(v), _p(a), _p(b), _p(o), _p(S), _p(S_out),
-                              _p(slots), _p(lens), B, H, L, d, num_slots, _dt(q), _stream(stream)))
+    args = _gdn_step_args(q, k, v, a, b, o, S, S_out, slots, lens)
+    _check(_lib.hlta_gdn_step(*args, B, H, L, d, num_slots, _dt(q), _stream_address(stream)))
 
 
 def hlta_gdn_step_raw(q, k, v, x, y, c, o, S, S_out, slots, lens, B, H, L, d, num_slots,
                       stream=None):
-    _gdn_step_check(q, k, v, x, y, o, S, S_out, slots, lens)
-    _check(_lib.hlta_gdn_step_raw(_p(q), _p(k), _p(v), _p(x), _p(y), float(c), _p(o), _p(S),
-                                  _p(S_out), _p(slots), _p(lens), B, H, L, d, num_slots, _dt(q),
-                                  _stream(stream)))
+    args = _gdn_step_args(q, k, v, x, y, o, S, S_out, slots, lens)
+    _check(_lib.hlta_gdn_step_raw(*args[:5], c, *args[5:], B, H, L, d, num_slots, _dt(q),
+                                  _stream_address(stream)))
 
 
 def hlta_device_status(stream=None) -> int:

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <stdint.h>
 
 namespace hlta {
@@ -205,6 +206,12 @@ cudaError_t launch_frame_advance(int *f, int F, cudaStream_t s);
 // in place; sign -1 for the inverse rotation
 cudaError_t launch_rope(void *q, void *k, bool bf16, int B, int Htot, int h0, int Hr, long L,
                         int N, int d, double base, int pos_mode, int sign, cudaStream_t s);
+
+// SMs of the current device (asked once per device; 148 without a device).
+int device_sms();
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device (once per kernel and
+// device: `done` is the kernel's own word of device bits).
+cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<unsigned long long> &done);
 
 // Rotary positions over several axes (rope_axes.cu); q or k null: skipped.
 cudaError_t launch_rope_axes(const void *q, const void *k, void *q_out, void *k_out, int B, int Hq, int Hk,

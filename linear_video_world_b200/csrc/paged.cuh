@@ -7,6 +7,27 @@
 namespace hlta {
 namespace paged {
 
+// Division by a number fixed for the launch (of non-negative numbers below 2^31): quotient
+// (umulhi(m, x) + x) >> s with s the bits of d - 1 and m = floor(2^32 (2^s - d) / d) + 1 (the
+// invariant division of Granlund and Montgomery).
+struct FastDiv {
+    unsigned d, m, s;
+};
+__host__ inline FastDiv fast_div(unsigned d)
+{
+    FastDiv f;
+    f.d = d;
+    f.s = 0;
+    while ((1ull << f.s) < d) ++f.s;
+    f.m = (unsigned)((((1ull << f.s) - d) << 32) / d + 1);
+    return f;
+}
+__device__ __forceinline__ int fdiv(int x, const FastDiv &f)
+{
+    return (int)((__umulhi(f.m, (unsigned)x) + (unsigned)x) >> f.s);
+}
+__device__ __forceinline__ int frem(int x, const FastDiv &f) { return x - fdiv(x, f) * (int)f.d; }
+
 // A rollout of the batch: kv tokens cached, n of them new (the chunk), h before the chunk.
 // Lengths that do not fit are clamped (h may be negative: the chunk's first rows then lie before
 // position 0).
@@ -29,14 +50,24 @@ __device__ __forceinline__ Roll roll_of(const int *kv_lens, const int *new_lens,
 struct Span {
     int lo, hi;
 };
-__device__ __forceinline__ Span span_of(const Roll &r, int i, int N, int w)
+// (w frames of N tokens back; `back` = (w - 1) N, clamped to 2^30, or 2^30 for no window).
+struct Mask {
+    FastDiv N;
+    int back;
+};
+__host__ inline Mask mask_of(int N, int w)
 {
-    const long long f = i / N;
-    const long long hi = (long long)r.h + (f + 1) * N;
-    const long long lo = w > 0 ? (long long)r.h + (f - w + 1) * N : 0;
+    // frames longer than any chunk (2^29 tokens) are all alike
+    const long long n = N < (1 << 30) ? N : (1 << 30) - 1, b = w > 0 ? (long long)(w - 1) * n : 1LL << 30;
+    return Mask{fast_div((unsigned)n), (int)(b < (1LL << 30) ? b : 1LL << 30)};
+}
+__device__ __forceinline__ Span span_of(const Roll &r, int i, const Mask &m)
+{
+    // h + start is a position, at most 2^30, and N below that: the sums stay inside 32 bits
+    const int start = fdiv(i, m.N) * (int)m.N.d, hi = r.h + start + (int)m.N.d, lo = r.h + start - m.back;
     Span s;
-    s.hi = (int)(hi < 0 ? 0 : hi < r.kv ? hi : r.kv);
-    s.lo = (int)(lo < 0 ? 0 : lo < r.kv ? lo : r.kv);
+    s.hi = max(0, min(hi, r.kv));
+    s.lo = max(0, min(lo, r.kv));
     return s;
 }
 
@@ -63,9 +94,28 @@ __device__ __forceinline__ int page_of(const PagedKV &c, int b, int p)
 // in the workspace, at most two per block: slot 0 for the first piece of its range, slot 1 for the
 // last.
 struct Line {
-    int B, H, L, N, w, cap, gs, ngang, passes;
+    int B, H, L, cap, gs, ngang, passes;
+    FastDiv byL;
+    Mask mask;
     const int *kv_lens, *new_lens;
 };
+__host__ inline Line line_of(const PagedAttnArgs &a, int gs, int ngang, int passes)
+{
+    Line p;
+    p.B = a.B; p.H = a.c.H; p.L = (int)a.L;
+    p.cap = a.c.max_pages << a.c.page_log2;
+    p.gs = gs; p.ngang = ngang; p.passes = passes;
+    p.byL = fast_div((unsigned)(a.L > 0 ? a.L : 1));
+    p.mask = mask_of(a.N, a.w);
+    p.kv_lens = a.c.kv_lens; p.new_lens = a.new_lens;
+    return p;
+}
+// 64-bit quotient; in 32 bits where both fit (a third of the time)
+__device__ __forceinline__ long long quot(long long a, long long b)
+{
+    return (unsigned long long)a >> 32 || (unsigned long long)b >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 template <int TK>
 struct Tiles {
     Roll r;
@@ -78,7 +128,7 @@ __device__ __forceinline__ Tiles<TK> tiles_of(const Line &p, int b)
     x.r = roll_of(p.kv_lens, p.new_lens, b, p.L, p.cap);
     x.t0 = x.T = 0;
     if (x.r.n > 0) {
-        const int lo = span_of(x.r, 0, p.N, p.w).lo, hi = span_of(x.r, x.r.n - 1, p.N, p.w).hi;
+        const int lo = span_of(x.r, 0, p.mask).lo, hi = span_of(x.r, x.r.n - 1, p.mask).hi;
         if (hi > lo) {
             x.t0 = lo / TK;
             x.T = (hi + TK - 1) / TK - x.t0;
@@ -114,9 +164,9 @@ __device__ __forceinline__ Place place_of(const Line &p, int g)
     c.left = 0;
     c.pass = c.b = c.h = c.t = 0;
     if (g >= ng) return c;
-    const long long a = W * g / ng;
-    c.left = (int)(W * (g + 1) / ng - a);
-    c.pass = (int)(a / per);
+    const long long a = quot(W * g, ng);
+    c.left = (int)(quot(W * (g + 1), ng) - a);
+    c.pass = p.passes > 1 ? (int)quot(a, per) : 0;
     long long x = a - per * c.pass;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const long long n = b0 + lane < p.B ? (long long)tiles_of<TK>(p, b0 + lane).T * p.H : 0;
@@ -129,10 +179,10 @@ __device__ __forceinline__ Place place_of(const Line &p, int g)
         if (in) {
             const int f = __ffs(in) - 1;
             const long long before = __shfl_sync(0xffffffffu, s - n, f);
-            const int T = (int)(__shfl_sync(0xffffffffu, n, f) / p.H);
+            const int T = tiles_of<TK>(p, b0 + f).T;
             c.b = b0 + f;
             x -= before;
-            c.h = (int)(x / T);
+            c.h = (int)quot(x, T);
             c.t = (int)(x - (long long)c.h * T);
             return c;
         }
@@ -196,9 +246,9 @@ __device__ __forceinline__ Holders holders_of(const Line &p, int pass, int b, in
     if (o.T == 0) return o;
     // gang g holds [W g / ng, W (g + 1) / ng), rounded down
     const long long ng = W < p.ngang ? W : p.ngang;
-    o.g0 = (int)(((a + 1) * ng - 1) / W);
-    o.g1 = (int)(((a + o.T) * ng - 1) / W);
-    o.slot0 = W * o.g0 / ng == a ? 0 : 1;
+    o.g0 = (int)quot((a + 1) * ng - 1, W);
+    o.g1 = (int)quot((a + o.T) * ng - 1, W);
+    o.slot0 = quot(W * o.g0, ng) == a ? 0 : 1;
     return o;
 }
 

@@ -86,6 +86,37 @@ hlta_status done(cudaError_t e, const char *what)
 size_t pad(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
+
+int device_sms()
+{
+    static std::atomic<int> sms[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return 148;
+    }
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 148;
+    }
+    sms[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<unsigned long long> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
+}
+
 }  // namespace hlta
 
 using namespace hlta;
@@ -133,7 +164,7 @@ hlta_status hlta_paged_append(const void *k, const void *v, void *k_pages, void 
 
 size_t hlta_paged_attn_workspace_bytes(int B, int Hq, int Hkv, long L, int d, int page, int max_pages, int weights, hlta_dtype dt)
 {
-    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || L < 0 || L > (1L << 30) || d < 1 || d > 128 || max_pages < 1 || page < 1 ||
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || L < 0 || L > (1L << 29) || d < 1 || d > 128 || max_pages < 1 || page < 1 ||
         (long)max_pages * page > (1L << 30) || (dt != HLTA_BF16 && dt != HLTA_FP32))
         return 0;
     if (dt == HLTA_BF16 && paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, weights != 0))
@@ -149,7 +180,7 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
 {
     hlta_status st;
     if ((!q || !o) && B > 0 && L > 0) return FAIL("null tensor pointer");
-    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || L < 0 || L > (1L << 30))
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || L < 0 || L > (1L << 29))
         return FAIL("bad shape B=%d Hq=%d Hkv=%d L=%ld (Hq must be a multiple of Hkv)", B, Hq, Hkv, L);
     if ((st = check_type(dt, d, true)) != HLTA_OK) return st;
     if ((st = check_cache(k_pages, v_pages, table, kv_lens, B, Hkv, num_pages, page, max_pages)) != HLTA_OK) return st;

@@ -58,7 +58,7 @@ __device__ __forceinline__ void stage(const PagedKV &c, const void *pages, int b
 }
 
 template <typename E>
-__global__ void __launch_bounds__(THREADS) paged_attn_kernel(PagedAttnArgs a, int nsplit, float *ws_m, float *ws_l, float *ws_o)
+__global__ void __launch_bounds__(THREADS) paged_attn_kernel(PagedAttnArgs a, Mask mask, int nsplit, float *ws_m, float *ws_l, float *ws_o)
 {
     extern __shared__ float smem[];
     const int d = a.c.d, dp = (d + 3) & ~3, kst = dp + 4;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(THREADS) paged_attn_kernel(PagedAttnArgs a, in
     for (int r = 0; r < QB; ++r) {
         const int i = (r0 + r) % (int)a.L;
         if (r0 + r >= R || i >= ro.n) continue;
-        const Span s = span_of(ro, i, a.N, a.w);
+        const Span s = span_of(ro, i, mask);
         if (s.hi > s.lo) {
             lo = min(lo, s.lo);
             hi = max(hi, s.hi);
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(THREADS) paged_attn_kernel(PagedAttnArgs a, in
     for (int r = 0; r < RPW; ++r) {
         const int rr = r0 + warp * RPW + r, i = rr % (int)a.L;
         live[r] = rr < R && i < ro.n;
-        sp[r] = live[r] ? span_of(ro, i, a.N, a.w) : Span{0, 0};
+        sp[r] = live[r] ? span_of(ro, i, mask) : Span{0, 0};
     }
     const int t_lo = hi > lo ? lo / KT : 0, nt = hi > lo ? (hi + KT - 1) / KT - t_lo : 0;
     const int ta = t_lo + (int)((long)nt * blockIdx.z / nsplit), tb = t_lo + (int)((long)nt * (blockIdx.z + 1) / nsplit);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(PagedAttnArgs a, in
 // the head group that sees them, 2^(score - lse) in the order of the rows; each warp takes every
 // fourth group of four rows, and the four partial sums are joined at the end.
 template <typename E>
-__global__ void __launch_bounds__(THREADS) paged_weights_kernel(PagedAttnArgs a)
+__global__ void __launch_bounds__(THREADS) paged_weights_kernel(PagedAttnArgs a, Mask mask)
 {
     extern __shared__ float smem[];
     const int d = a.c.d, dp = (d + 3) & ~3, kst = dp + 4;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(THREADS) paged_weights_kernel(PagedAttnArgs a)
         bool any = false;
         for (int r = rb; r < min(R, rb + QB); ++r) {
             const int i = r % (int)a.L;
-            const Span s = i < ro.n ? span_of(ro, i, a.N, a.w) : Span{0, 0};
+            const Span s = i < ro.n ? span_of(ro, i, mask) : Span{0, 0};
             any = any || (s.lo < p0 + KT && s.hi > p0 && s.hi > s.lo);
         }
         if (!any) continue;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(THREADS) paged_weights_kernel(PagedAttnArgs a)
         for (int r = 0; r < RPW; ++r) {
             const int rr = rb + warp * RPW + r, i = rr % (int)a.L;
             if (rr >= R || i >= ro.n) continue;
-            const Span v = span_of(ro, i, a.N, a.w);
+            const Span v = span_of(ro, i, mask);
             if (v.hi <= v.lo) continue;
             const float z = a.lse[row0 + rr] * 1.4426950408889634f;
             const int pa = p0 + lane, pb = pa + 32;
@@ -306,7 +306,7 @@ cudaError_t run(const PagedAttnArgs &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (R > 0) {
         const dim3 grid((unsigned)((R + QB - 1) / QB), (unsigned)(a.B * a.c.H), (unsigned)ns);
-        paged_attn_kernel<E><<<grid, THREADS, sm, s>>>(a, ns, m, l, o), note_launch();
+        paged_attn_kernel<E><<<grid, THREADS, sm, s>>>(a, mask_of(a.N, a.w), ns, m, l, o), note_launch();
     }
     if (R > 0 && ns > 1) {
         const long blocks = (rows + THREADS / 32 - 1) / (THREADS / 32);
@@ -324,7 +324,7 @@ cudaError_t run_weights(const PagedAttnArgs &a, cudaStream_t s)
     const size_t sw = (size_t)(KT * (dp + 4) + QB * dp + THREADS / 32 * KT) * 4;
     cudaError_t e = cudaFuncSetAttribute(paged_weights_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sw);
     if (e != cudaSuccess) return e;
-    paged_weights_kernel<E><<<dim3((unsigned)((keys + KT - 1) / KT), (unsigned)(a.B * a.c.H)), THREADS, sw, s>>>(a), note_launch();
+    paged_weights_kernel<E><<<dim3((unsigned)((keys + KT - 1) / KT), (unsigned)(a.B * a.c.H)), THREADS, sw, s>>>(a, mask_of(a.N, a.w)), note_launch();
     return cudaGetLastError();
 }
 

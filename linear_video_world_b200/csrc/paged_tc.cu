@@ -67,6 +67,7 @@ enum {
 };
 constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS;   // the block's start on the line; the softmax warps' places
 constexpr uint32_t SM_TMEM = SM_PLACE + 9 * 32, SM_ABORT = SM_TMEM + 4;
+std::atomic<unsigned long long> g_shared{0};
 constexpr size_t SMEM_BYTES = SM_ABORT + 4;
 static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
 static_assert(sizeof(Place) <= 32, "place");
@@ -145,7 +146,7 @@ __device__ __forceinline__ Span rows_span(const Params &p, const Roll &ro, int r
     const int L = p.line.L;
     r1 = min(r1, p.R);
     if (r0 >= r1) return Span{0, 0};
-    int i0 = r0 % L, i1 = i0 + (r1 - 1 - r0);
+    int i0 = frem(r0, p.line.byL), i1 = i0 + (r1 - 1 - r0);
     if (i1 >= L) {
         // the range holds the head's last tokens and the next head's first ones
         i0 = 0;
@@ -153,8 +154,8 @@ __device__ __forceinline__ Span rows_span(const Params &p, const Roll &ro, int r
     }
     if (i0 >= ro.n) return Span{0, 0};
     Span s;
-    s.lo = span_of(ro, i0, p.line.N, p.line.w).lo;
-    s.hi = span_of(ro, min(i1, ro.n - 1), p.line.N, p.line.w).hi;
+    s.lo = span_of(ro, i0, p.line.mask).lo;
+    s.hi = span_of(ro, min(i1, ro.n - 1), p.line.mask).hi;
     if (s.hi <= s.lo) s.lo = s.hi = 0;
     return s;
 }
@@ -203,6 +204,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gang = blockIdx.x / p.line.gs, member = blockIdx.x % p.line.gs;
 
+    asm volatile("griddepcontrol.launch_dependents;");      // the second kernel may be set up meanwhile
     if (sbase & 1023u) {                    // not seen: the attribute asks for it
         if (threadIdx.x == 0) atomicOr(p.c.err, DEVERR_ATTN_WAIT);
         return;
@@ -226,6 +228,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         *abort_flag = 0;
         mbar_init_fence();
     }
+    if (warp == WARP_TMA && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)(lane == 0 ? &tq : lane == 1 ? &tk : &tv)) : "memory");
     if (warp == WARP_TMA) {
         const Place c = place_of<BN>(p.line, gang);
         if (lane < 9) *place(lane) = c;
@@ -421,10 +425,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                 Place at = *place(1 + warp);
                 Share s;
                 if (!next_share(p, at, member, s)) break;
-                const int r = s.rt * ROWS + q * BM + row, i = r % p.line.L;
+                const int r = s.rt * ROWS + q * BM + row, i = frem(r, p.line.byL);
                 // a row that is none takes the row tile's span: it computes what nobody reads, and
                 // its warp keeps to the unmasked path
-                const Span v = r < p.R && i < s.x.x.r.n ? span_of(s.x.x.r, i, p.line.N, p.line.w) : s.u;
+                const Span v = r < p.R && i < s.x.x.r.n ? span_of(s.x.x.r, i, p.line.mask) : s.u;
                 a = q ? s.a1 : s.a0;
                 b = q ? s.b1 : s.b0;
                 ta = s.ta;
@@ -530,7 +534,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             items += 2 * n;
             const bool have = k > k0;
             const int r = s.rt * ROWS + q * BM + row;
-            const bool live = r < p.R && r % p.line.L < s.x.x.r.n;
+            const bool live = r < p.R && frem(r, p.line.byL) < s.x.x.r.n;
             const long grow = (long)(s.x.b * p.c.H + s.x.h) * p.R + r;
             const int rr = q * BM + row;
             const long slot = (long)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
@@ -590,10 +594,11 @@ __global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constan
     const int b = bh / p.c.H, h = bh % p.c.H;
     const int rt = r / ROWS, pass = rt / p.line.gs, member = rt % p.line.gs, rr = r % ROWS;
     const Holders g = holders_of<BN>(p.line, pass, b, h);
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the first kernel's results from here on
     if (g.T > 0 && g.g0 == g.g1) return;
     const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
     if (ro.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
-    if (r >= p.R || r % p.line.L >= ro.n) return;
+    if (r >= p.R || frem(r, p.line.byL) >= ro.n) return;
     float m = -INFINITY, l = 0.f;
     float4 acc[4];
 #pragma unroll
@@ -635,16 +640,6 @@ __global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constan
     if (p.lse && warp == 0) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
-int sm_count()
-{
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return 148;
-    }
-    return n;
-}
-
 // Blocks per gang for nr row tiles on `sms` SMs: as many as waste the fewest block-passes, the
 // largest of equals (more blocks that meet in L2).
 int gang_size(int nr, int sms)
@@ -664,7 +659,7 @@ int gang_size(int nr, int sms)
 
 }  // namespace
 
-size_t paged_attn_tc_bytes() { return (size_t)sm_count() * 2 * ROWS * (D * 4 + 8); }
+size_t paged_attn_tc_bytes() { return (size_t)device_sms() * 2 * ROWS * (D * 4 + 8); }
 
 cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
 {
@@ -678,29 +673,34 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     if ((e = make_tmap_2d_bf16(&mq, a.q, q_rows, D, 64, BM, true)) != cudaSuccess) return e;
     if ((e = make_tmap_2d_bf16(&mk, a.c.k, kv_rows, D, 64, (uint32_t)psz, true)) != cudaSuccess) return e;
     if ((e = make_tmap_2d_bf16(&mv, a.c.v, kv_rows, D, 64, (uint32_t)psz, true)) != cudaSuccess) return e;
-    const int sms = sm_count();
+    const int sms = device_sms();
     Params p;
     p.c = a.c;
     p.G = a.G;
     p.R = (int)R;
     p.nr = (int)((R + ROWS - 1) / ROWS);
-    p.line.B = a.B; p.line.H = a.c.H; p.line.L = (int)a.L; p.line.N = a.N; p.line.w = a.w;
-    p.line.cap = a.c.max_pages << a.c.page_log2;
-    p.line.kv_lens = a.c.kv_lens; p.line.new_lens = a.new_lens;
-    p.line.gs = gang_size(p.nr, sms);
-    p.line.ngang = sms / p.line.gs;
-    p.line.passes = (p.nr + p.line.gs - 1) / p.line.gs;
+    const int gs = gang_size(p.nr, sms);
+    p.line = line_of(a, gs, sms / gs, (p.nr + gs - 1) / gs);
     p.sl2 = a.sl2;
     p.o = (__nv_bfloat16 *)a.o;
     p.lse = a.lse;
     p.part = (float *)a.ws;
     p.ml = (float2 *)((char *)a.ws + (size_t)sms * 2 * ROWS * D * 4);
-    if ((e = cudaFuncSetAttribute(paged_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess) return e;
+    if ((e = allow_shared((const void *)paged_attn_tc_kernel, SMEM_BYTES, g_shared)) != cudaSuccess) return e;
     paged_attn_tc_kernel<<<p.line.gs * p.line.ngang, THREADS, SMEM_BYTES, s>>>(mq, mk, mv, p), note_launch();
     const long blocks = (long)a.B * a.c.H * ((R + 31) / 32);
     if (blocks > 0x7fffffffL) return cudaErrorNotSupported;
-    paged_join_tc_kernel<<<(unsigned)blocks, 256, 0, s>>>(p), note_launch();
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_join_tc_kernel, p), note_launch();
+    return e;
 }
 
 }  // namespace hlta

@@ -38,6 +38,7 @@ constexpr uint32_t SM_MERGE = NSLOT * TILE;                          // two warp
 constexpr uint32_t SM_ML = SM_MERGE + 2 * 64 * 32 * 4;               // [warp][row] (maximum, sum)
 constexpr uint32_t SM_OK = SM_ML + CW * MROWS * 8, SM_BAR = SM_OK + 16, SM_PLACE = SM_BAR + 16 * NSLOT;
 constexpr uint32_t SM_ABORT = SM_PLACE + 32;
+std::atomic<unsigned long long> g_shared{0};
 constexpr size_t SMEM_BYTES = SM_ABORT + 16;
 static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two blocks per SM");
 constexpr int KEYS = 2048;                              // keys per block of the second kernel
@@ -112,6 +113,7 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         *abort_flag = 0;
         mbar_init_fence();
     }
+    if (threadIdx.x < 2) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)(threadIdx.x ? &tv : &tk)) : "memory");
     if (warp == CW) {
         const Place c = place_of<BN>(p.line, blockIdx.x);
         if (lane == 0) *(Place *)(smem + SM_PLACE) = c;
@@ -132,7 +134,7 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     };
     // the span of the chunk's live rows: every tile of the line lies in it
     auto span_all = [&](const Roll &r) {
-        return Span{span_of(r, 0, p.line.N, p.line.w).lo, span_of(r, r.n - 1, p.line.N, p.line.w).hi};
+        return Span{span_of(r, 0, p.line.mask).lo, span_of(r, r.n - 1, p.line.mask).hi};
     };
 
     if (warp == CW) {
@@ -204,9 +206,9 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         uint32_t qa[8][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int r = g + 8 * j, i = r % p.line.L;
+            const int r = g + 8 * j, i = frem(r, p.line.byL);
             live[j] = r < p.R && i < x.x.r.n;
-            v[j] = live[j] ? span_of(x.x.r, i, p.line.N, p.line.w) : Span{0, 0};
+            v[j] = live[j] ? span_of(x.x.r, i, p.line.mask) : Span{0, 0};
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 const uint32_t *s = reinterpret_cast<const uint32_t *>(p.q + (row0 + r) * D + 16 * kk + 2 * c);
@@ -359,9 +361,13 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
 }
 
 // Joins the pieces of heads whose keys were cut, in the order of the blocks, and turns the scores
-// into weights. Block (x, b * H + h): keys x * KEYS ... of that head; block x = 0 also joins.
-__global__ void __launch_bounds__(128) paged_token_join_kernel(const __grid_constant__ Params p)
+// into weights. Block (x, b * H + h): keys x * KEYS ... of that head; block x = 0 also joins. The
+// pieces' factors come first, a lane per piece, so that the sums over pieces wait for no chain of
+// loads.
+constexpr int JT = 256, MAXP = 512;                     // threads; pieces of a head (blocks of the first kernel)
+__global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_constant__ Params p)
 {
+    __shared__ float s_f[MAXP][MROWS];      // factor of a piece's row
     __shared__ float2 s_ml[MROWS];          // a row's maximum, and one over its sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y % p.c.H, b = blockIdx.y / p.c.H;
@@ -370,56 +376,60 @@ __global__ void __launch_bounds__(128) paged_token_join_kernel(const __grid_cons
     if (blockIdx.x > 0 && k0 >= ro.kv) return;
     const Holders hd = holders_of<BN>(p.line, 0, b, h);
     const bool cut = hd.T > 0 && hd.g0 != hd.g1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");      // the first kernel's results from here on
     if (blockIdx.x == 0 && ro.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the first kernel's results from here on
     const long row0 = (long)blockIdx.y * p.R;
-    const int g = lane >> 2, c = lane & 3;
+    const int np = cut ? hd.g1 - hd.g0 + 1 : 0;
+    auto slot = [&](int i) { return (long)(hd.g0 + i) * 2 + (i == 0 ? hd.slot0 : 0); };
     if (hd.T == 0 || cut) {
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[4][4] = {};
-        for (int i = hd.g0; cut && i <= hd.g1; ++i) {
-            const long sl = (long)i * 2 + (i == hd.g0 ? hd.slot0 : 0);
-            m[0] = fmaxf(m[0], p.ml[sl * MROWS + g].x);
-            m[1] = fmaxf(m[1], p.ml[sl * MROWS + g + 8].x);
-        }
-#pragma unroll 4
-        for (int i = hd.g0; cut && i <= hd.g1; ++i) {
-            const long sl = (long)i * 2 + (i == hd.g0 ? hd.slot0 : 0);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 y = p.ml[sl * MROWS + g + 8 * j];
-                const float f = tc::ex2(y.x - (m[j] == -INFINITY ? 0.f : m[j]));
-                l[j] = fmaf(y.y, f, l[j]);
-                if (blockIdx.x == 0)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            o[n][2 * j + e] = fmaf(p.part[(sl * 64 + (warp * 4 + n) * 4 + 2 * j + e) * 32 + lane], f, o[n][2 * j + e]);
-            }
-        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int r = g + 8 * j;
-            if (warp == 0 && c == 0) s_ml[r] = make_float2(m[j], 1.f / l[j]);
-            if (blockIdx.x > 0 || r >= p.R || r % p.line.L >= ro.n) continue;
-            const float inv = l[j] > 0.f ? 1.f / l[j] : l[j] == l[j] ? 0.f : l[j];
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-                *reinterpret_cast<uint32_t *>(p.o + (row0 + r) * D + 8 * (warp * 4 + n) + 2 * c) = tc::pack_bf16(o[n][2 * j] * inv, o[n][2 * j + 1] * inv);
-            if (p.lse && warp == 0 && c == 0) p.lse[row0 + r] = (m[j] + log2f(l[j])) * 0.69314718055994531f;
+            const int r = warp * 2 + j;
+            float m = -INFINITY, l = 0.f;
+            for (int i = lane; i < np; i += 32) m = fmaxf(m, p.ml[slot(i) * MROWS + r].x);
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int i = lane; i < np; i += 32) {
+                const float2 y = p.ml[slot(i) * MROWS + r];
+                const float f = tc::ex2(y.x - (m == -INFINITY ? 0.f : m));
+                s_f[i][r] = f;
+                l = fmaf(y.y, f, l);
+            }
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) {
+                s_ml[r] = make_float2(m, l > 0.f ? 1.f / l : l == l ? 0.f : l);
+                if (p.lse && blockIdx.x == 0 && r < p.R && frem(r, p.line.byL) < ro.n) p.lse[row0 + r] = (m + log2f(l)) * 0.69314718055994531f;
+            }
         }
     } else if (p.w_out && threadIdx.x < p.R) {
         const float2 y = p.whole[(long)blockIdx.y * MROWS + threadIdx.x];
         s_ml[threadIdx.x] = make_float2(y.x, 1.f / y.y);
     }
-    if (!p.w_out) return;
     __syncthreads();
-    const Span u = ro.n > 0 ? Span{span_of(ro, 0, p.line.N, p.line.w).lo, span_of(ro, ro.n - 1, p.line.N, p.line.w).hi} : Span{0, 0};
-    for (int k = k0 + threadIdx.x; k < min(k0 + KEYS, ro.kv); k += 128) {
+    if (blockIdx.x == 0 && (hd.T == 0 || cut)) {
+        // eight channels of a row: a pair of registers of the fragment, four lanes
+        const int pair = threadIdx.x >> 3, r = (threadIdx.x & 7) + 8 * (pair & 1);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
+#pragma unroll 8
+        for (int i = 0; i < np; ++i) {
+            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (slot(i) * 64 + 2 * pair) * 8 + (threadIdx.x & 7);
+            const float4 u = src[0], v = src[8];
+            const float f = s_f[i][r];
+            a.x = fmaf(u.x, f, a.x); a.y = fmaf(u.y, f, a.y); a.z = fmaf(u.z, f, a.z); a.w = fmaf(u.w, f, a.w);
+            d.x = fmaf(v.x, f, d.x); d.y = fmaf(v.y, f, d.y); d.z = fmaf(v.z, f, d.z); d.w = fmaf(v.w, f, d.w);
+        }
+        if (r < p.R && frem(r, p.line.byL) < ro.n) {
+            const float inv = s_ml[r].y;
+            *reinterpret_cast<uint4 *>(p.o + (row0 + r) * D + 8 * (pair >> 1)) =
+                make_uint4(tc::pack_bf16(a.x * inv, d.x * inv), tc::pack_bf16(a.y * inv, d.y * inv), tc::pack_bf16(a.z * inv, d.z * inv), tc::pack_bf16(a.w * inv, d.w * inv));
+        }
+    }
+    if (!p.w_out) return;
+    const Span u = ro.n > 0 ? Span{span_of(ro, 0, p.line.mask).lo, span_of(ro, ro.n - 1, p.line.mask).hi} : Span{0, 0};
+    for (int k = k0 + threadIdx.x; k < min(k0 + KEYS, ro.kv); k += JT) {
         float t = 0.f;
         if (k >= u.lo && k < u.hi)
             for (int r = 0; r < p.R; ++r) {
-                if (r % p.line.L >= ro.n) continue;
+                if (frem(r, p.line.byL) >= ro.n) continue;
                 const float s = p.scores[(row0 + r) * p.line.cap + k];
                 // a row that does not see the key stored -inf (a row that sees none: no NaN from -inf + inf)
                 if (s != -INFINITY) t = fmaf(tc::ex2(s - s_ml[r].x), s_ml[r].y, t);
@@ -430,16 +440,7 @@ __global__ void __launch_bounds__(128) paged_token_join_kernel(const __grid_cons
     }
 }
 
-int sm_count()
-{
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return 148;
-    }
-    return n;
-}
-size_t part_bytes() { return (size_t)sm_count() * 4 * (64 * 32 * 4 + MROWS * 8); }
+size_t part_bytes() { return (size_t)device_sms() * 4 * (64 * 32 * 4 + MROWS * 8); }
 
 }  // namespace
 
@@ -464,18 +465,14 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, cudaStream_t s)
     cudaError_t e;
     if ((e = make_tmap_2d_bf16(&mk, a.c.k, kv_rows, D, 64, box, true)) != cudaSuccess) return e;
     if ((e = make_tmap_2d_bf16(&mv, a.c.v, kv_rows, D, 64, box, true)) != cudaSuccess) return e;
-    const int sms = sm_count();
+    const int sms = device_sms();
     Params p;
     p.c = a.c;
     p.G = a.G;
     p.R = (int)(a.G * a.L);
-    p.line.B = a.B; p.line.H = a.c.H; p.line.L = (int)a.L; p.line.N = a.N; p.line.w = a.w;
-    p.line.cap = a.c.max_pages << a.c.page_log2;
-    p.line.kv_lens = a.c.kv_lens; p.line.new_lens = a.new_lens;
-    p.line.gs = 1; p.line.passes = 1;
     // no more blocks than the longest rollouts have tiles
-    const long most = (long)a.B * a.c.H * ((p.line.cap + BN - 1) / BN);
-    p.line.ngang = (int)std::min<long>(2L * sms, most);
+    const long most = (long)a.B * a.c.H * (((a.c.max_pages << a.c.page_log2) + BN - 1) / BN);
+    p.line = line_of(a, 1, (int)std::min<long>(std::min<long>(2L * sms, MAXP), most), 1);
     p.sl2 = a.sl2;
     p.q = (const __nv_bfloat16 *)a.q;
     p.o = (__nv_bfloat16 *)a.o;
@@ -485,12 +482,12 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, cudaStream_t s)
     p.whole = (float2 *)((char *)a.ws + part_bytes());
     p.scores = a.w_out ? (float *)(p.whole + (size_t)a.B * a.c.H * MROWS) : nullptr;
     p.w_in = a.w_in; p.w_out = a.w_out; p.decay = a.decay;
-    if ((e = cudaFuncSetAttribute(paged_token_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess) return e;
+    if ((e = allow_shared((const void *)paged_token_kernel, SMEM_BYTES, g_shared)) != cudaSuccess) return e;
     paged_token_kernel<<<p.line.ngang, THREADS, SMEM_BYTES, s>>>(mk, mv, p), note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.w_out ? (p.line.cap + KEYS - 1) / KEYS : 1), (unsigned)(a.B * a.c.H));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(JT);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

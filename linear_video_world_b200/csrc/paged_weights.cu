@@ -31,6 +31,7 @@ constexpr uint32_t SM_SPAN = SM_Z + 2 * RT * 4, SM_SUM = SM_SPAN + 2 * RT * 8;  
 constexpr uint32_t SM_BAR = SM_SUM + BN * 4;
 enum { B_KFULL, B_KEMPTY = B_KFULL + NK, B_QFULL = B_KEMPTY + NK, B_QEMPTY = B_QFULL + NQ, B_SFULL = B_QEMPTY + NQ, B_SFREE = B_SFULL + NS, NBARS = B_SFREE + NS };
 constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS, SM_OK = SM_PLACE + 32, SM_TMEM = SM_OK + 32, SM_ABORT = SM_TMEM + 4;
+std::atomic<unsigned long long> g_shared{0};
 constexpr size_t SMEM_BYTES = SM_ABORT + 4;
 static_assert(SMEM_BYTES <= 232448 && SM_BAR % 8 == 0, "shared memory of one block");
 
@@ -50,7 +51,7 @@ struct RowTile {
 __device__ __forceinline__ RowTile row_tile(const Params &p, const Roll &ro, int rt, int p0)
 {
     const int L = p.line.L, r0 = rt * RT, r1 = min(r0 + RT, p.R);
-    int i0 = r0 % L, i1 = i0 + (r1 - 1 - r0);
+    int i0 = frem(r0, p.line.byL), i1 = i0 + (r1 - 1 - r0);
     if (i1 >= L) {                  // runs into the next head
         i0 = 0;
         i1 = L - 1;
@@ -58,7 +59,7 @@ __device__ __forceinline__ RowTile row_tile(const Params &p, const Roll &ro, int
     RowTile o{false, false};
     if (i0 >= ro.n) return o;
     const int last = min(i1, ro.n - 1);
-    const Span a = span_of(ro, i0, p.line.N, p.line.w), b = span_of(ro, last, p.line.N, p.line.w);
+    const Span a = span_of(ro, i0, p.line.mask), b = span_of(ro, last, p.line.mask);
     o.any = a.lo < p0 + BN && b.hi > p0 && b.hi > a.lo;
     // spans move with the token: the first row's end and the last row's start bound them all
     o.full = r1 - r0 == RT && i1 < ro.n && a.hi >= p0 + BN && b.lo <= p0;
@@ -128,7 +129,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
         bool ok = true;
         while (ok && next_piece<BN>(p.line, at, x)) {
             const Roll &ro = x.x.r;
-            const Span u{span_of(ro, 0, p.line.N, p.line.w).lo, span_of(ro, ro.n - 1, p.line.N, p.line.w).hi};
+            const Span u{span_of(ro, 0, p.line.mask).lo, span_of(ro, ro.n - 1, p.line.mask).hi};
             const long row0 = (long)(x.b * p.c.H + x.h) * p.R;
             for (int t = x.ta; ok && t < x.tb; ++t) {
                 const int p0 = t * BN + lane * psz;
@@ -226,12 +227,12 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
                     ++nq;
                     if (!mine) continue;
                     // the row tile's log-sum-exp (log2) and spans; rows that are none see nothing
-                    const int r = rt * RT + row, i = r % p.line.L;
+                    const int r = rt * RT + row, i = frem(r, p.line.byL);
                     const bool live = r < p.R && i < ro.n;
                     asm volatile("bar.sync %0, 128;" ::"r"(grp_bar) : "memory");       // the previous one's were read
                     z[row] = live ? p.lse[head * p.R + r] * -1.4426950408889634f : 0.f;
                     if (!k.full) {
-                        const Span v = live ? span_of(ro, i, p.line.N, p.line.w) : Span{0, 0};
+                        const Span v = live ? span_of(ro, i, p.line.mask) : Span{0, 0};
                         spans[row] = make_int2(v.lo, v.hi);
                     }
                     asm volatile("bar.sync %0, 128;" ::"r"(grp_bar) : "memory");
@@ -317,20 +318,15 @@ cudaError_t launch_paged_weights_tc(const PagedAttnArgs &a, cudaStream_t s)
     cudaError_t e;
     if ((e = make_tmap_2d_bf16(&mq, a.q, q_rows, D, 64, RT, true)) != cudaSuccess) return e;
     if ((e = make_tmap_2d_bf16(&mk, a.c.k, kv_rows, D, 64, 1u << a.c.page_log2, true)) != cudaSuccess) return e;
-    int dev = 0, sms = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int sms = device_sms();
     Params p;
     p.c = a.c;
     p.R = (int)R;
-    p.line.B = a.B; p.line.H = a.c.H; p.line.L = (int)a.L; p.line.N = a.N; p.line.w = a.w;
-    p.line.cap = a.c.max_pages << a.c.page_log2;
-    p.line.kv_lens = a.c.kv_lens; p.line.new_lens = a.new_lens;
-    p.line.gs = 1; p.line.passes = 1; p.line.ngang = sms;
+    p.line = line_of(a, 1, sms, 1);
     p.sl2 = a.sl2;
     p.lse = a.lse; p.w_in = a.w_in; p.w_out = a.w_out; p.decay = a.decay;
     if (a.w > 0 || a.new_lens) paged_decay_kernel<<<dim3((unsigned)((p.line.cap + 255) / 256), (unsigned)(a.B * a.c.H)), 256, 0, s>>>(p), note_launch();
-    if ((e = cudaFuncSetAttribute(paged_weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) != cudaSuccess) return e;
+    if ((e = allow_shared((const void *)paged_weights_tc_kernel, SMEM_BYTES, g_shared)) != cudaSuccess) return e;
     paged_weights_tc_kernel<<<sms, THREADS, SMEM_BYTES, s>>>(mq, mk, p), note_launch();
     return cudaGetLastError();
 }
