@@ -28,19 +28,21 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// The rollout's state slot and token count; false: skipped (padded, out of range, or its slot
-// taken by an earlier rollout). Called by every thread of the block.
-__device__ __forceinline__ bool rollout(const GdnStepArgs &p, int b, long &slot, int &n)
+// The rollout's state slot and token count as the tables say.
+__device__ __forceinline__ void rollout(const GdnStepArgs &p, int b, long &slot, int &n)
 {
     slot = p.slots ? p.slots[b] : b;
     n = p.lens ? p.lens[b] : (int)p.L;
-    if (slot < 0) return false;
+}
+// Whether to skip it: out of range, or its slot taken by an earlier rollout. Every thread of the block.
+__device__ __forceinline__ bool refused(const GdnStepArgs &p, int b, long slot, int n)
+{
     int bad = slot >= p.num_slots || n < 0 || n > p.L;
     if (p.slots)
         for (int i = threadIdx.x; i < b; i += blockDim.x) bad |= p.slots[i] == slot;
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0) atomicOr(p.err, DEVERR_TABLE);
-    return !bad;
+    return bad;
 }
 
 // gates of a token: given, or a = exp(-c softplus(x)), b = sigmoid(y)
@@ -57,39 +59,46 @@ __device__ __forceinline__ void gates(const GdnStepArgs &p, long at, float &a, f
 // scale to unit norm; a zero vector stays zero
 __device__ __forceinline__ float unit(float sumsq) { return sumsq > 0.f ? rsqrtf(sumsq) : 0.f; }
 
-constexpr int D = 128, TOK = 4, RPT = 4, NT = 128;      // staged tokens, rows per thread, threads
-constexpr int ROWS = NT / 8 * RPT;                      // rows per block (64)
+constexpr int D = 128, TOK = 4, RPT = 2, NT = 128;      // staged tokens, rows per thread, threads
+constexpr int ROWS = NT / 8 * RPT;                      // rows per block (32)
 
 template <typename E>
-__global__ void __launch_bounds__(NT) gdn_step_kernel(const GdnStepArgs p)
+__global__ void __launch_bounds__(NT, 6) gdn_step_kernel(const GdnStepArgs p)
 {
-    __shared__ __align__(16) float qs[TOK][D], ks[TOK][D];
+    __shared__ __align__(16) float qs[TOK][D], ks[TOK][D], vs[TOK][ROWS];
     __shared__ float as[TOK], bs[TOK], kq[TOK];
     const int b = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     long slot;
     int n;
-    if (!rollout(p, b, slot, n)) return;
-    const int sub = threadIdx.x & 7, row0 = blockIdx.x * ROWS + (threadIdx.x >> 3);
+    rollout(p, b, slot, n);
+    if (slot < 0) return;
+    const int sub = threadIdx.x & 7, row0 = blockIdx.x * ROWS, row = threadIdx.x >> 3;
     const long bh = (long)b * p.H + h;
-    const float *S = p.S + (slot * p.H + h) * D * D;
-    float *So = p.S_out + (slot * p.H + h) * D * D;
+    const float *S = p.S + (min(slot, p.num_slots - 1) * p.H + h) * D * D + (long)(row0 + row) * D + sub * 4;
+    // the state's loads are in flight while the tables are looked through and the tokens staged
     float s[RPT][16];
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const float4 v = *(const float4 *)(S + (row0 + r * (NT / 8)) * D + x * 32 + sub * 4);
+            const float4 v = *(const float4 *)(S + r * (NT / 8) * D + x * 32);
             s[r][4 * x] = v.x; s[r][4 * x + 1] = v.y; s[r][4 * x + 2] = v.z; s[r][4 * x + 3] = v.w;
         }
+    if (refused(p, b, slot, n)) return;
     for (int t0 = 0; t0 < n; t0 += TOK) {
-        __syncthreads();
+        if (t0) __syncthreads();
         if (t0 + warp < n) {            // one warp stages a token
-            const long at = (bh * p.L + t0 + warp) * D;
+            const long tok = bh * p.L + t0 + warp, at = tok * D;
             float q[4], k[4], qq = 0.f, kk = 0.f, qk = 0.f;
+            vs[warp][lane] = ldf((const E *)p.v + at + row0 + lane);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 q[x] = ldf((const E *)p.q + at + x * 32 + lane);
                 k[x] = ldf((const E *)p.k + at + x * 32 + lane);
+            }
+            if (lane == 0) gates(p, tok, as[warp], bs[warp]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
                 qq = fmaf(q[x], q[x], qq);
                 kk = fmaf(k[x], k[x], kk);
                 qk = fmaf(q[x], k[x], qk);
@@ -105,49 +114,53 @@ __global__ void __launch_bounds__(NT) gdn_step_kernel(const GdnStepArgs p)
                 qs[warp][x * 32 + lane] = q[x] * fq;
                 ks[warp][x * 32 + lane] = k[x] * fk;
             }
-            if (lane == 0) {
-                gates(p, bh * p.L + t0 + warp, as[warp], bs[warp]);
-                kq[warp] = qk * fq * fk;
-            }
+            if (lane == 0) kq[warp] = qk * fq * fk;
         }
         __syncthreads();
-        for (int t = t0; t < min(n, t0 + TOK); ++t) {
-            const int j = t - t0;
-            float q[16], k[16];
+        for (int j = 0; j < min(TOK, n - t0); ++j) {
+            float u[RPT] = {}, w[RPT] = {};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float4 vq = *(const float4 *)&qs[j][x * 32 + sub * 4], vk = *(const float4 *)&ks[j][x * 32 + sub * 4];
-                q[4 * x] = vq.x; q[4 * x + 1] = vq.y; q[4 * x + 2] = vq.z; q[4 * x + 3] = vq.w;
-                k[4 * x] = vk.x; k[4 * x + 1] = vk.y; k[4 * x + 2] = vk.z; k[4 * x + 3] = vk.w;
+                const float4 q = *(const float4 *)&qs[j][x * 32 + sub * 4], k = *(const float4 *)&ks[j][x * 32 + sub * 4];
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) {
+                    u[r] = fmaf(s[r][4 * x], k.x, fmaf(s[r][4 * x + 1], k.y, fmaf(s[r][4 * x + 2], k.z, fmaf(s[r][4 * x + 3], k.w, u[r]))));
+                    w[r] = fmaf(s[r][4 * x], q.x, fmaf(s[r][4 * x + 1], q.y, fmaf(s[r][4 * x + 2], q.z, fmaf(s[r][4 * x + 3], q.w, w[r]))));
+                }
             }
+#pragma unroll
+            for (int o = 4; o; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) {
+                    u[r] += __shfl_xor_sync(0xffffffffu, u[r], o);
+                    w[r] += __shfl_xor_sync(0xffffffffu, w[r], o);
+                }
             const float a = as[j], bb = bs[j], qk = kq[j];
+            float g[RPT];
 #pragma unroll
             for (int r = 0; r < RPT; ++r) {
-                float u = 0.f, w = 0.f;
+                g[r] = bb * (vs[j][row + r * (NT / 8)] - a * u[r]);
+                if (sub == 0) stf((E *)p.o + (bh * p.L + t0 + j) * D + row0 + row + r * (NT / 8), fmaf(a, w[r], g[r] * qk));
+            }
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    u = fmaf(s[r][x], k[x], u);
-                    w = fmaf(s[r][x], q[x], w);
+            for (int x = 0; x < 4; ++x) {
+                const float4 k = *(const float4 *)&ks[j][x * 32 + sub * 4];
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) {
+                    s[r][4 * x] = fmaf(a, s[r][4 * x], g[r] * k.x);
+                    s[r][4 * x + 1] = fmaf(a, s[r][4 * x + 1], g[r] * k.y);
+                    s[r][4 * x + 2] = fmaf(a, s[r][4 * x + 2], g[r] * k.z);
+                    s[r][4 * x + 3] = fmaf(a, s[r][4 * x + 3], g[r] * k.w);
                 }
-#pragma unroll
-                for (int o = 4; o; o >>= 1) {
-                    u += __shfl_xor_sync(0xffffffffu, u, o);
-                    w += __shfl_xor_sync(0xffffffffu, w, o);
-                }
-                const long at = (bh * p.L + t) * D + row0 + r * (NT / 8);
-                const float g = bb * (ldf((const E *)p.v + at) - a * u);
-#pragma unroll
-                for (int x = 0; x < 16; ++x) s[r][x] = fmaf(a, s[r][x], g * k[x]);
-                if (sub == 0) stf((E *)p.o + at, fmaf(a, w, g * qk));
             }
         }
     }
+    float *So = p.S_out + (slot * p.H + h) * D * D + (long)(row0 + row) * D + sub * 4;
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-            *(float4 *)(So + (row0 + r * (NT / 8)) * D + x * 32 + sub * 4) =
-                make_float4(s[r][4 * x], s[r][4 * x + 1], s[r][4 * x + 2], s[r][4 * x + 3]);
+            *(float4 *)(So + r * (NT / 8) * D + x * 32) = make_float4(s[r][4 * x], s[r][4 * x + 1], s[r][4 * x + 2], s[r][4 * x + 3]);
 }
 
 // fp32 tensors of any d <= 128: a warp per state row, up to four channels a lane.
@@ -156,7 +169,8 @@ __global__ void __launch_bounds__(NT) gdn_step_any_kernel(const GdnStepArgs p)
     const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31, d = p.d;
     long slot;
     int n;
-    if (!rollout(p, b, slot, n)) return;
+    rollout(p, b, slot, n);
+    if (slot < 0 || refused(p, b, slot, n)) return;
     const int row = blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
     if (row >= d) return;
     const long bh = (long)b * p.H + h, base = (slot * p.H + h) * d * d + (long)row * d;

@@ -2,11 +2,15 @@
 // copy their keys, values and weights to the destination's pages.
 //
 // Choice, one block per (rollout, key head): of the middle positions the `take` largest weights,
-// found by a radix select over order-preserving 32-bit keys of the weights (four passes of 8 bits,
-// from the top: each pass counts the digits of the keys that still match the threshold's prefix);
-// then one pass in order of position numbers the kept ones with a block scan of two counts
-// (above the threshold; equal to it, of which the first `ties` stay).
-// Copy: a warp per kept position, 16 bytes a lane, K and V in flight together. HBM bound.
+// found by a radix select over order-preserving 32-bit keys of the weights (three passes of 11, 11
+// and 10 bits, from the top: each counts the digits of the keys that still match the threshold's
+// prefix). The keys are read from memory once and kept in shared memory (up to KEEP of them; longer
+// rollouts read them again). A warp whose keys share a digit adds them with one atomic: unused
+// positions have equal weights. Then each warp takes a run of positions and numbers the kept ones
+// by ballots, after a scan over the warps' counts (above the threshold; equal to it, of which the
+// first `left` stay).
+// Copy: a warp takes eight kept positions, all their 16-byte words of K and V in flight together.
+// Bound by HBM.
 #include "hlta_internal.cuh"
 #include "paged.cuh"
 
@@ -18,7 +22,10 @@ namespace {
 
 using namespace paged;
 
-constexpr int ST = 1024;                // threads of the choice
+constexpr int ST = 1024, SW = ST / 32;                  // threads and warps of the choice
+constexpr int BINS = 2048, KEEP = 49152;
+constexpr size_t CHOOSE_SMEM = (size_t)(KEEP + BINS) * 4;
+std::atomic<unsigned long long> g_shared{0};
 
 // rises with the weight; equal weights (0 and -0 too) give equal keys, NaN the least
 __device__ __forceinline__ uint32_t key_of(float w)
@@ -28,44 +35,14 @@ __device__ __forceinline__ uint32_t key_of(float w)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ int2 block_scan(int2 v, int2 *warp_s, int2 &total)
-{
-    // exclusive scan over the block's threads in thread order
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int2 x = v;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
-        if (lane >= o) {
-            x.x += a;
-            x.y += b;
-        }
-    }
-    __syncthreads();
-    if (lane == 31) warp_s[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int2 y = lane < ST / 32 ? warp_s[lane] : make_int2(0, 0);
-        for (int o = 1; o < 32; o <<= 1) {
-            const int a = __shfl_up_sync(0xffffffffu, y.x, o), b = __shfl_up_sync(0xffffffffu, y.y, o);
-            if (lane >= o) {
-                y.x += a;
-                y.y += b;
-            }
-        }
-        warp_s[lane] = y;
-    }
-    __syncthreads();
-    total = warp_s[ST / 32 - 1];
-    const int2 before = warp ? warp_s[warp - 1] : make_int2(0, 0);
-    return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
-}
-
 __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int *kept)
 {
-    __shared__ int hist[256];
-    __shared__ int2 warp_s[32];
-    __shared__ uint32_t s_prefix;
+    extern __shared__ uint32_t sm[];
+    uint32_t *hist = sm, *keys = sm + BINS;
+    __shared__ int warp_n[SW], warp_e[SW];
+    __shared__ uint32_t s_digit;
     __shared__ int s_left;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int h = blockIdx.x % a.c.H, b = blockIdx.x / a.c.H;
     const int cap = a.c.max_pages << a.c.page_log2;
     const int kv = a.c.kv_lens[b];
@@ -78,92 +55,143 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
         return;
     }
     const float *w = a.weights + (long)blockIdx.x * cap;
-    const int lo = a.sink, hi = n - a.recent, take = a.budget - a.sink - a.recent;
-    // the take-th largest key of [lo, hi) (take < hi - lo since n > budget)
+    const int lo = a.sink, m = n - a.recent - a.sink, take = a.budget - a.sink - a.recent;
+    const bool held = m <= KEEP;
+    if (held && take > 0) {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < m; i += ST) keys[i] = key_of(w[lo + i]);
+    }
+    auto key = [&](int i) { return held ? keys[i] : key_of(w[lo + i]); };
+    // the take-th largest key of the m middle ones (take < m since n > budget)
     uint32_t prefix = 0, mask = 0;
     int left = take;
     if (take > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = threadIdx.x; i < 256; i += ST) hist[i] = 0;
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+            for (int i = threadIdx.x; i < BINS; i += ST) hist[i] = 0;
             __syncthreads();
-            for (int i = lo + threadIdx.x; i < hi; i += ST) {
-                const uint32_t k = key_of(w[i]);
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+#pragma unroll 4
+            for (int i0 = 0; i0 < m; i0 += ST) {
+                const int i = i0 + threadIdx.x;
+                const uint32_t k = i < m ? key(i) : 0u;
+                const bool in = i < m && (k & mask) == prefix;
+                const uint32_t d = in ? (k >> shift) & ((1u << width) - 1u) : 0xffffffffu;
+                if (__all_sync(0xffffffffu, d == __shfl_sync(0xffffffffu, d, 0))) {
+                    if (lane == 0 && in) atomicAdd(&hist[d], 32u);
+                } else if (in) {
+                    atomicAdd(&hist[d], 1u);
+                }
             }
             __syncthreads();
-            if (threadIdx.x == 0) {
-                int d = 255, acc = 0;
-                while (d > 0 && acc + hist[d] < left) acc += hist[d--];
-                s_prefix = prefix | ((uint32_t)d << shift);
-                s_left = left - acc;
+            // the digit at which the count from the top reaches `left`: thread t owns digits
+            // BINS - 1 - 2 t and BINS - 2 - 2 t
+            const int c0 = (int)hist[BINS - 1 - 2 * threadIdx.x], c1 = (int)hist[BINS - 2 - 2 * threadIdx.x];
+            int x = c0 + c1;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) warp_n[warp] = x;
+            __syncthreads();
+            int before = 0;
+            for (int v = 0; v < SW; ++v) before += v < warp ? warp_n[v] : 0;
+            before += x - c0 - c1;
+            if (before < left && before + c0 + c1 >= left) {
+                const bool second = before + c0 < left;
+                s_digit = (uint32_t)(BINS - 1 - 2 * (int)threadIdx.x - (second ? 1 : 0));
+                s_left = left - before - (second ? c0 : 0);
             }
             __syncthreads();
-            prefix = s_prefix;
+            prefix |= s_digit << shift;
+            mask |= ((1u << width) - 1u) << shift;
             left = s_left;
-            mask |= 255u << shift;
-            __syncthreads();
         }
     } else {
-        prefix = 0xffffffffu;       // nothing is above it
+        prefix = 0xffffffffu;       // nothing is above it, and none of its equals stay
         left = 0;
     }
-    // number the kept positions in order
-    int2 base = make_int2(0, 0);    // kept so far; equal to the threshold so far
-    for (int i0 = 0; i0 < n; i0 += ST) {
-        const int i = i0 + threadIdx.x;
-        bool sure = false, equal = false;
-        if (i < n) {
-            if (i < lo || i >= hi) sure = true;
-            else {
-                const uint32_t k = key_of(w[i]);
-                sure = k > prefix;
-                equal = k == prefix && left > 0;
-            }
-        }
-        int2 total;
-        const int2 at = block_scan(make_int2(sure ? 1 : 0, equal ? 1 : 0), warp_s, total);
-        // of the equal ones before this position, those among the first `left` are kept
-        const int eq = base.y + at.y;
-        const int rank = base.x + at.x + min(eq, left);
-        if (sure || (equal && eq < left)) out[rank] = i;
-        base.x += total.x;
-        base.y += total.y;
+    for (int i = threadIdx.x; i < a.sink; i += ST) out[i] = i;
+    for (int i = threadIdx.x; i < a.recent; i += ST) out[a.sink + take + i] = n - a.recent + i;
+    if (take == 0) return;
+    // number the kept middle positions in order: each warp a run of them
+    const int run = ((m + SW - 1) / SW + 31) & ~31, i_lo = min(m, warp * run), i_hi = min(m, i_lo + run);
+    int above = 0, equal = 0;
+    for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < i_hi ? key(i) : 0u;
+        above += __popc(__ballot_sync(0xffffffffu, i < i_hi && k > prefix));
+        equal += __popc(__ballot_sync(0xffffffffu, i < i_hi && k == prefix));
+    }
+    if (lane == 0) {
+        warp_n[warp] = above;
+        warp_e[warp] = equal;
+    }
+    __syncthreads();
+    above = equal = 0;
+    for (int v = 0; v < warp; ++v) {
+        above += warp_n[v];
+        equal += warp_e[v];
+    }
+    for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < i_hi ? key(i) : 0u;
+        const unsigned is_above = __ballot_sync(0xffffffffu, i < i_hi && k > prefix), is_equal = __ballot_sync(0xffffffffu, i < i_hi && k == prefix);
+        const unsigned below = (1u << lane) - 1u;
+        const int eq = equal + __popc(is_equal & below), rank = above + __popc(is_above & below) + min(eq, left);
+        if ((is_above >> lane & 1u) || ((is_equal >> lane & 1u) && eq < left)) out[a.sink + rank] = lo + i;
+        above += __popc(is_above);
+        equal += __popc(is_equal);
     }
 }
 
-template <int ROW16>
-__device__ __forceinline__ void copy_row(const char *s, char *d, int bytes, int lane)
-{
-    if constexpr (ROW16) {
-        for (int x = lane * 16; x < bytes; x += 512) *(uint4 *)(d + x) = *(const uint4 *)(s + x);
-    } else {
-        for (int x = lane * 2; x < bytes; x += 64) *(uint16_t *)(d + x) = *(const uint16_t *)(s + x);
-    }
-}
+constexpr int CPW = 8;                                  // kept positions per warp of the copy
 
-template <int ROW16>
-__global__ void __launch_bounds__(256) evict_copy_kernel(PagedEvictArgs a, const int *kept, int row_bytes)
+// WORD: bytes per access (16, or 2 for rows of another length)
+template <typename WORD>
+__global__ void __launch_bounds__(256) evict_copy_kernel(PagedEvictArgs a, const int *kept, int words)
 {
     const int lane = threadIdx.x & 31;
+    const int per = (a.budget + CPW - 1) / CPW;         // warps per head
     const long item = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const long bh = item / a.budget;
+    const long bh = item / per;
     if (bh >= (long)a.B * a.c.H) return;
-    const int r = (int)(item - bh * a.budget);
-    const int h = (int)(bh % a.c.H), b = (int)(bh / a.c.H);
-    const int src = kept[item];
-    if (src < 0) return;
+    const int r0 = (int)(item - bh * per) * CPW, h = (int)(bh % a.c.H), b = (int)(bh / a.c.H);
     const int psz = 1 << a.c.page_log2;
-    const int dpg = a.dst_table[(long)b * a.max_dst + (r >> a.c.page_log2)];
-    if (dpg < 0 || dpg >= a.num_dst) {
-        if (lane == 0) atomicOr(a.c.err, DEVERR_TABLE);
-        return;
+    // lanes 0-7: where the eight positions come from and go, in words
+    long s = 0, d = -1;
+    if (lane < CPW && r0 + lane < a.budget) {
+        const int r = r0 + lane, src = kept[bh * a.budget + r];
+        if (src >= 0) {
+            const int dpg = a.dst_table[(long)b * a.max_dst + (r >> a.c.page_log2)];
+            if (dpg < 0 || dpg >= a.num_dst) {
+                atomicOr(a.c.err, DEVERR_TABLE);
+            } else {
+                s = (((long)page_of(a.c, b, src) * a.c.H + h) * psz + (src & (psz - 1))) * words;
+                d = (((long)dpg * a.c.H + h) * psz + (r & (psz - 1))) * words;
+                if (a.w_out)
+                    a.w_out[bh * ((long)a.max_dst << a.c.page_log2) + r] = a.weights[bh * ((long)a.c.max_pages << a.c.page_log2) + src];
+            }
+        }
     }
-    const long s = (((long)page_of(a.c, b, src) * a.c.H + h) * psz + (src & (psz - 1))) * row_bytes;
-    const long d = (((long)dpg * a.c.H + h) * psz + (r & (psz - 1))) * row_bytes;
-    copy_row<ROW16>((const char *)a.c.k + s, (char *)a.k_dst + d, row_bytes, lane);
-    copy_row<ROW16>((const char *)a.c.v + s, (char *)a.v_dst + d, row_bytes, lane);
-    if (a.w_out && lane == 0)
-        a.w_out[bh * ((long)a.max_dst << a.c.page_log2) + r] = a.weights[bh * ((long)a.c.max_pages << a.c.page_log2) + src];
+    // a lane's words of K and V of all eight: the row of K, then that of V
+    for (int x0 = 0; x0 < 2 * words; x0 += 32) {
+        const int x = x0 + lane;
+        const bool in = x < 2 * words, in_k = x < words;
+        const WORD *src = (const WORD *)(in_k ? a.c.k : a.c.v) + (in_k ? x : x - words);
+        WORD *dst = (WORD *)(in_k ? a.k_dst : a.v_dst) + (in_k ? x : x - words);
+        WORD v[CPW];
+#pragma unroll
+        for (int j = 0; j < CPW; ++j) {
+            const long at = __shfl_sync(0xffffffffu, s, j);
+            const bool go = __shfl_sync(0xffffffffu, d, j) >= 0;
+            if (in && go) v[j] = src[at];
+        }
+#pragma unroll
+        for (int j = 0; j < CPW; ++j) {
+            const long at = __shfl_sync(0xffffffffu, d, j);
+            if (in && at >= 0) dst[at] = v[j];
+        }
+    }
 }
 
 }  // namespace
@@ -174,13 +202,15 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, bool bf16, cudaStream_t 
 {
     const long bh = (long)a.B * a.c.H;
     if (bh == 0) return cudaSuccess;
-    const long blocks = (bh * a.budget + 7) / 8;
+    const long blocks = (bh * ((a.budget + CPW - 1) / CPW) + 7) / 8;
     if (bh > 0x7fffffffL || blocks > 0x7fffffffL) return cudaErrorNotSupported;
     int *kept = a.kept ? a.kept : (int *)a.ws;
-    evict_choose_kernel<<<(unsigned)bh, ST, 0, s>>>(a, kept), note_launch();
+    cudaError_t e = allow_shared((const void *)evict_choose_kernel, CHOOSE_SMEM, g_shared);
+    if (e != cudaSuccess) return e;
+    evict_choose_kernel<<<(unsigned)bh, ST, CHOOSE_SMEM, s>>>(a, kept), note_launch();
     const int row = a.c.d * (bf16 ? 2 : 4);
-    if (row % 16 == 0) evict_copy_kernel<1><<<(unsigned)blocks, 256, 0, s>>>(a, kept, row), note_launch();
-    else evict_copy_kernel<0><<<(unsigned)blocks, 256, 0, s>>>(a, kept, row), note_launch();
+    if (row % 16 == 0) evict_copy_kernel<uint4><<<(unsigned)blocks, 256, 0, s>>>(a, kept, row / 16), note_launch();
+    else evict_copy_kernel<uint16_t><<<(unsigned)blocks, 256, 0, s>>>(a, kept, row / 2), note_launch();
     return cudaGetLastError();
 }
 

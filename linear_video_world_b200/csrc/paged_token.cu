@@ -41,7 +41,7 @@ constexpr uint32_t SM_ABORT = SM_PLACE + 32;
 std::atomic<unsigned long long> g_shared{0};
 constexpr size_t SMEM_BYTES = SM_ABORT + 16;
 static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two blocks per SM");
-constexpr int KEYS = 2048;                              // keys per block of the second kernel
+constexpr int KEYS = 4096;                              // keys per block of the second kernel
 
 struct Params {
     Line line;
@@ -425,18 +425,42 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
     }
     if (!p.w_out) return;
     const Span u = ro.n > 0 ? Span{span_of(ro, 0, p.line.mask).lo, span_of(ro, ro.n - 1, p.line.mask).hi} : Span{0, 0};
-    for (int k = k0 + threadIdx.x; k < min(k0 + KEYS, ro.kv); k += JT) {
-        float t = 0.f;
-        if (k >= u.lo && k < u.hi)
+    // four keys a thread: the capacity is a multiple of 16, so neither rows nor words straddle
+    const long head = (long)blockIdx.y * p.line.cap;
+#pragma unroll 2
+    for (int k = k0 + 4 * threadIdx.x; k < min(k0 + KEYS, ro.kv); k += 4 * JT) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+        if (k + 3 >= u.lo && k < u.hi) {
+#pragma unroll 4
             for (int r = 0; r < p.R; ++r) {
                 if (frem(r, p.line.byL) >= ro.n) continue;
-                const float s = p.scores[(row0 + r) * p.line.cap + k];
-                // a row that does not see the key stored -inf (a row that sees none: no NaN from -inf + inf)
-                if (s != -INFINITY) t = fmaf(tc::ex2(s - s_ml[r].x), s_ml[r].y, t);
+                const float4 y = *reinterpret_cast<const float4 *>(p.scores + (row0 + r) * p.line.cap + k);
+                const float s[4] = {y.x, y.y, y.z, y.w};
+                // what no row of the chunk sees was not stored; a key that this row does not see is
+                // -inf (a row that sees none: no NaN from -inf + inf)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (k + j >= u.lo && k + j < u.hi && s[j] != -INFINITY) t[j] = fmaf(tc::ex2(s[j] - s_ml[r].x), s_ml[r].y, t[j]);
             }
-        const long at = (long)blockIdx.y * p.line.cap + k;
-        if (p.w_in && k < ro.h) t = fmaf(p.decay, p.w_in[at], t);
-        p.w_out[at] = t;
+        }
+        float old[4] = {0.f, 0.f, 0.f, 0.f};
+        if (p.w_in && k < ro.h) {
+            if (k + 3 < ro.h && !((uintptr_t)p.w_in & 15u)) {
+                const float4 y = *reinterpret_cast<const float4 *>(p.w_in + head + k);
+                old[0] = y.x; old[1] = y.y; old[2] = y.z; old[3] = y.w;
+            } else {
+                for (int j = 0; j < 4; ++j)
+                    if (k + j < ro.h) old[j] = p.w_in[head + k + j];
+            }
+        }
+        for (int j = 0; j < 4; ++j)
+            if (p.w_in && k + j < ro.h) t[j] = fmaf(p.decay, old[j], t[j]);
+        if (k + 3 < ro.kv && !((uintptr_t)p.w_out & 15u)) {
+            *reinterpret_cast<float4 *>(p.w_out + head + k) = make_float4(t[0], t[1], t[2], t[3]);
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (k + j < ro.kv) p.w_out[head + k + j] = t[j];
+        }
     }
 }
 
