@@ -1,20 +1,23 @@
 // Eviction from a paged cache by accumulated attention weight: choose the positions to keep, then
 // copy their keys, values and weights to the destination's pages.
 //
-// Choice, one block per (rollout, key head): of the middle positions the `take` largest weights,
-// found by a radix select over order-preserving 32-bit keys of the weights (three passes of 11, 11
-// and 10 bits, from the top: each counts the digits of the keys that still match the threshold's
-// prefix). The keys are read from memory once and kept in shared memory (up to KEEP of them; longer
-// rollouts read them again). A warp whose keys share a digit adds them with one atomic: unused
-// positions have equal weights. Then each warp takes a run of positions and numbers the kept ones
-// by ballots, after a scan over the warps' counts (above the threshold; equal to it, of which the
-// first `left` stay).
+// Choice, a cluster of one to eight blocks per (rollout, key head), as many as still fill the GPU
+// (64 rows of 20000 to 32760 positions: 38 us with one block each, CHOICE_TIME with two): of the
+// middle positions the `take` largest weights, found by a radix select over order-preserving 32-bit
+// keys of the weights (three passes of 11, 11 and 10 bits, from the top: each counts the digits of
+// the keys that still match the threshold's prefix; the blocks read one another's counts). Each
+// block has a run of the positions; it reads their keys from memory once and keeps them in shared
+// memory (up to KEEP; longer runs are read again). A warp whose keys share a digit adds them with one
+// atomic: unused positions have equal weights. Then each warp takes a run of its block's positions
+// and numbers the kept ones by ballots, after a scan over the blocks' and warps' counts (above the
+// threshold; equal to it, of which the first `left` stay).
 // Copy: a warp takes eight kept positions, all their 16-byte words of K and V in flight together.
 // Bound by HBM.
 #include "hlta_internal.cuh"
 #include "paged.cuh"
 
 #include <algorithm>
+#include <cooperative_groups.h>
 #include <math.h>
 
 namespace hlta {
@@ -39,30 +42,36 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
 {
     extern __shared__ uint32_t sm[];
     uint32_t *hist = sm, *keys = sm + BINS;
-    __shared__ int warp_n[SW], warp_e[SW];
+    __shared__ int warp_n[SW], warp_e[SW], block_n[2];
     __shared__ uint32_t s_digit;
     __shared__ int s_left;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.x % a.c.H, b = blockIdx.x / a.c.H;
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int nblk = (int)cluster.num_blocks(), blk = (int)cluster.block_rank();
+    const long bh = blockIdx.x / nblk;
+    const int h = (int)(bh % a.c.H), b = (int)(bh / a.c.H), tid = blk * ST + (int)threadIdx.x;
     const int cap = a.c.max_pages << a.c.page_log2;
     const int kv = a.c.kv_lens[b];
     const int n = max(0, min(kv, cap));
-    if (n != kv && threadIdx.x == 0) atomicOr(a.c.err, DEVERR_TABLE);
-    int *out = kept + (long)blockIdx.x * a.budget;
-    if (h == 0 && threadIdx.x == 0) a.new_lens[b] = min(n, a.budget);
-    if (n <= a.budget) {
-        for (int i = threadIdx.x; i < a.budget; i += ST) out[i] = i < n ? i : -1;
+    if (n != kv && tid == 0) atomicOr(a.c.err, DEVERR_TABLE);
+    int *out = kept + bh * a.budget;
+    if (h == 0 && tid == 0) a.new_lens[b] = min(n, a.budget);
+    if (n <= a.budget) {                    // the whole cluster alike
+        for (int i = tid; i < a.budget; i += nblk * ST) out[i] = i < n ? i : -1;
         return;
     }
-    const float *w = a.weights + (long)blockIdx.x * cap;
-    const int lo = a.sink, m = n - a.recent - a.sink, take = a.budget - a.sink - a.recent;
+    const int middle = n - a.recent - a.sink, take = a.budget - a.sink - a.recent;
+    // this block's run of the middle positions: [lo, lo + m)
+    const int first = (int)((long)middle * blk / nblk), m = (int)((long)middle * (blk + 1) / nblk) - first, lo = a.sink + first;
+    const float *w = a.weights + bh * cap;
     const bool held = m <= KEEP;
     if (held && take > 0) {
 #pragma unroll 8
         for (int i = threadIdx.x; i < m; i += ST) keys[i] = key_of(w[lo + i]);
     }
     auto key = [&](int i) { return held ? keys[i] : key_of(w[lo + i]); };
-    // the take-th largest key of the m middle ones (take < m since n > budget)
+    // the take-th largest key of the middle ones (take < middle since n > budget)
     uint32_t prefix = 0, mask = 0;
     int left = take;
     if (take > 0) {
@@ -82,10 +91,15 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
                     atomicAdd(&hist[d], 1u);
                 }
             }
-            __syncthreads();
+            cluster.sync();
             // the digit at which the count from the top reaches `left`: thread t owns digits
             // BINS - 1 - 2 t and BINS - 2 - 2 t
-            const int c0 = (int)hist[BINS - 1 - 2 * threadIdx.x], c1 = (int)hist[BINS - 2 - 2 * threadIdx.x];
+            int c0 = 0, c1 = 0;
+            for (int v = 0; v < nblk; ++v) {
+                const uint32_t *theirs = cluster.map_shared_rank(hist, v);
+                c0 += (int)theirs[BINS - 1 - 2 * threadIdx.x];
+                c1 += (int)theirs[BINS - 2 - 2 * threadIdx.x];
+            }
             int x = c0 + c1;
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -101,7 +115,7 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
                 s_digit = (uint32_t)(BINS - 1 - 2 * (int)threadIdx.x - (second ? 1 : 0));
                 s_left = left - before - (second ? c0 : 0);
             }
-            __syncthreads();
+            cluster.sync();                     // and the counts may be cleared
             prefix |= s_digit << shift;
             mask |= ((1u << width) - 1u) << shift;
             left = s_left;
@@ -110,8 +124,8 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
         prefix = 0xffffffffu;       // nothing is above it, and none of its equals stay
         left = 0;
     }
-    for (int i = threadIdx.x; i < a.sink; i += ST) out[i] = i;
-    for (int i = threadIdx.x; i < a.recent; i += ST) out[a.sink + take + i] = n - a.recent + i;
+    for (int i = tid; i < a.sink; i += nblk * ST) out[i] = i;
+    for (int i = tid; i < a.recent; i += nblk * ST) out[a.sink + take + i] = n - a.recent + i;
     if (take == 0) return;
     // number the kept middle positions in order: each warp a run of them
     const int run = ((m + SW - 1) / SW + 31) & ~31, i_lo = min(m, warp * run), i_hi = min(m, i_lo + run);
@@ -128,10 +142,21 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
     }
     __syncthreads();
     above = equal = 0;
-    for (int v = 0; v < warp; ++v) {
-        above += warp_n[v];
-        equal += warp_e[v];
+    for (int v = 0; v < SW; ++v) {
+        above += v < warp ? warp_n[v] : 0;
+        equal += v < warp ? warp_e[v] : 0;
     }
+    if (threadIdx.x == ST - 1) {
+        block_n[0] = above + warp_n[SW - 1];
+        block_n[1] = equal + warp_e[SW - 1];
+    }
+    cluster.sync();
+    for (int v = 0; v < blk; ++v) {
+        const int *theirs = cluster.map_shared_rank(block_n, v);
+        above += theirs[0];
+        equal += theirs[1];
+    }
+    cluster.sync();                             // no block ends while another reads its counts
     for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
         const int i = i0 + lane;
         const uint32_t k = i < i_hi ? key(i) : 0u;
@@ -203,11 +228,26 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, bool bf16, cudaStream_t 
     const long bh = (long)a.B * a.c.H;
     if (bh == 0) return cudaSuccess;
     const long blocks = (bh * ((a.budget + CPW - 1) / CPW) + 7) / 8;
-    if (bh > 0x7fffffffL || blocks > 0x7fffffffL) return cudaErrorNotSupported;
+    if (bh > 0x0fffffffL || blocks > 0x7fffffffL) return cudaErrorNotSupported;
     int *kept = a.kept ? a.kept : (int *)a.ws;
     cudaError_t e = allow_shared((const void *)evict_choose_kernel, CHOOSE_SMEM, g_shared);
     if (e != cudaSuccess) return e;
-    evict_choose_kernel<<<(unsigned)bh, ST, CHOOSE_SMEM, s>>>(a, kept), note_launch();
+    // blocks per row: while they fit the SMs, and none has fewer positions than threads
+    int nblk = 1;
+    while (nblk < 8 && bh * nblk * 2 <= device_sms() && (long)(a.c.max_pages << a.c.page_log2) >= 2L * nblk * ST) nblk *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(bh * nblk));
+    cfg.blockDim = dim3(ST);
+    cfg.dynamicSmemBytes = CHOOSE_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)nblk;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, evict_choose_kernel, a, kept)) != cudaSuccess) return e;
+    note_launch();
     const int row = a.c.d * (bf16 ? 2 : 4);
     if (row % 16 == 0) evict_copy_kernel<uint4><<<(unsigned)blocks, 256, 0, s>>>(a, kept, row / 16), note_launch();
     else evict_copy_kernel<uint16_t><<<(unsigned)blocks, 256, 0, s>>>(a, kept, row / 2), note_launch();

@@ -305,12 +305,18 @@ Turns turns_of(const hlta_rope_axes_t *sp, int inverse)
     if (!sp) return t;
     int j = 0;
     const int P = sp->pairs[0] + sp->pairs[1] + sp->pairs[2];
-    for (int a = 0; a < 3; ++a)
-        for (int i = 0; i < sp->pairs[a]; ++i, ++j) {
-            const long double power = sp->shared_freq ? (long double)j / P : (long double)i / sp->pairs[a];
-            t.f[j] = (double)(powl((long double)sp->base, -power) / 6.283185307179586476925287L);
+    // a ladder by repeated products in extended precision: 64 roundings of 2^-64 stay below the one
+    // to double, and cost a fraction of as many powers
+    long double f = 1.L;
+    for (int a = 0; a < 3; ++a) {
+        if (!sp->pairs[a]) continue;
+        const long double step = powl((long double)sp->base, -1.L / (sp->shared_freq ? P : sp->pairs[a]));
+        if (!sp->shared_freq) f = 1.L;
+        for (int i = 0; i < sp->pairs[a]; ++i, ++j, f *= step) {
+            t.f[j] = (double)(f / 6.283185307179586476925287L);
             t.axis[j] = (unsigned char)a;
         }
+    }
     t.P = P;
     t.layout = sp->layout;
     t.gh = sp->pos ? 1 : sp->grid_h;
