@@ -95,16 +95,17 @@ __device__ __forceinline__ int page_of(const PagedKV &c, int b, int p)
 // last.
 struct Line {
     int B, H, L, cap, gs, ngang, passes;
+    int steps;                      // places on the line per key tile (1; more where a tile's work is cut too)
     FastDiv byL;
     Mask mask;
     const int *kv_lens, *new_lens;
 };
-__host__ inline Line line_of(const PagedAttnArgs &a, int gs, int ngang, int passes)
+__host__ inline Line line_of(const PagedAttnArgs &a, int gs, int ngang, int passes, int steps = 1)
 {
     Line p;
     p.B = a.B; p.H = a.c.H; p.L = (int)a.L;
     p.cap = a.c.max_pages << a.c.page_log2;
-    p.gs = gs; p.ngang = ngang; p.passes = passes;
+    p.gs = gs; p.ngang = ngang; p.passes = passes; p.steps = steps;
     p.byL = fast_div((unsigned)(a.L > 0 ? a.L : 1));
     p.mask = mask_of(a.N, a.w);
     p.kv_lens = a.c.kv_lens; p.new_lens = a.new_lens;
@@ -119,7 +120,7 @@ __device__ __forceinline__ long long quot(long long a, long long b)
 template <int TK>
 struct Tiles {
     Roll r;
-    int t0, T;                      // first key tile; tiles
+    int t0, T;                      // first key tile; places (tiles x steps)
 };
 template <int TK>
 __device__ __forceinline__ Tiles<TK> tiles_of(const Line &p, int b)
@@ -131,7 +132,7 @@ __device__ __forceinline__ Tiles<TK> tiles_of(const Line &p, int b)
         const int lo = span_of(x.r, 0, p.mask).lo, hi = span_of(x.r, x.r.n - 1, p.mask).hi;
         if (hi > lo) {
             x.t0 = lo / TK;
-            x.T = (hi + TK - 1) / TK - x.t0;
+            x.T = ((hi + TK - 1) / TK - x.t0) * p.steps;
         }
     }
     return x;
@@ -192,7 +193,7 @@ __device__ __forceinline__ Place place_of(const Line &p, int g)
     return c;
 }
 
-// The piece at c (key tiles [ta, tb) of its head, `whole` when that is all of them), and c moved
+// The piece at c (key tiles, or steps, [ta, tb) of its head, `whole` when that is all of them), and c moved
 // behind it. False at the end of the range.
 template <int TK>
 struct Piece {
@@ -216,7 +217,7 @@ __device__ __forceinline__ bool next_piece(const Line &p, Place &c, Piece<TK> &o
     o.b = c.b;
     o.h = c.h;
     const int take = min(c.left, o.x.T - c.t);
-    o.ta = o.x.t0 + c.t;
+    o.ta = o.x.t0 * p.steps + c.t;
     o.tb = o.ta + take;
     o.whole = take == o.x.T;
     c.left -= take;
@@ -231,25 +232,30 @@ __device__ __forceinline__ bool next_piece(const Line &p, Place &c, Piece<TK> &o
     return true;
 }
 
-// The gangs that hold pieces of one head's keys in one pass: g0 .. g1 (one warp).
+// The gangs that hold pieces of places [a, a + n) of the line (one warp): g0 .. g1.
 struct Holders {
-    int g0, g1, slot0, T;           // slot of g0's piece; the others lie in slot 0
+    int g0, g1, slot0, T;           // slot of g0's piece (the others lie in slot 0); places
 };
-template <int TK>
-__device__ __forceinline__ Holders holders_of(const Line &p, int pass, int b, int h)
+__device__ __forceinline__ Holders holders_at(const Line &p, long long W, long long a, int n)
 {
-    const long long per = tiles_before<TK>(p, p.B) * p.H, W = per * p.passes;
     Holders o;
-    o.T = tiles_of<TK>(p, b).T;
+    o.T = n;
     o.g0 = o.g1 = o.slot0 = 0;
-    const long long a = per * pass + tiles_before<TK>(p, b) * p.H + (long long)h * o.T;
-    if (o.T == 0) return o;
+    if (n == 0) return o;
     // gang g holds [W g / ng, W (g + 1) / ng), rounded down
     const long long ng = W < p.ngang ? W : p.ngang;
     o.g0 = (int)quot((a + 1) * ng - 1, W);
-    o.g1 = (int)quot((a + o.T) * ng - 1, W);
+    o.g1 = (int)quot((a + n) * ng - 1, W);
     o.slot0 = quot(W * o.g0, ng) == a ? 0 : 1;
     return o;
+}
+// ... of one head's keys in one pass.
+template <int TK>
+__device__ __forceinline__ Holders holders_of(const Line &p, int pass, int b, int h)
+{
+    const long long per = tiles_before<TK>(p, p.B) * p.H;
+    const int T = tiles_of<TK>(p, b).T;
+    return holders_at(p, per * p.passes, per * pass + tiles_before<TK>(p, b) * p.H + (long long)h * T, T);
 }
 
 }  // namespace paged

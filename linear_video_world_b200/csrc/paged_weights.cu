@@ -7,8 +7,12 @@
 // exchange between lanes. A block owns a key tile of 128 and streams the rows past it.
 // Bound by the exponentials: 1024 cycles (16 a cycle) per 128 x 128 scores against 512 of products.
 // Roles: warps 0-3 and 4-7 sum every other row tile; warp 8 copies K tiles (two buffers; a lane per
-// page) and row tiles (a ring of four) by TMA; warp 9 issues the products into four buffers of tensor
-// memory. Equal shares of the line of key tiles (paged.cuh, one block a gang).
+// page) and row tiles (a ring of four) by TMA and lays the rows' log-sum-exp and spans beside them;
+// warp 9 issues the products into four buffers of tensor memory. Equal shares of the line of (key
+// tile, row tile) steps (paged.cuh, one block a gang): the sums of a key tile that is cut between
+// blocks go to the workspace and a second kernel joins them in the order of the blocks. (Whole key
+// tiles per block: 312 of them on 148 SMs took three rounds for two; with the log-sum-exp fetched by
+// the summing warps themselves 61 us, now WEIGHTS_TIME.)
 #include "hlta_internal.cuh"
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
@@ -26,8 +30,9 @@ constexpr int BN = 128, RT = 128, D = 128;              // keys per tile, rows p
 constexpr int THREADS = 320, WARP_TMA = 8, WARP_MMA = 9;
 constexpr uint32_t HALF = 128 * 128, TILE = 2 * HALF;
 constexpr int NQ = 4, NK = 2, NS = 4;
-constexpr uint32_t SM_K = 0, SM_Q = NK * TILE, SM_Z = SM_Q + NQ * TILE;         // z: [group][128 rows]
-constexpr uint32_t SM_SPAN = SM_Z + 2 * RT * 4, SM_SUM = SM_SPAN + 2 * RT * 8;  // spans; sums of group 1
+static_assert(NQ == NS, "a row tile's ring slot and its buffer of products have the same number");
+constexpr uint32_t SM_K = 0, SM_Q = NK * TILE, SM_Z = SM_Q + NQ * TILE;         // z: [slot][128 rows]
+constexpr uint32_t SM_SPAN = SM_Z + NQ * RT * 4, SM_SUM = SM_SPAN + NQ * RT * 8;    // spans; sums of group 1
 constexpr uint32_t SM_BAR = SM_SUM + BN * 4;
 enum { B_KFULL, B_KEMPTY = B_KFULL + NK, B_QFULL = B_KEMPTY + NK, B_QEMPTY = B_QFULL + NQ, B_SFULL = B_QEMPTY + NQ, B_SFREE = B_SFULL + NS, NBARS = B_SFREE + NS };
 constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS, SM_OK = SM_PLACE + 32, SM_TMEM = SM_OK + 32, SM_ABORT = SM_TMEM + 4;
@@ -42,6 +47,7 @@ struct Params {
     float sl2;
     const float *lse, *w_in;
     float *w_out, decay;
+    float *part;                    // [block][2][128 keys]
 };
 
 // the keys that row tile rt's live rows see, and whether all of its rows are live and see [p0, p0 + BN)
@@ -84,6 +90,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
     auto BAR = [&](int i) { return sbase + SM_BAR + 8u * (uint32_t)i; };
     volatile int *abort_flag = (volatile int *)(smem + SM_ABORT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;");      // the second kernel may be set up meanwhile
     if (sbase & 1023u) {                    // not seen: the attribute asks for it
         if (threadIdx.x == 0) atomicOr(p.c.err, DEVERR_ATTN_WAIT);
         return;
@@ -118,7 +125,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
     const uint32_t tmem = *(uint32_t *)(smem + SM_TMEM);
     Place at = *(Place *)(smem + SM_PLACE);
     Piece<BN> x;
-    const int nrt = (p.R + RT - 1) / RT;
+    const int nrt = p.line.steps;
     auto wait_bar = [&](uint32_t bar, uint32_t parity) -> bool {
         return mbar_try(bar, parity) || mbar_wait(bar, parity, abort_flag, p.c.err, DEVERR_ATTN_WAIT);
     };
@@ -131,7 +138,9 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
             const Roll &ro = x.x.r;
             const Span u{span_of(ro, 0, p.line.mask).lo, span_of(ro, ro.n - 1, p.line.mask).hi};
             const long row0 = (long)(x.b * p.c.H + x.h) * p.R;
-            for (int t = x.ta; ok && t < x.tb; ++t) {
+            for (int st = x.ta; ok && st < x.tb;) {
+                const int t = st / nrt, rt0 = st - t * nrt, rt1 = min(nrt, rt0 + x.tb - st);
+                st += rt1 - rt0;
                 const int p0 = t * BN + lane * psz;
                 const int pg = lane < npg && p0 < u.hi && p0 + psz > u.lo ? page_of(p.c, x.b, max(p0, u.lo)) : -1;
                 const int ks = (int)(nk % NK);
@@ -148,19 +157,39 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
                     tma_load_2d(dst + HALF, &tk, 64, row, BAR(B_KFULL + ks));
                 }
                 ++nk;
-                if (lane == 0) {
-                    for (int rt = 0; ok && rt < nrt; ++rt) {
-                        if (!row_tile(p, ro, rt, t * BN).any) continue;
-                        const int qs = (int)(nq % NQ);
-                        if (nq >= NQ && !(ok = wait_bar(BAR(B_QEMPTY + qs), (uint32_t)(nq / NQ + 1) & 1u))) break;
+                for (int rt = rt0; rt < rt1; ++rt) {
+                    const RowTile k = row_tile(p, ro, rt, t * BN);
+                    if (!k.any) continue;
+                    // the rows' log-sum-exp (log2, negative) and spans; rows that are none see nothing
+                    float z[4];
+                    Span v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = rt * RT + 4 * lane + j, i = frem(r, p.line.byL);
+                        const bool live = r < p.R && i < ro.n;
+                        z[j] = live ? p.lse[row0 + r] * -1.4426950408889634f : 0.f;
+                        v[j] = live && !k.full ? span_of(ro, i, p.line.mask) : Span{0, 0};
+                    }
+                    const int qs = (int)(nq % NQ);
+                    // the slot's product is done, and its scores, log-sum-exp and spans were read
+                    if (lane == 0 && nq >= NQ)
+                        w = wait_bar(BAR(B_QEMPTY + qs), (uint32_t)(nq / NQ + 1) & 1u) && wait_bar(BAR(B_SFREE + qs), (uint32_t)(nq / NQ + 1) & 1u);
+                    if (!(ok = __shfl_sync(0xffffffffu, w, 0))) break;
+                    *(float4 *)(smem + SM_Z + (qs * RT + 4 * lane) * 4) = make_float4(z[0], z[1], z[2], z[3]);
+                    if (!k.full) {
+                        int4 *d = (int4 *)(smem + SM_SPAN + (qs * RT + 4 * lane) * 8);
+                        d[0] = make_int4(v[0].lo, v[0].hi, v[1].lo, v[1].hi);
+                        d[1] = make_int4(v[2].lo, v[2].hi, v[3].lo, v[3].hi);
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
                         mbar_expect_tx(BAR(B_QFULL + qs), TILE);
                         const int row = (int)(row0 + rt * RT);
                         tma_load_2d(sbase + SM_Q + (uint32_t)qs * TILE, &tq, 0, row, BAR(B_QFULL + qs));
                         tma_load_2d(sbase + SM_Q + (uint32_t)qs * TILE + HALF, &tq, 64, row, BAR(B_QFULL + qs));
-                        ++nq;
                     }
+                    ++nq;
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
         }
         if (lane == 0 && *abort_flag) {
@@ -178,10 +207,12 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
             uint32_t nk = 0, nq = 0;
             bool ok = true;
             while (ok && next_piece<BN>(p.line, at, x)) {
-                for (int t = x.ta; ok && t < x.tb; ++t) {
+                for (int st = x.ta; ok && st < x.tb;) {
+                    const int t = st / nrt, rt0 = st - t * nrt, rt1 = min(nrt, rt0 + x.tb - st);
+                    st += rt1 - rt0;
                     const uint32_t ks = nk % NK;
                     if (!(ok = wait_bar(BAR(B_KFULL + ks), (nk / NK) & 1u))) break;
-                    for (int rt = 0; rt < nrt; ++rt) {
+                    for (int rt = rt0; rt < rt1; ++rt) {
                         if (!row_tile(p, x.x.r, rt, t * BN).any) continue;
                         const uint32_t qs = nq % NQ, sb = nq % NS;
                         if (!(ok = wait_bar(BAR(B_QFULL + qs), (nq / NQ) & 1u))) break;
@@ -206,47 +237,35 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
     } else {
         const int grp = warp >> 2, row = (warp & 3) * 32 + lane;        // the group; this thread's key
         const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        float *z = (float *)(smem + SM_Z) + grp * RT;
-        int2 *spans = (int2 *)(smem + SM_SPAN) + grp * RT;
         float *sums = (float *)(smem + SM_SUM);
         volatile int *sok = (volatile int *)(smem + SM_OK);
-        const int grp_bar = 1 + grp;
         uint32_t nq = 0;
+        int tiles = 0;                      // key tiles so far: a cut one is the first or the last
         bool ok = true;
         while (next_piece<BN>(p.line, at, x)) {
             const Roll ro = x.x.r;
             const long head = (long)x.b * p.c.H + x.h;
-            for (int t = x.ta; ok && t < x.tb; ++t) {
+            for (int st = x.ta; ok && st < x.tb;) {
+                const int t = st / nrt, rt0 = st - t * nrt, rt1 = min(nrt, rt0 + x.tb - st);
+                st += rt1 - rt0;
                 const int p0 = t * BN, key = p0 + row;
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                for (int rt = 0; rt < nrt; ++rt) {
+                for (int rt = rt0; rt < rt1; ++rt) {
                     const RowTile k = row_tile(p, ro, rt, p0);
                     if (!k.any) continue;
                     const uint32_t sb = nq % NS, par = (nq / NS) & 1u;
                     const bool mine = (int)(nq & 1) == grp;
                     ++nq;
                     if (!mine) continue;
-                    // the row tile's log-sum-exp (log2) and spans; rows that are none see nothing
-                    const int r = rt * RT + row, i = frem(r, p.line.byL);
-                    const bool live = r < p.R && i < ro.n;
-                    asm volatile("bar.sync %0, 128;" ::"r"(grp_bar) : "memory");       // the previous one's were read
-                    z[row] = live ? p.lse[head * p.R + r] * -1.4426950408889634f : 0.f;
-                    if (!k.full) {
-                        const Span v = live ? span_of(ro, i, p.line.mask) : Span{0, 0};
-                        spans[row] = make_int2(v.lo, v.hi);
-                    }
-                    asm volatile("bar.sync %0, 128;" ::"r"(grp_bar) : "memory");
-                    ok = __all_sync(0xffffffffu, ok && wait_bar(BAR(B_SFULL + sb), par));
+                    ok = __all_sync(0xffffffffu, ok && wait_bar(BAR(B_QFULL + sb), par) && wait_bar(BAR(B_SFULL + sb), par));
                     tc::fence_after_sync();
+                    const float *z = (const float *)(smem + SM_Z) + sb * RT;
+                    const int2 *spans = (const int2 *)(smem + SM_SPAN) + sb * RT;
                     const float2 sl = make_float2(p.sl2, p.sl2);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t sv[64];
                         tc::tmem_ld64(tlane + 128u * sb + 64u * h, sv);
-                        if (h == 1) {
-                            tc::fence_before_sync();
-                            mbar_arrive(BAR(B_SFREE + sb));
-                        }
                         if (k.full) {
 #pragma unroll
                             for (int c = 0; c < 64; c += 4) {
@@ -263,10 +282,12 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
                             for (int c = 0; c < 64; ++c) {
                                 const int2 v = spans[64 * h + c];
                                 const float e = tc::ex2(fmaf(__uint_as_float(sv[c]), p.sl2, z[64 * h + c]));
-                                acc[0].x += key >= v.x && key < v.y ? e : 0.f;
+                                acc[c & 1].x += key >= v.x && key < v.y ? e : 0.f;
                             }
                         }
                     }
+                    tc::fence_before_sync();
+                    mbar_arrive(BAR(B_SFREE + sb));
                 }
                 // group 1's sums join group 0's; both groups give up together
                 const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
@@ -274,12 +295,18 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
                 if (lane == 0) sok[warp] = ok;
                 asm volatile("bar.sync 3, 256;" ::: "memory");
                 for (int w = 0; w < 8; ++w) ok = ok && sok[w];
-                if (ok && grp == 0 && key < ro.kv) {
-                    const long o = head * p.line.cap + key;
+                const bool whole = rt0 == 0 && rt1 == nrt;
+                if (ok && grp == 0) {
                     float s = sum + sums[row];
-                    if (p.w_in && key < ro.h) s = fmaf(p.decay, p.w_in[o], s);
-                    p.w_out[o] = s;
+                    if (!whole) {
+                        p.part[((long)blockIdx.x * 2 + (tiles == 0 ? 0 : 1)) * BN + row] = s;
+                    } else if (key < ro.kv) {
+                        const long o = head * p.line.cap + key;
+                        if (p.w_in && key < ro.h) s = fmaf(p.decay, p.w_in[o], s);
+                        p.w_out[o] = s;
+                    }
                 }
+                ++tiles;
                 asm volatile("bar.sync 3, 256;" ::: "memory");
             }
             if (!ok) break;
@@ -295,17 +322,31 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
     }
 }
 
-// The positions of no key tile (before the window; every position of a rollout without new tokens):
-// w_out = decay w_in.
-__global__ void __launch_bounds__(256) paged_decay_kernel(const __grid_constant__ Params p)
+// Joins the sums of key tiles that were cut between blocks, in the order of the blocks, and gives the
+// positions of no key tile (before the window; every position of a rollout without new tokens)
+// decay w_in. A block per 128 positions.
+__global__ void __launch_bounds__(BN) paged_weights_join_kernel(const __grid_constant__ Params p)
 {
     const int h = blockIdx.y % p.c.H, b = blockIdx.y / p.c.H;
-    (void)h;
+    const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
+    const int t = blockIdx.x, k = t * BN + threadIdx.x;
+    if (t * BN >= ro.kv) return;
     const Tiles<BN> x = tiles_of<BN>(p.line, b);
-    const int k = blockIdx.x * 256 + threadIdx.x;
-    if (k >= x.r.kv || (k >= x.t0 * BN && k < (x.t0 + x.T) * BN)) return;
+    const int nt = x.T / p.line.steps;
+    float s = 0.f;
+    if (t >= x.t0 && t < x.t0 + nt) {
+        const long long W = tiles_before<BN>(p.line, p.line.B) * p.line.H;
+        const Holders g = holders_at(p.line, W, tiles_before<BN>(p.line, b) * p.line.H + (long long)h * x.T + (long long)(t - x.t0) * p.line.steps, p.line.steps);
+        if (g.g0 == g.g1) return;
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's results from here on
+        for (int i = g.g0; i <= g.g1; ++i) s += p.part[((long)i * 2 + (i == g.g0 ? g.slot0 : 0)) * BN + threadIdx.x];
+    } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+    if (k >= ro.kv) return;
     const long at = (long)blockIdx.y * p.line.cap + k;
-    p.w_out[at] = p.w_in && k < x.r.h ? p.decay * p.w_in[at] : 0.f;
+    if (p.w_in && k < ro.h) s = fmaf(p.decay, p.w_in[at], s);
+    p.w_out[at] = s;
 }
 
 }  // namespace
@@ -322,13 +363,26 @@ cudaError_t launch_paged_weights_tc(const PagedAttnArgs &a, cudaStream_t s)
     Params p;
     p.c = a.c;
     p.R = (int)R;
-    p.line = line_of(a, 1, sms, 1);
+    const int nrt = (int)((R + RT - 1) / RT);
+    if ((long)((a.c.max_pages << a.c.page_log2) / BN + 2) * nrt >= (1L << 30)) return cudaErrorNotSupported;
+    p.line = line_of(a, 1, sms, 1, nrt);
+    p.part = (float *)a.ws;         // the attention's pieces are joined by now
     p.sl2 = a.sl2;
     p.lse = a.lse; p.w_in = a.w_in; p.w_out = a.w_out; p.decay = a.decay;
-    if (a.w > 0 || a.new_lens) paged_decay_kernel<<<dim3((unsigned)((p.line.cap + 255) / 256), (unsigned)(a.B * a.c.H)), 256, 0, s>>>(p), note_launch();
     if ((e = allow_shared((const void *)paged_weights_tc_kernel, SMEM_BYTES, g_shared)) != cudaSuccess) return e;
     paged_weights_tc_kernel<<<sms, THREADS, SMEM_BYTES, s>>>(mq, mk, p), note_launch();
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.line.cap + BN - 1) / BN), (unsigned)(a.B * a.c.H));
+    cfg.blockDim = dim3(BN);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_weights_join_kernel, p), note_launch();
+    return e;
 }
 
 }  // namespace hlta
