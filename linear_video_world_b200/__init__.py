@@ -120,7 +120,7 @@ def _stream(stream):
 
 
 def _dt(t) -> int:
-    import torch
+    torch = _th()
     if t.dtype == torch.bfloat16:
         return HLTA_BF16
     if t.dtype == torch.float32:
@@ -313,31 +313,32 @@ def hlta_gdn_chunk_bwd(q, k, v, a, b, S0, dO, dS_final, dq, dk, dv, da, db, dS0,
                                    _stream(stream)))
 
 
-def _need_dtype(dtype, *named):
-    for t, n in named:
-        if t is not None and t.dtype != dtype:
-            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {dtype} (got {t.dtype})")
+# The serving calls (rotary axes, paged cache, recurrent gated delta rule) take a few microseconds
+# on the GPU, so their checks are one pass over the tensors and torch is looked up once.
+_torch = None
 
 
-def _need_shape(t, n, *shape):
-    if t is not None and t.shape != shape:
-        raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {list(shape)} (got {list(t.shape)})")
+def _th():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
-def _device():
-    """The current CUDA device, -1 without one (a host tensor's device index, too, is refused)."""
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
-
-
-def _addresses(dev, *named):
-    """Addresses of the serving calls' tensors (None: a null pointer), each contiguous and on
-    device `dev`, where their kernels are launched."""
+def _args(th, *wanted):
+    """Addresses of (tensor, name, dtype, shape) tuples (None: a null pointer, any dtype or shape):
+    each contiguous, on the current device (where the kernels are launched), as described."""
+    dev = th.cuda.current_device() if th.cuda.is_initialized() else -2
     out = []
-    for t, n in named:
+    for t, n, dtype, shape in wanted:
         if t is None:
             out.append(None)
             continue
+        if dtype is not None and t.dtype != dtype:
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {dtype} (got {t.dtype})")
+        if shape is not None and t.shape != shape:
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {list(shape)} (got {list(t.shape)})")
         if t.get_device() != dev or not t.is_contiguous():
             if not t.is_cuda or not t.is_contiguous():
                 raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be a contiguous CUDA tensor")
@@ -346,60 +347,50 @@ def _addresses(dev, *named):
     return out
 
 
-def _stream_address(stream):
-    import torch
+def _stream_address(th, stream):
     if stream is None:
         # the address alone: a Stream object costs as much as a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return th._C._cuda_getCurrentRawStream(th.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def rope_axes_spec(pairs, grid=None, pos=None, t0=None, base=10000.0, halves=False,
-                   shared_freq=False):
+                   shared_freq=False, B=None, L=None):
     """hlta_rope_axes_t from its parts: pairs = (time, height, width); grid = (height, width) of
     a frame, or pos [B, L, 3] int32; t0 [B] int32, the first frame's index of each rollout."""
     if (grid is None) == (pos is None):
         raise HltaError(HLTA_ERR_INVALID_ARG, "give either a grid or positions")
     if pos is not None and t0 is not None:
         raise HltaError(HLTA_ERR_INVALID_ARG, "t0 goes with a grid")
-    spec = hlta_rope_axes_t()
-    spec.pairs[:] = pairs
-    spec.layout, spec.shared_freq, spec.base = halves, shared_freq, base
-    spec.grid_h, spec.grid_w = grid if grid is not None else (1, 1)
+    gh, gw = (1, 1) if grid is None else grid
+    at_pos = at_t0 = None
     if pos is not None or t0 is not None:
-        _need_dtype(_int32(), (pos, "pos"), (t0, "t0"))
-        spec.pos, spec.t0 = _addresses(_device(), (pos, "pos"), (t0, "t0"))
-    return spec
-
-
-def _int32():
-    import torch
-    return torch.int32
-
-
-def _float32():
-    import torch
-    return torch.float32
+        th = _th()
+        at_pos, at_t0 = _args(th, (pos, "pos", th.int32, None if B is None else (B, L, 3)),
+                              (t0, "t0", th.int32, None if B is None else (B,)))
+    return hlta_rope_axes_t((ctypes.c_int * 3)(*pairs), halves, shared_freq, gh, gw, base, at_pos,
+                            at_t0)
 
 
 def hlta_rope_axes(q, k, q_out, k_out, B, Hq, Hk, L, d, spec, inverse=False, stream=None):
-    named = ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))
-    ref = q if q is not None else k
-    _need_dtype(ref.dtype, *named)
-    _check(_lib.hlta_rope_axes(*_addresses(_device(), *named), B, Hq, Hk, L, d,
-                               ctypes.byref(spec), 1 if inverse else 0, _dt(ref),
-                               _stream_address(stream)))
+    th, dt = _th(), (q if q is not None else k).dtype
+    _check(_lib.hlta_rope_axes(
+        *_args(th, (q, "q", dt, None), (k, "k", dt, None), (q_out, "q_out", dt, None),
+               (k_out, "k_out", dt, None)),
+        B, Hq, Hk, L, d, ctypes.byref(spec), 1 if inverse else 0, _dt(q if q is not None else k),
+        _stream_address(th, stream)))
 
 
 def hlta_paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens, B, Hkv, L, d, num_pages,
                       page, max_pages, spec=None, stream=None):
-    named = ((k, "k"), (v, "v"), (k_pages, "k_pages"), (v_pages, "v_pages"))
-    ints = ((table, "table"), (kv_lens, "kv_lens"), (new_lens, "new_lens"))
-    _need_dtype(k.dtype, *named)
-    _need_dtype(_int32(), *ints)
-    _check(_lib.hlta_paged_append(*_addresses(_device(), *named, *ints), B, Hkv, L, d, num_pages,
-                                  page, max_pages, None if spec is None else ctypes.byref(spec),
-                                  _dt(k), _stream_address(stream)))
+    th, dt = _th(), k.dtype
+    i32 = th.int32
+    _check(_lib.hlta_paged_append(
+        *_args(th, (k, "k", dt, None), (v, "v", dt, None), (k_pages, "k_pages", dt, None),
+               (v_pages, "v_pages", dt, None), (table, "table", i32, None),
+               (kv_lens, "kv_lens", i32, None), (new_lens, "new_lens", i32, None)),
+        B, Hkv, L, d, num_pages, page, max_pages, None if spec is None else ctypes.byref(spec),
+        _dt(k), _stream_address(th, stream)))
 
 
 def hlta_paged_attn_workspace_bytes(B, Hq, Hkv, L, d, page, max_pages, weights=False,
@@ -411,18 +402,16 @@ def hlta_paged_attn_workspace_bytes(B, Hq, Hkv, L, d, page, max_pages, weights=F
 def hlta_paged_attn_fwd(q, k_pages, v_pages, table, kv_lens, new_lens, o, lse, w_in, w_out, decay,
                         B, Hq, Hkv, L, d, num_pages, page, max_pages, N, w, scale, workspace,
                         stream=None):
-    named = ((q, "q"), (k_pages, "k_pages"), (v_pages, "v_pages"), (o, "o"))
-    ints = ((table, "table"), (kv_lens, "kv_lens"), (new_lens, "new_lens"))
-    floats = ((lse, "lse"), (w_in, "w_in"), (w_out, "w_out"))
-    _need_dtype(q.dtype, *named)
-    _need_dtype(_int32(), *ints)
-    _need_dtype(_float32(), *floats)
-    pq, pk, pv, po, pt, pl, pn, ps, pi, pw, ws = _addresses(_device(), *named, *ints, *floats,
-                                                            (workspace, "workspace"))
-    _check(_lib.hlta_paged_attn_fwd(pq, pk, pv, pt, pl, pn, po, ps, pi, pw, decay, B, Hq, Hkv, L,
-                                    d, num_pages, page, max_pages, N, w, scale, ws,
-                                    workspace.numel() * workspace.element_size(), _dt(q),
-                                    _stream_address(stream)))
+    th, dt = _th(), q.dtype
+    i32, f32 = th.int32, th.float32
+    *addr, ws = _args(th, (q, "q", dt, None), (k_pages, "k_pages", dt, None),
+                      (v_pages, "v_pages", dt, None), (table, "table", i32, None),
+                      (kv_lens, "kv_lens", i32, None), (new_lens, "new_lens", i32, None),
+                      (o, "o", dt, None), (lse, "lse", f32, None), (w_in, "w_in", f32, None),
+                      (w_out, "w_out", f32, None), (workspace, "workspace", None, None))
+    _check(_lib.hlta_paged_attn_fwd(*addr, decay, B, Hq, Hkv, L, d, num_pages, page, max_pages, N,
+                                    w, scale, ws, workspace.nbytes, _dt(q),
+                                    _stream_address(th, stream)))
 
 
 def hlta_paged_evict_workspace_bytes(B, Hkv, budget) -> int:
@@ -432,39 +421,39 @@ def hlta_paged_evict_workspace_bytes(B, Hkv, budget) -> int:
 def hlta_paged_evict(weights, k_pages, v_pages, table, kv_lens, B, Hkv, d, num_pages, page,
                      max_pages, budget, sink, recent, k_dst, v_dst, dst_table, num_dst, max_dst,
                      new_lens, kept, w_out, workspace, stream=None):
-    named = ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_dst, "k_dst"), (v_dst, "v_dst"))
-    ints = ((table, "table"), (kv_lens, "kv_lens"), (dst_table, "dst_table"),
-            (new_lens, "new_lens"), (kept, "kept"))
-    floats = ((weights, "weights"), (w_out, "w_out"))
-    _need_dtype(k_pages.dtype, *named)
-    _need_dtype(_int32(), *ints)
-    _need_dtype(_float32(), *floats)
-    pk, pv, dk, dv, pt, pl, dt, pn, pi, pw, po, ws = _addresses(
-        _device(), *named, *ints, *floats, (workspace, "workspace"))
-    _check(_lib.hlta_paged_evict(pw, pk, pv, pt, pl, B, Hkv, d, num_pages, page, max_pages, budget,
-                                 sink, recent, dk, dv, dt, num_dst, max_dst, pn, pi, po, ws,
-                                 workspace.numel() * workspace.element_size(), _dt(k_pages),
-                                 _stream_address(stream)))
+    th, dt = _th(), k_pages.dtype
+    i32, f32 = th.int32, th.float32
+    src = _args(th, (weights, "weights", f32, None), (k_pages, "k_pages", dt, None),
+                (v_pages, "v_pages", dt, None), (table, "table", i32, None),
+                (kv_lens, "kv_lens", i32, None))
+    kd, vd, dst, nl, kp, wo, ws = _args(
+        th, (k_dst, "k_dst", dt, None), (v_dst, "v_dst", dt, None),
+        (dst_table, "dst_table", i32, None), (new_lens, "new_lens", i32, None),
+        (kept, "kept", i32, None), (w_out, "w_out", f32, None), (workspace, "workspace", None, None))
+    _check(_lib.hlta_paged_evict(*src, B, Hkv, d, num_pages, page, max_pages, budget, sink, recent,
+                                 kd, vd, dst, num_dst, max_dst, nl, kp, wo, ws, workspace.nbytes,
+                                 _dt(k_pages), _stream_address(th, stream)))
 
 
-def _gdn_step_args(q, k, v, a, b, o, S, S_out, slots, lens):
-    _need_dtype(q.dtype, (k, "k"), (v, "v"), (o, "o"))
-    _need_dtype(_float32(), (a, "a"), (b, "b"), (S, "S"), (S_out, "S_out"))
-    _need_dtype(_int32(), (slots, "slots"), (lens, "lens"))
-    return _addresses(_device(), (q, "q"), (k, "k"), (v, "v"), (a, "a"), (b, "b"), (o, "o"),
-                      (S, "S"), (S_out, "S_out"), (slots, "slots"), (lens, "lens"))
+def _gdn_step_args(th, q, k, v, a, b, o, S, S_out, slots, lens, qs=None, gs=None, ss=None, bs=None):
+    dt, f32, i32 = q.dtype, th.float32, th.int32
+    return _args(th, (q, "q", dt, qs), (k, "k", dt, qs), (v, "v", dt, qs), (a, "a", f32, gs),
+                 (b, "b", f32, gs), (o, "o", dt, qs), (S, "S", f32, ss), (S_out, "S_out", f32, ss),
+                 (slots, "slots", i32, bs), (lens, "lens", i32, bs))
 
 
 def hlta_gdn_step(q, k, v, a, b, o, S, S_out, slots, lens, B, H, L, d, num_slots, stream=None):
-    args = _gdn_step_args(q, k, v, a, b, o, S, S_out, slots, lens)
-    _check(_lib.hlta_gdn_step(*args, B, H, L, d, num_slots, _dt(q), _stream_address(stream)))
+    th = _th()
+    _check(_lib.hlta_gdn_step(*_gdn_step_args(th, q, k, v, a, b, o, S, S_out, slots, lens), B, H, L,
+                              d, num_slots, _dt(q), _stream_address(th, stream)))
 
 
 def hlta_gdn_step_raw(q, k, v, x, y, c, o, S, S_out, slots, lens, B, H, L, d, num_slots,
                       stream=None):
-    args = _gdn_step_args(q, k, v, x, y, o, S, S_out, slots, lens)
+    th = _th()
+    args = _gdn_step_args(th, q, k, v, x, y, o, S, S_out, slots, lens)
     _check(_lib.hlta_gdn_step_raw(*args[:5], c, *args[5:], B, H, L, d, num_slots, _dt(q),
-                                  _stream_address(stream)))
+                                  _stream_address(th, stream)))
 
 
 def hlta_device_status(stream=None) -> int:
@@ -672,47 +661,37 @@ def rope_axes(q, k, pairs, grid=None, pos=None, t0=None, base=10000.0, halves=Fa
               shared_freq=False, inverse=False, out=None, stream=None):
     """q and k ([B, H, L, d], either may be None) rotated by positions on three axes (see
     hlta_rope_axes); `out` = (q_out, k_out), which may be (q, k) for in place."""
-    import torch
-    ref = q if q is not None else k
-    B, _, L, d = ref.shape
-    Hq, Hk = (0 if t is None else t.shape[1] for t in (q, k))
-    for t, n, H in ((q, "q", Hq), (k, "k", Hk)):
-        _need_shape(t, n, B, H, L, d)
-    _need_shape(pos, "pos", B, L, 3)
-    _need_shape(t0, "t0", B)
-    spec = rope_axes_spec(pairs, grid, pos, t0, base, halves, shared_freq)
+    th, ref = _th(), q if q is not None else k
+    B, H, L, d = ref.shape
+    Hk = k.shape[1] if k is not None else 0
+    spec = rope_axes_spec(pairs, grid, pos, t0, base, halves, shared_freq, B, L)
     if out is None:
-        out = tuple(None if t is None else torch.empty_like(t) for t in (q, k))
+        out = (None if q is None else th.empty_like(q), None if k is None else th.empty_like(k))
         _on(stream, *out)
-    _need_shape(out[0], "q_out", B, Hq, L, d)
-    _need_shape(out[1], "k_out", B, Hk, L, d)
-    hlta_rope_axes(q, k, out[0], out[1], B, Hq, Hk, L, d, spec, inverse, stream)
+    dt, qs, ks = ref.dtype, (B, H, L, d), (B, Hk, L, d)
+    _check(_lib.hlta_rope_axes(
+        *_args(th, (q, "q", dt, qs), (k, "k", dt, ks), (out[0], "q_out", dt, qs),
+               (out[1], "k_out", dt, ks)),
+        B, H, Hk, L, d, ctypes.byref(spec), 1 if inverse else 0, _dt(ref),
+        _stream_address(th, stream)))
     return out
-
-
-def _cache_shape(k_pages, v_pages, table, kv_lens, new_lens=None):
-    pages, H, page, d = k_pages.shape
-    B, width = table.shape
-    _need_shape(v_pages, "v_pages", pages, H, page, d)
-    _need_shape(kv_lens, "kv_lens", B)
-    _need_shape(new_lens, "new_lens", B)
-    return pages, H, page, d, B, width
 
 
 def paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens=None, rope=None, stream=None):
     """Append a chunk (k, v [B, Hkv, L, d]) to a paged cache (see hlta_paged_append); `rope`: the
     arguments of rope_axes_spec as a dict, for k to be rotated on the way."""
-    pages, H, page, d, B, width = _cache_shape(k_pages, v_pages, table, kv_lens, new_lens)
+    th, dt = _th(), k.dtype
+    i32, pages = th.int32, k_pages.shape
+    num, H, page, d = pages
+    B, width = table.shape
     L = k.shape[2]
-    _need_shape(k, "k", B, H, L, d)
-    _need_shape(v, "v", B, H, L, d)
-    spec = None
-    if rope is not None:
-        _need_shape(rope.get("pos"), "pos", B, L, 3)
-        _need_shape(rope.get("t0"), "t0", B)
-        spec = rope_axes_spec(**rope)
-    hlta_paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens, B, H, L, d, pages, page,
-                      width, spec, stream)
+    spec = None if rope is None else ctypes.byref(rope_axes_spec(**rope, B=B, L=L))
+    cs, bs = (B, H, L, d), (B,)
+    _check(_lib.hlta_paged_append(
+        *_args(th, (k, "k", dt, cs), (v, "v", dt, cs), (k_pages, "k_pages", dt, pages),
+               (v_pages, "v_pages", dt, pages), (table, "table", i32, None),
+               (kv_lens, "kv_lens", i32, bs), (new_lens, "new_lens", i32, bs)),
+        B, H, L, d, num, page, width, spec, _dt(k), _stream_address(th, stream)))
 
 
 def paged_attn(q, k_pages, v_pages, table, kv_lens, new_lens=None, N=1, w=0, scale=0.0, out=None,
@@ -720,23 +699,29 @@ def paged_attn(q, k_pages, v_pages, table, kv_lens, new_lens=None, N=1, w=0, sca
     """Attention of a chunk (q [B, Hq, L, d]) over a paged cache it was appended to (see
     hlta_paged_attn_fwd). Rows behind a rollout's new tokens are left as they are in `out`
     (zeros when it is allocated here)."""
-    import torch
-    pages, H, page, d, B, width = _cache_shape(k_pages, v_pages, table, kv_lens, new_lens)
-    Hq, L = q.shape[1:3]
-    _need_shape(q, "q", B, Hq, L, d)
-    _need_shape(lse, "lse", B, Hq, L)
-    _need_shape(w_in, "w_in", B, H, width * page)
-    _need_shape(w_out, "w_out", B, H, width * page)
+    th, dt = _th(), q.dtype
+    i32, f32, pages, qs = th.int32, th.float32, k_pages.shape, q.shape
+    num, H, page, d = pages
+    B, width = table.shape
+    Hq, L = qs[1], qs[2]
     if out is None:
-        out = torch.empty_like(q) if new_lens is None else torch.zeros_like(q)
+        out = th.empty_like(q) if new_lens is None else th.zeros_like(q)
         _on(stream, out)
-    _need_shape(out, "out", B, Hq, L, d)
+    code = _dt(q)
     if workspace is None:
-        workspace = _workspace(hlta_paged_attn_workspace_bytes(B, Hq, H, L, d, page, width,
-                                                               w_out is not None, _dt(q)), q.device)
+        workspace = th.empty(_lib.hlta_paged_attn_workspace_bytes(
+            B, Hq, H, L, d, page, width, 0 if w_out is None else 1, code), dtype=th.uint8,
+            device=q.device)
         _on(stream, workspace)
-    hlta_paged_attn_fwd(q, k_pages, v_pages, table, kv_lens, new_lens, out, lse, w_in, w_out, decay,
-                        B, Hq, H, L, d, pages, page, width, N, w, scale, workspace, stream)
+    bs, ws_shape = (B,), (B, H, width * page)
+    *addr, ws = _args(th, (q, "q", dt, (B, Hq, L, d)), (k_pages, "k_pages", dt, pages),
+                      (v_pages, "v_pages", dt, pages), (table, "table", i32, None),
+                      (kv_lens, "kv_lens", i32, bs), (new_lens, "new_lens", i32, bs),
+                      (out, "out", dt, qs), (lse, "lse", f32, (B, Hq, L)),
+                      (w_in, "w_in", f32, ws_shape), (w_out, "w_out", f32, ws_shape),
+                      (workspace, "workspace", None, None))
+    _check(_lib.hlta_paged_attn_fwd(*addr, decay, B, Hq, H, L, d, num, page, width, N, w, scale,
+                                    ws, workspace.nbytes, code, _stream_address(th, stream)))
     return out
 
 
@@ -745,58 +730,62 @@ def paged_evict(weights, k_pages, v_pages, table, kv_lens, budget, sink, recent,
     """Copy the `budget` positions of largest accumulated weight (the first `sink` and the last
     `recent` always among them) of every rollout and key head to the destination's pages (see
     hlta_paged_evict). Returns the new lengths [B] int32."""
-    import torch
-    pages, H, page, d, B, width = _cache_shape(k_pages, v_pages, table, kv_lens, new_lens)
-    num_dst, dwidth = k_dst.shape[0], dst_table.shape[1]
-    _need_shape(weights, "weights", B, H, width * page)
-    _need_shape(k_dst, "k_dst", num_dst, H, page, d)
-    _need_shape(v_dst, "v_dst", num_dst, H, page, d)
-    _need_shape(dst_table, "dst_table", B, dwidth)
-    _need_shape(kept, "kept", B, H, budget)
-    _need_shape(w_out, "w_out", B, H, dwidth * page)
+    th, dt = _th(), k_pages.dtype
+    i32, f32, pages, to = th.int32, th.float32, k_pages.shape, k_dst.shape
+    num, H, page, d = pages
+    (B, width), (_, dwidth) = table.shape, dst_table.shape
+    bs = (B,)
     if new_lens is None:
-        new_lens = torch.empty_like(kv_lens)
+        new_lens = th.empty_like(kv_lens)
         _on(stream, new_lens)
     if workspace is None:
-        workspace = _workspace(hlta_paged_evict_workspace_bytes(B, H, budget), weights.device)
+        workspace = th.empty(_lib.hlta_paged_evict_workspace_bytes(B, H, budget), dtype=th.uint8,
+                             device=weights.device)
         _on(stream, workspace)
-    hlta_paged_evict(weights, k_pages, v_pages, table, kv_lens, B, H, d, pages, page, width, budget,
-                     sink, recent, k_dst, v_dst, dst_table, num_dst, dwidth, new_lens, kept, w_out,
-                     workspace, stream)
+    src = _args(th, (weights, "weights", f32, (B, H, width * page)),
+                (k_pages, "k_pages", dt, pages), (v_pages, "v_pages", dt, pages),
+                (table, "table", i32, None), (kv_lens, "kv_lens", i32, bs))
+    kd, vd, dst, nl, kp, wo, ws = _args(
+        th, (k_dst, "k_dst", dt, (to[0], H, page, d)), (v_dst, "v_dst", dt, to),
+        (dst_table, "dst_table", i32, (B, dwidth)), (new_lens, "new_lens", i32, bs),
+        (kept, "kept", i32, (B, H, budget)), (w_out, "w_out", f32, (B, H, dwidth * page)),
+        (workspace, "workspace", None, None))
+    _check(_lib.hlta_paged_evict(*src, B, H, d, num, page, width, budget, sink, recent, kd, vd, dst,
+                                 to[0], dwidth, nl, kp, wo, ws, workspace.nbytes, _dt(k_pages),
+                                 _stream_address(th, stream)))
     return new_lens
 
 
-def _gdn_step_shapes(q, k, v, a, b, S, slots, lens, out, S_out, stream):
-    import torch
-    B, H, L, d = q.shape
-    for t, n in ((k, "k"), (v, "v"), (out, "out")):
-        _need_shape(t, n, B, H, L, d)
-    for t, n in ((a, "a"), (b, "b")):
-        _need_shape(t, n, B, H, L)
-    _need_shape(S, "S", S.shape[0], H, d, d)
-    _need_shape(S_out, "S_out", *S.shape)
-    _need_shape(slots, "slots", B)
-    _need_shape(lens, "lens", B)
+def _gdn_step(raw, q, k, v, a, b, S, slots, lens, out, S_out, stream):
+    th, qs = _th(), q.shape
+    B, H, L, d = qs
     if out is None:
-        out = torch.empty_like(q) if slots is None and lens is None else torch.zeros_like(q)
+        out = th.empty_like(q) if slots is None and lens is None else th.zeros_like(q)
         _on(stream, out)
-    return (B, H, L, d), out, S if S_out is None else S_out
+    if S_out is None:
+        S_out = S
+    num = S.shape[0]
+    args = _gdn_step_args(th, q, k, v, a, b, out, S, S_out, slots, lens, qs, (B, H, L),
+                          (num, H, d, d), (B,))
+    if raw is None:
+        st = _lib.hlta_gdn_step(*args, B, H, L, d, num, _dt(q), _stream_address(th, stream))
+    else:
+        st = _lib.hlta_gdn_step_raw(*args[:5], raw, *args[5:], B, H, L, d, num, _dt(q),
+                                    _stream_address(th, stream))
+    _check(st)
+    return out, S_out
 
 
 def gdn_step(q, k, v, a, b, S, slots=None, lens=None, out=None, S_out=None, stream=None):
     """One step of one or a few tokens of the gated delta rule over a pool of states S
     [slots, H, d, d], updated in place unless S_out is given (see hlta_gdn_step). Returns
-    (o, S_out)."""
-    (B, H, L, d), o, So = _gdn_step_shapes(q, k, v, a, b, S, slots, lens, out, S_out, stream)
-    hlta_gdn_step(q, k, v, a, b, o, S, So, slots, lens, B, H, L, d, S.shape[0], stream)
-    return o, So
+    (o, S_out). Outputs allocated here are zero where the call leaves rows as they are."""
+    return _gdn_step(None, q, k, v, a, b, S, slots, lens, out, S_out, stream)
 
 
 def gdn_step_raw(q, k, v, x, y, c, S, slots=None, lens=None, out=None, S_out=None, stream=None):
     """gdn_step from raw q, k and raw gate inputs (see hlta_gdn_step_raw)."""
-    (B, H, L, d), o, So = _gdn_step_shapes(q, k, v, x, y, S, slots, lens, out, S_out, stream)
-    hlta_gdn_step_raw(q, k, v, x, y, c, o, S, So, slots, lens, B, H, L, d, S.shape[0], stream)
-    return o, So
+    return _gdn_step(float(c), q, k, v, x, y, S, slots, lens, out, S_out, stream)
 
 
 class Stream:

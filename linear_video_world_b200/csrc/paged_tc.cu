@@ -14,8 +14,8 @@
 //                    cores idle between its groups of products: 1.09 PFLOP/s in place of 1.17)
 //   warp 11          completes the warpgroup that gives registers to the softmax warps
 // S = Q K^T goes to tensor memory, the softmax reads a row's 128 scores into registers and frees it
-// at once, so S of the next tile is done while P of this one is formed; P goes to shared memory,
-// stored in two halves, each as soon as the previous P V has read that half.
+// at once, so S of the next tile is done while P of this one is formed; P goes to shared memory, once
+// the previous P V has read it (half of this tile's exponentials are done by then).
 // What bounds it: per tile of 2 x 128 rows the products take 2051 cycles (64 per 128 x 128 x 16,
 // measured, from shared or tensor memory alike; a product of 64 keys takes 62, so tiles are not
 // halved), the exponentials 2048 (16 a cycle). So neither may wait for the other.
@@ -62,8 +62,7 @@ enum {
     B_FULL, B_EMPTY = B_FULL + NSLOT,               // per slot
     B_SFULL = B_EMPTY + NSLOT,                      // per sub-tile from here
     B_SFREE = B_SFULL + QT, B_PFULL = B_SFREE + QT,
-    B_PVA = B_PFULL + QT, B_PVDONE = B_PVA + QT,    // P V: its first half, all of it
-    B_ODONE = B_PVDONE + QT, B_OFREE = B_ODONE + QT, NBARS = B_OFREE + QT
+    B_PVDONE = B_PFULL + QT, B_ODONE = B_PVDONE + QT, B_OFREE = B_ODONE + QT, NBARS = B_OFREE + QT
 };
 constexpr uint32_t SM_PLACE = SM_BAR + 8 * NBARS;   // the block's start on the line; the softmax warps' places
 constexpr uint32_t SM_TMEM = SM_PLACE + 9 * 32, SM_ABORT = SM_TMEM + 4;
@@ -220,7 +219,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             mbar_init(BAR(B_SFULL + q), 1);
             mbar_init(BAR(B_SFREE + q), BM);
             mbar_init(BAR(B_PFULL + q), BM);
-            mbar_init(BAR(B_PVA + q), 1);
             mbar_init(BAR(B_PVDONE + q), 1);
             mbar_init(BAR(B_ODONE + q), 1);
             mbar_init(BAR(B_OFREE + q), BM);
@@ -323,8 +321,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                 const uint64_t dv0 = tc::sw128_desc(sbase + SM_SLOT, HALF, 1024);     // MN-major (V)
                 const uint64_t dp = tc::sw128_desc(sbase + SM_P + q * TILE, 16, 1024);
                 const uint32_t s_tm = tmem + 128u * q, o_tm = tmem + 256u + 128u * q;
-                const uint32_t sfull = BAR(B_SFULL + q), sfree = BAR(B_SFREE + q), pfull = BAR(B_PFULL + q), pva = BAR(B_PVA + q),
-                               pvdone = BAR(B_PVDONE + q), ofree = BAR(B_OFREE + q);
+                const uint32_t sfull = BAR(B_SFULL + q), sfree = BAR(B_SFREE + q), pfull = BAR(B_PFULL + q), pvdone = BAR(B_PVDONE + q), ofree = BAR(B_OFREE + q);
                 Place at = *place(0);
                 uint32_t slot = 0, lap = 0;                           // the next ring item, the parity of its lap
                 uint32_t s_par = 0, p_par = 0;                        // parities of the next S, the next P
@@ -373,7 +370,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                         if (t + 1 == tb) tc::umma_commit(BAR(B_QFREE));               // the share's last S was issued
                         return true;
                     };
-                    // O += P V of tile t, committed in two halves
+                    // O += P V of tile t
                     auto do_pv = [&](int t) -> bool {
                         if (!item()) return false;
                         if (t >= a && t < b) {
@@ -387,7 +384,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                             for (int kk = 0; kk < BN / 16; ++kk) {
                                 tc::umma_bf16(o_tm, dp + ((uint64_t)((kk >> 2) * HALF + (kk & 3) * 32) >> 4), dv + (uint64_t)((kk * 2048) >> 4), IDESC_O,
                                               kk > 0 ? 1u : acc);
-                                if (kk == BN / 32 - 1) tc::umma_commit(pva);
                             }
                             tc::umma_commit(pvdone);
                             tc::umma_commit(BAR(B_EMPTY) + 8u * slot);
@@ -466,7 +462,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                 const float2 sl = make_float2(p.sl2, p.sl2), nm = make_float2(negm, negm);
                 float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 uint32_t pk[32];
-                // P of 64 keys into registers; stored when the previous P V is done with that half
+                // P of 64 keys into registers; stored when the previous P V is done
                 auto half = [&](int h) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
@@ -484,10 +480,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                                      : "memory");
                 };
                 half(0);
-                if (k >= 1 && !(ok = __all_sync(0xffffffffu, wait_bar(BAR(B_PVA + q), (uint32_t)(k - 1) & 1u)))) break;
+                if (k >= 1 && !(ok = __all_sync(0xffffffffu, wait_bar(BAR(B_PVDONE + q), (uint32_t)(k - 1) & 1u)))) break;
                 store(0);
                 half(1);
-                if (k >= 1 && !(ok = __all_sync(0xffffffffu, wait_bar(BAR(B_PVDONE + q), (uint32_t)(k - 1) & 1u)))) break;
                 store(1);
                 if (resc) {
                     tc::fence_after_sync();

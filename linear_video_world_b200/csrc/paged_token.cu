@@ -382,9 +382,7 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
     const int np = cut ? hd.g1 - hd.g0 + 1 : 0;
     auto slot = [&](int i) { return (long)(hd.g0 + i) * 2 + (i == 0 ? hd.slot0 : 0); };
     if (hd.T == 0 || cut) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = warp * 2 + j;
+        for (int r = warp; r < p.R; r += JT / 32) {
             float m = -INFINITY, l = 0.f;
             for (int i = lane; i < np; i += 32) m = fmaxf(m, p.ml[slot(i) * MROWS + r].x);
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -397,7 +395,7 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
             for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             if (lane == 0) {
                 s_ml[r] = make_float2(m, l > 0.f ? 1.f / l : l == l ? 0.f : l);
-                if (p.lse && blockIdx.x == 0 && r < p.R && frem(r, p.line.byL) < ro.n) p.lse[row0 + r] = (m + log2f(l)) * 0.69314718055994531f;
+                if (p.lse && blockIdx.x == 0 && frem(r, p.line.byL) < ro.n) p.lse[row0 + r] = (m + log2f(l)) * 0.69314718055994531f;
             }
         }
     } else if (p.w_out && threadIdx.x < p.R) {
@@ -406,20 +404,32 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
     }
     __syncthreads();
     if (blockIdx.x == 0 && (hd.T == 0 || cut)) {
-        // eight channels of a row: a pair of registers of the fragment, four lanes
-        const int pair = threadIdx.x >> 3, r = (threadIdx.x & 7) + 8 * (pair & 1);
+        // An item is eight channels of a row: a pair of registers of the fragment in four lanes, 16
+        // items a row. With few rows several lanes share an item and take its pieces in turn.
+        int share = 1;
+        while (share < 16 && 2 * share * p.R <= JT / 16) share *= 2;
+        const int item = threadIdx.x / share, r = item >> 4, n = item & 15;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
+        if (r < p.R) {
+            // row r of the fragment: lanes 4 (r & 7) .., registers 4 n + 2 (r >> 3) and the next
+            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (4 * n + 2 * (r >> 3)) * 8 + (r & 7);
 #pragma unroll 8
-        for (int i = 0; i < np; ++i) {
-            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (slot(i) * 64 + 2 * pair) * 8 + (threadIdx.x & 7);
-            const float4 u = src[0], v = src[8];
-            const float f = s_f[i][r];
-            a.x = fmaf(u.x, f, a.x); a.y = fmaf(u.y, f, a.y); a.z = fmaf(u.z, f, a.z); a.w = fmaf(u.w, f, a.w);
-            d.x = fmaf(v.x, f, d.x); d.y = fmaf(v.y, f, d.y); d.z = fmaf(v.z, f, d.z); d.w = fmaf(v.w, f, d.w);
+            for (int i = threadIdx.x % share; i < np; i += share) {
+                const float4 u = src[slot(i) * 512], v = src[slot(i) * 512 + 8];
+                const float f = s_f[i][r];
+                a.x = fmaf(u.x, f, a.x); a.y = fmaf(u.y, f, a.y); a.z = fmaf(u.z, f, a.z); a.w = fmaf(u.w, f, a.w);
+                d.x = fmaf(v.x, f, d.x); d.y = fmaf(v.y, f, d.y); d.z = fmaf(v.z, f, d.z); d.w = fmaf(v.w, f, d.w);
+            }
         }
-        if (r < p.R && frem(r, p.line.byL) < ro.n) {
+        for (int o = share >> 1; o; o >>= 1) {
+            a.x += __shfl_xor_sync(0xffffffffu, a.x, o); a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+            a.z += __shfl_xor_sync(0xffffffffu, a.z, o); a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+            d.x += __shfl_xor_sync(0xffffffffu, d.x, o); d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
+            d.z += __shfl_xor_sync(0xffffffffu, d.z, o); d.w += __shfl_xor_sync(0xffffffffu, d.w, o);
+        }
+        if (threadIdx.x % share == 0 && r < p.R && frem(r, p.line.byL) < ro.n) {
             const float inv = s_ml[r].y;
-            *reinterpret_cast<uint4 *>(p.o + (row0 + r) * D + 8 * (pair >> 1)) =
+            *reinterpret_cast<uint4 *>(p.o + (row0 + r) * D + 8 * n) =
                 make_uint4(tc::pack_bf16(a.x * inv, d.x * inv), tc::pack_bf16(a.y * inv, d.y * inv), tc::pack_bf16(a.z * inv, d.z * inv), tc::pack_bf16(a.w * inv, d.w * inv));
         }
     }
