@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(NT, 6) gdn_step_kernel(const GdnStepArgs p)
         if (t0 + warp < n) {            // one warp stages a token
             const long tok = bh * p.L + t0 + warp, at = tok * D;
             float q[4], k[4], qq = 0.f, kk = 0.f, qk = 0.f;
-            vs[warp][lane] = ldf((const E *)p.v + at + row0 + lane);
+            for (int x = lane; x < ROWS; x += 32) vs[warp][x] = ldf((const E *)p.v + at + row0 + x);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 q[x] = ldf((const E *)p.q + at + x * 32 + lane);

@@ -8,8 +8,9 @@
 // used for every head.
 //
 // Bound by HBM: every element is read and written once. A thread owns one 16-byte chunk of a
-// token's row (layout 1: the two chunks that its pairs join) and walks heads in groups of four,
-// all four loads in flight before the first store; the heads are split over blockIdx.y until the
+// token's row (layout 1: the two chunks that its pairs join) and walks heads in groups of eight,
+// all eight loads in flight before the first store (groups of four: 3 % slower at 21 frames of 16 heads,
+// 5 % at one frame of 8); the heads are split over blockIdx.y until the
 // grid fills the GPU, so a call of few tokens has one group of heads per thread and pays one
 // round trip. Rows whose d or 2P is no multiple of the chunk take one pair or channel per thread.
 #include "hlta_internal.cuh"
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(THREADS) turn_kernel_v(const __grid_constant__
     constexpr int V = 16 / (int)sizeof(E);
     constexpr int NC = LAYOUT ? 2 : 1;           // chunks a rotating thread owns
     constexpr int NP = LAYOUT ? V : V / 2;       // pairs in them
-    constexpr int NB = 4;                        // heads in flight
+    constexpr int NB = 8;                        // heads in flight
     __shared__ double f_s[MAXP];
     __shared__ unsigned char a_s[MAXP];
     for (int i = threadIdx.x; i < MAXP; i += THREADS) {
@@ -278,11 +279,11 @@ cudaError_t launch(const Turns &t, Job w, int B, bool bf16, cudaStream_t s)
     w.total = (long)B * w.L * w.units;
     const long blocks = (w.total + THREADS - 1) / THREADS;
     if (blocks > 0x7fffffffL) return cudaErrorNotSupported;
-    // heads per thread: all of them once the tokens alone fill the GPU (148 SMs of 8 blocks), fewer
-    // for fewer tokens, down to one group of four in flight
-    const long want = (148L * 8 + blocks - 1) / blocks;
-    const int groups = (int)std::min<long>(std::max<long>(want, 1), (Htot + 3) / 4);
-    w.per = (((Htot + groups - 1) / groups) + 3) & ~3;
+    // heads per thread: all of them once the tokens alone fill the GPU twice (148 SMs of 8 blocks),
+    // fewer for fewer tokens, down to one group in flight
+    const long want = (148L * 16 + blocks - 1) / blocks;
+    const int groups = (int)std::min<long>(std::max<long>(want, 1), (Htot + 7) / 8);
+    w.per = (((Htot + groups - 1) / groups) + 7) & ~7;
     const dim3 grid((unsigned)blocks, (unsigned)((Htot + w.per - 1) / w.per));
     if (!vec) {
         if (bf16) turn_kernel<__nv_bfloat16, PAGED><<<grid, THREADS, 0, s>>>(t, w), note_launch();
