@@ -2,7 +2,7 @@
 // copy their keys, values and weights to the destination's pages.
 //
 // Choice, a cluster of one to eight blocks per (rollout, key head), as many as still fill the GPU
-// (64 rows of 20000 to 32760 positions: 38 us with one block each, CHOICE_TIME with two): of the
+// (64 rows of 20000 to 32760 positions: 38 us with one block each, 24 us with two): of the
 // middle positions the `take` largest weights, found by a radix select over order-preserving 32-bit
 // keys of the weights (three passes of 11, 11 and 10 bits, from the top: each counts the digits of
 // the keys that still match the threshold's prefix; the blocks read one another's counts). Each
@@ -27,7 +27,7 @@ using namespace paged;
 
 constexpr int ST = 1024, SW = ST / 32;                  // threads and warps of the choice
 constexpr int BINS = 2048, KEEP = 49152;
-constexpr size_t CHOOSE_SMEM = (size_t)(KEEP + BINS) * 4;
+constexpr size_t CHOOSE_SMEM = (size_t)(KEEP + 2 * BINS) * 4;
 std::atomic<unsigned long long> g_shared{0};
 
 // rises with the weight; equal weights (0 and -0 too) give equal keys, NaN the least
@@ -41,7 +41,7 @@ __device__ __forceinline__ uint32_t key_of(float w)
 __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int *kept)
 {
     extern __shared__ uint32_t sm[];
-    uint32_t *hist = sm, *keys = sm + BINS;
+    uint32_t *keys = sm + 2 * BINS;             // behind two sets of counts, used in turn
     __shared__ int warp_n[SW], warp_e[SW], block_n[2];
     __shared__ uint32_t s_digit;
     __shared__ int s_left;
@@ -49,6 +49,16 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int nblk = (int)cluster.num_blocks(), blk = (int)cluster.block_rank();
+    auto sync = [&] {
+        if (nblk > 1) cluster.sync();
+        else __syncthreads();
+    };
+    // sum of the warps' numbers before this one
+    auto before_warp = [&](const int *v) {
+        int x = lane < warp ? v[lane] : 0;
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    };
     const long bh = blockIdx.x / nblk;
     const int h = (int)(bh % a.c.H), b = (int)(bh / a.c.H), tid = blk * ST + (int)threadIdx.x;
     const int cap = a.c.max_pages << a.c.page_log2;
@@ -77,6 +87,7 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
     if (take > 0) {
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+            uint32_t *hist = sm + (pass & 1) * BINS;
             for (int i = threadIdx.x; i < BINS; i += ST) hist[i] = 0;
             __syncthreads();
 #pragma unroll 4
@@ -91,7 +102,7 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
                     atomicAdd(&hist[d], 1u);
                 }
             }
-            cluster.sync();
+            sync();
             // the digit at which the count from the top reaches `left`: thread t owns digits
             // BINS - 1 - 2 t and BINS - 2 - 2 t
             int c0 = 0, c1 = 0;
@@ -107,15 +118,13 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
             }
             if (lane == 31) warp_n[warp] = x;
             __syncthreads();
-            int before = 0;
-            for (int v = 0; v < SW; ++v) before += v < warp ? warp_n[v] : 0;
-            before += x - c0 - c1;
+            const int before = before_warp(warp_n) + x - c0 - c1;
             if (before < left && before + c0 + c1 >= left) {
                 const bool second = before + c0 < left;
                 s_digit = (uint32_t)(BINS - 1 - 2 * (int)threadIdx.x - (second ? 1 : 0));
                 s_left = left - before - (second ? c0 : 0);
             }
-            cluster.sync();                     // and the counts may be cleared
+            __syncthreads();
             prefix |= s_digit << shift;
             mask |= ((1u << width) - 1u) << shift;
             left = s_left;
@@ -130,6 +139,7 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
     // number the kept middle positions in order: each warp a run of them
     const int run = ((m + SW - 1) / SW + 31) & ~31, i_lo = min(m, warp * run), i_hi = min(m, i_lo + run);
     int above = 0, equal = 0;
+#pragma unroll 4
     for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
         const int i = i0 + lane;
         const uint32_t k = i < i_hi ? key(i) : 0u;
@@ -141,22 +151,20 @@ __global__ void __launch_bounds__(ST) evict_choose_kernel(PagedEvictArgs a, int 
         warp_e[warp] = equal;
     }
     __syncthreads();
-    above = equal = 0;
-    for (int v = 0; v < SW; ++v) {
-        above += v < warp ? warp_n[v] : 0;
-        equal += v < warp ? warp_e[v] : 0;
-    }
+    above = before_warp(warp_n);
+    equal = before_warp(warp_e);
     if (threadIdx.x == ST - 1) {
         block_n[0] = above + warp_n[SW - 1];
         block_n[1] = equal + warp_e[SW - 1];
     }
-    cluster.sync();
+    sync();
     for (int v = 0; v < blk; ++v) {
         const int *theirs = cluster.map_shared_rank(block_n, v);
         above += theirs[0];
         equal += theirs[1];
     }
-    cluster.sync();                             // no block ends while another reads its counts
+    sync();                                     // no block ends while another reads its counts
+#pragma unroll 4
     for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
         const int i = i0 + lane;
         const uint32_t k = i < i_hi ? key(i) : 0u;
@@ -182,6 +190,8 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(PagedEvictArgs a, const
     if (bh >= (long)a.B * a.c.H) return;
     const int r0 = (int)(item - bh * per) * CPW, h = (int)(bh % a.c.H), b = (int)(bh / a.c.H);
     const int psz = 1 << a.c.page_log2;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the choice (set up at its end: blocks that
+                                                            // wait from its start on cost it 15 us)
     // lanes 0-7: where the eight positions come from and go, in words
     long s = 0, d = -1;
     if (lane < CPW && r0 + lane < a.budget) {
@@ -249,9 +259,15 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, bool bf16, cudaStream_t 
     if ((e = cudaLaunchKernelEx(&cfg, evict_choose_kernel, a, kept)) != cudaSuccess) return e;
     note_launch();
     const int row = a.c.d * (bf16 ? 2 : 4);
-    if (row % 16 == 0) evict_copy_kernel<uint4><<<(unsigned)blocks, 256, 0, s>>>(a, kept, row / 16), note_launch();
-    else evict_copy_kernel<uint16_t><<<(unsigned)blocks, 256, 0, s>>>(a, kept, row / 2), note_launch();
-    return cudaGetLastError();
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    e = row % 16 == 0 ? cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint4>, a, (const int *)kept, row / 16)
+                      : cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint16_t>, a, (const int *)kept, row / 2);
+    if (e == cudaSuccess) note_launch();
+    return e;
 }
 
 }  // namespace hlta
