@@ -788,6 +788,110 @@ def gdn_step_raw(q, k, v, x, y, c, S, slots=None, lens=None, out=None, S_out=Non
     return _gdn_step(float(c), q, k, v, x, y, S, slots, lens, out, S_out, stream)
 
 
+class PagedCache:
+    """Paged key/value cache of B rollouts of different ages (paged_append / paged_attn /
+    paged_evict): the page pool, and the tables that the host keeps and copies to the device when
+    pages change hands. The pool's pages are handed out as rollouts grow, returned by `evict` and
+    `release`. Everything runs on the current stream, which has to be the same one from call to call.
+
+    max_len: the longest a rollout may grow; num_pages: pages of the pool (an eviction needs free
+    pages for what it keeps while it copies). weights: keep the attention weights that `attend`
+    accumulates (times `decay` per call), which `evict` goes by."""
+
+    def __init__(self, B, Hkv, d, num_pages, max_len, page=64, dtype=None, weights=False, decay=1.0):
+        th = _th()
+        if B < 1 or Hkv < 1 or num_pages < 1 or max_len < 1 or page not in (16, 32, 64, 128):
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"bad cache: B={B} Hkv={Hkv} num_pages={num_pages} "
+                            f"max_len={max_len} page={page}")
+        self.B, self.page, self.max_len, self.decay = B, page, max_len, float(decay)
+        self.width = -(-max_len // page)
+        dt = th.bfloat16 if dtype is None else dtype
+        self.k_pages, self.v_pages = (th.empty((num_pages, Hkv, page, d), dtype=dt, device="cuda")
+                                      for _ in range(2))
+        self.table = th.zeros((B, self.width), dtype=th.int32, device="cuda")
+        self.kv_lens = th.zeros(B, dtype=th.int32, device="cuda")
+        self.new_lens = th.zeros(B, dtype=th.int32, device="cuda")
+        self.weights = th.zeros((B, Hkv, self.width * page), device="cuda") if weights else None
+        self.lens = [0] * B                             # tokens cached, per rollout
+        self._free = list(range(num_pages - 1, -1, -1))
+        self._pages = [[] for _ in range(B)]
+
+    def _grow(self, lens):
+        """Pages for the given lengths, or an error that leaves everything as it was."""
+        for b, n in enumerate(lens):
+            if n > self.max_len:
+                raise HltaError(HLTA_ERR_INVALID_ARG, f"rollout {b} would hold {n} tokens, at most {self.max_len}")
+        want = [max(0, -(-n // self.page) - len(p)) for n, p in zip(lens, self._pages)]
+        if sum(want) > len(self._free):
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"{sum(want)} pages wanted, {len(self._free)} free")
+        for p, n in zip(self._pages, want):
+            p.extend(self._free.pop() for _ in range(n))
+        return sum(want) > 0
+
+    def _tables(self, pages):
+        if pages:
+            self.table.copy_(_th().tensor([p + [0] * (self.width - len(p)) for p in self._pages],
+                                          dtype=_th().int32))
+        self.kv_lens.copy_(_th().tensor(self.lens, dtype=_th().int32))
+
+    def append(self, k, v, new_lens=None, rope=None):
+        """Append a chunk (k, v [B, Hkv, L, d]; new_lens: tokens that each rollout really has, a
+        list, None for all L); `rope` as in paged_append."""
+        L = k.shape[2]
+        new = [L] * self.B if new_lens is None else [int(n) for n in new_lens]
+        if len(new) != self.B or any(n < 0 or n > L for n in new):
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"new_lens must be {self.B} numbers in [0, {L}] (got {new})")
+        lens = [a + n for a, n in zip(self.lens, new)]
+        pages = self._grow(lens)
+        self.lens = lens
+        self._tables(pages)
+        self.new_lens.copy_(_th().tensor(new, dtype=_th().int32))
+        paged_append(k, v, self.k_pages, self.v_pages, self.table, self.kv_lens, self.new_lens, rope)
+
+    def attend(self, q, N=1, w=0, scale=0.0, out=None, lse=None):
+        """Attention of the chunk appended last (q [B, Hq, L, d]); adds to the weights if kept."""
+        return paged_attn(q, self.k_pages, self.v_pages, self.table, self.kv_lens, self.new_lens, N,
+                          w, scale, out, lse, self.weights, self.weights, self.decay)
+
+    def evict(self, budget, sink=0, recent=0):
+        """Cut every rollout of more than `budget` tokens to that many (see hlta_paged_evict).
+        Returns the rollouts that were cut."""
+        th = _th()
+        if self.weights is None:
+            raise HltaError(HLTA_ERR_INVALID_ARG, "this cache keeps no weights")
+        cut = [b for b, n in enumerate(self.lens) if n > budget]
+        need = -(-budget // self.page)
+        if need * len(cut) > len(self._free):
+            raise HltaError(HLTA_ERR_INVALID_ARG, f"{need * len(cut)} pages wanted, {len(self._free)} free")
+        if not cut:
+            return cut
+        # the copies go to free pages; rollouts that stay as they are take no part (length 0)
+        to = {b: [self._free[-1 - i * need - j] for j in range(need)] for i, b in enumerate(cut)}
+        dst = th.tensor([to.get(b, [0] * need) for b in range(self.B)], dtype=th.int32).cuda()
+        lens = th.tensor([n if b in to else 0 for b, n in enumerate(self.lens)], dtype=th.int32).cuda()
+        weights = self.weights.clone()
+        w_out = th.empty((self.B, self.weights.shape[1], need * self.page), device="cuda")
+        paged_evict(self.weights, self.k_pages, self.v_pages, self.table, lens, budget, sink, recent,
+                    self.k_pages, self.v_pages, dst, w_out=w_out)
+        for b in cut:
+            weights[b, :, :budget] = w_out[b, :, :budget]
+        del self._free[len(self._free) - need * len(cut):]
+        for b in cut:
+            self._free.extend(self._pages[b])
+            self._pages[b] = to[b]
+            self.lens[b] = budget
+        self.weights = weights
+        self._tables(True)
+        return cut
+
+    def release(self, b):
+        """Empty rollout b: its pages go back to the pool."""
+        self._free.extend(self._pages[b])
+        self._pages[b] = []
+        self.lens[b] = 0
+        self._tables(True)
+
+
 class Stream:
     """Streaming cache (hlta_stream_create_ex / _step / _step_frames / _state /
     _frame_counter / _checkpoint_bytes / _save / _load / _destroy). A step may be captured into a CUDA graph and replayed for the

@@ -1,0 +1,162 @@
+"""The serving operators together, as a rollout server uses them: PagedCache with rotary axes, frame
+windows and eviction, beside the recurrent gated delta rule, against a 64-bit form of the whole."""
+import pytest
+import torch
+
+from serving_util import attn_ref, gdn_ref, grid_positions, rope_ref
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+PAIRS = (22, 21, 21)
+
+
+@pytest.fixture(scope="module")
+def h():
+    import linear_video_world_b200 as h
+    assert torch.cuda.is_available()
+    return h
+
+
+class Twin:
+    """What PagedCache should hold: each rollout's rounded keys and values by position."""
+
+    def __init__(self, B, H, d, page, width, dtype):
+        self.keys = [torch.zeros(H, 0, d).to(dtype) for _ in range(B)]
+        self.vals = [torch.zeros(H, 0, d).to(dtype) for _ in range(B)]
+        self.page, self.k, self.table = page, torch.zeros(1, H, page, d), torch.zeros(B, width)
+
+    @property
+    def kv(self):
+        return [k.shape[1] for k in self.keys]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rollouts_with_windows_and_eviction(h, dtype):
+    """Frames of 6 tokens for three rollouts that start at different times, one padded; every step
+    rotates, appends, attends (three frames back, weights kept) and runs the gated delta heads;
+    after steps 3 and 5 the rollouts are cut to 20 tokens."""
+    B, Hq, H, Hg, d, N, page = 3, 4, 2, 2, 128, 6, 16
+    grid, gen = (2, 3), torch.Generator().manual_seed(5)
+    cache = h.PagedCache(B, H, d, num_pages=24, max_len=64, page=page, dtype=dtype, weights=True, decay=0.75)
+    twin = Twin(B, H, d, page, cache.width, dtype)
+    weights = torch.zeros(B, H, cache.width * page).double()
+    slack = torch.zeros_like(weights)
+    pool = 0.1 * torch.randn(B + 1, Hg, d, d, generator=gen)
+    slots = torch.tensor([3, 0, 1], dtype=torch.int32)
+    state, states = pool.cuda(), [pool[s].clone() for s in slots]
+    steps = [0] * B
+    for step in range(6):
+        new = [N, N if step >= 1 else 0, [N, N, 5, N, 1, N][step]]
+        q, k, v = (torch.randn(B, n, N, d, generator=gen).to(dtype) for n in (Hq, H, H))
+        t0 = torch.tensor(steps, dtype=torch.int32)
+        rq, _ = h.rope_axes(q.cuda(), None, PAIRS, grid=grid, t0=t0.cuda())
+        cache.append(k.cuda(), v.cuda(), new, rope=dict(pairs=PAIRS, grid=grid, t0=t0.cuda()))
+        # the rotation itself is compared elsewhere; here its rounded result goes on
+        rk = h.rope_axes(k.cuda(), None, PAIRS, grid=grid, t0=t0.cuda())[0].cpu()
+        ref = rope_ref(k, PAIRS, grid_positions(B, N, grid, t0))
+        assert float((rk.double() - ref).abs().max()) <= (2.0 ** -8 if dtype == BF else 2.0 ** -20) * float(ref.abs().max())
+        for b in range(B):
+            twin.keys[b] = torch.cat([twin.keys[b], rk[b, :, :new[b]]], 1)
+            twin.vals[b] = torch.cat([twin.vals[b], v[b, :, :new[b]]], 1)
+        assert cache.lens == twin.kv
+        lse = torch.zeros(B, Hq, N, device="cuda")
+        o = cache.attend(rq, N=N, w=3, lse=lse)
+        ro, rl, rw, ob, lb, wb = attn_ref(rq.cpu(), twin, new, N, 3, weights, 0.75)
+        for b, n in enumerate(new):
+            assert bool(((o[b, :, :n].cpu().double() - ro[b, :, :n]).abs() <= ob[b, :, :n]).all())
+            assert bool(((lse[b, :, :n].cpu().double() - rl[b, :, :n]).abs() <= lb[b, :, :n]).all())
+            assert bool((o[b, :, n:] == 0).all())
+            kv = cache.lens[b]
+            slack[b, :, :kv] = 0.75 * slack[b, :, :kv] + wb[b, :, :kv] + 1e-30
+            slack[b, :, kv - n:kv] = wb[b, :, kv - n:kv] + 1e-30
+            got = cache.weights[b, :, :kv].cpu().double()
+            assert bool(((got - rw[b, :, :kv]).abs() <= slack[b, :, :kv]).all())
+            weights[b, :, :kv] = rw[b, :, :kv]
+        # the gated delta heads of the same tokens
+        gq, gk, gv = (torch.randn(B, Hg, N, d, generator=gen) for _ in range(3))
+        gq, gk = (t / t.norm(dim=-1, keepdim=True) for t in (gq, gk))
+        gq, gk, gv = gq.to(dtype), gk.to(dtype), gv.to(dtype)
+        a, g = torch.rand(B, Hg, N, generator=gen), torch.rand(B, Hg, N, generator=gen)
+        go, _ = h.gdn_step(gq.cuda(), gk.cuda(), gv.cuda(), a.cuda(), g.cuda(), state, slots.cuda(), torch.tensor(new, dtype=torch.int32).cuda())
+        for b, n in enumerate(new):
+            po, pS, bound = gdn_ref(gq[b], gk[b], gv[b], a[b], g[b], states[b], n)
+            got = state[int(slots[b])].cpu()
+            assert float((got.double() - pS).abs().max()) <= bound
+            half = 2.0 ** -8 if dtype == BF else 0.0
+            assert bool(((go[b, :, :n].cpu().double() - po[:, :n]).abs() <= bound + half * (po[:, :n].abs() + bound)).all())
+            states[b] = got
+            steps[b] += 1 if n else 0
+        if step in (3, 5):
+            kept_by = cache.weights.cpu()
+            cut = cache.evict(20, sink=2, recent=N)
+            assert cut == [b for b in range(B) if twin.kv[b] > 20] and cut
+            # every page is free or one rollout's, no rollout has more than it needs
+            assert sorted(cache._free + sum(cache._pages, [])) == list(range(24))
+            assert [len(x) for x in cache._pages] == [-(-n // page) for n in cache.lens]
+            for b in cut:
+                n = twin.kv[b]
+                K, V, W = [], [], []
+                for g2 in range(H):
+                    w = kept_by[b, g2]
+                    mid = sorted(range(2, n - N), key=lambda i: (-float(w[i]), i))[:20 - 2 - N]
+                    keep = list(range(2)) + sorted(mid) + list(range(n - N, n))
+                    K.append(twin.keys[b][g2, keep])
+                    V.append(twin.vals[b][g2, keep])
+                    weights[b, g2, :20], slack[b, g2, :20] = weights[b, g2, keep].clone(), slack[b, g2, keep].clone()
+                    W.append(w[keep])
+                twin.keys[b], twin.vals[b] = torch.stack(K), torch.stack(V)
+                assert torch.equal(cache.weights[b, :, :20].cpu(), torch.stack(W))
+            assert cache.lens == twin.kv
+            for b in range(B):                          # what the pages hold now
+                for i in range(cache.lens[b]):
+                    pg = int(cache.table[b, i // page])
+                    assert torch.equal(cache.k_pages[pg, :, i % page].cpu(), twin.keys[b][:, i])
+                    assert torch.equal(cache.v_pages[pg, :, i % page].cpu(), twin.vals[b][:, i])
+    assert h.hlta_device_status() == 0
+
+
+def test_pages_are_counted(h):
+    cache = h.PagedCache(2, 1, 128, num_pages=5, max_len=80, page=16, weights=True)
+    k = torch.zeros(2, 1, 40, 128, device="cuda", dtype=BF)
+    cache.append(k, k, [40, 20])
+    assert cache.lens == [40, 20] and len(cache._free) == 0
+    for bad in (dict(new_lens=[1, 13]), dict(new_lens=[41, 0]), dict(new_lens=[1]), dict(new_lens=[-1, 0])):
+        with pytest.raises(h.HltaError):
+            cache.append(k, k, **bad)
+        assert cache.lens == [40, 20]
+    with pytest.raises(h.HltaError):
+        cache.evict(16)                                 # no free page to copy to
+    cache.append(k, k, [8, 12])
+    cache.release(1)
+    assert cache.lens == [48, 0] and len(cache._free) == 2
+    assert cache.evict(16) == [0] and cache.lens == [16, 0] and len(cache._free) == 4
+    cache.append(k, k, [40, 0])
+    with pytest.raises(h.HltaError):
+        cache.append(k, k, [25, 0])                     # past max_len
+    q = torch.zeros(2, 2, 40, 128, device="cuda", dtype=BF)
+    assert cache.attend(q).shape == q.shape and h.hlta_device_status() == 0
+    with pytest.raises(h.HltaError):
+        h.PagedCache(1, 1, 128, 4, 64, page=24)
+    plain = h.PagedCache(1, 1, 128, 4, 64)
+    with pytest.raises(h.HltaError):
+        plain.evict(3)
+
+
+def test_rollout_continues_as_one_call(h):
+    """A clip token by token, in chunks, and at once: the same positions see the same keys, so the
+    outputs agree within the roundings of P and the output of both."""
+    H, L = 2, 90
+    q, k, v = (torch.randn(1, H, L, 128, generator=torch.Generator().manual_seed(s)).to(BF).cuda() for s in (1, 2, 3))
+    got = []
+    for sizes in ([90], [1] * 90, [17, 1, 40, 16, 16]):
+        c = h.PagedCache(1, H, 128, 8, 128, page=16)
+        outs, at = [], 0
+        for n in sizes:
+            s = slice(at, at + n)
+            c.append(k[:, :, s].contiguous(), v[:, :, s].contiguous())
+            outs.append(c.attend(q[:, :, s].contiguous()))
+            at += n
+        got.append(torch.cat(outs, 2))
+    bound = 4 * 2.0 ** -8 * float(v.abs().max())
+    assert float((got[0] - got[1]).abs().max()) <= bound and float((got[0] - got[2]).abs().max()) <= bound
+    assert h.hlta_device_status() == 0
