@@ -252,10 +252,10 @@ cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, cudaStream_t s);  
 cudaError_t launch_paged_weights_tc(const PagedAttnArgs &a, cudaStream_t s);                // bf16, after the attention
 size_t paged_attn_tc_bytes();
 cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s);                   // bf16
-// bf16, few packed rows, the weights included
+// few packed rows, the weights included
 bool paged_token_fits(int B, int H, int G, long L, int cap, bool weights);
 size_t paged_token_bytes(int B, int H, int G, long L, int cap, bool weights);
-cudaError_t launch_paged_token(const PagedAttnArgs &a, cudaStream_t s);
+cudaError_t launch_paged_token(const PagedAttnArgs &a, bool bf16, cudaStream_t s);
 
 struct PagedEvictArgs {
     PagedKV c;

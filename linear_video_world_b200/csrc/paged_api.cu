@@ -167,7 +167,7 @@ size_t hlta_paged_attn_workspace_bytes(int B, int Hq, int Hkv, long L, int d, in
     if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || L < 0 || L > (1L << 29) || d < 1 || d > 128 || max_pages < 1 || page < 1 ||
         (long)max_pages * page > (1L << 30) || (dt != HLTA_BF16 && dt != HLTA_FP32))
         return 0;
-    if (dt == HLTA_BF16 && paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, weights != 0))
+    if (paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, weights != 0))
         return pad(paged_token_bytes(B, Hkv, Hq / Hkv, L, max_pages * page, weights != 0)) + 256;
     const size_t lse = weights ? pad((size_t)B * Hq * L * 4) : 0;
     return lse + pad(dt == HLTA_BF16 ? paged_attn_tc_bytes() : paged_attn_simt_bytes(B, Hq, Hkv, L, d, max_pages * page)) + 256;
@@ -212,8 +212,8 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
     a.N = N; a.w = w;
     a.sl2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d)) * 1.4426950408889634f;
     a.ws = ws;
-    if (dt == HLTA_BF16 && paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, w_out != nullptr))
-        return done(launch_paged_token(a, (cudaStream_t)stream), "paged attention");
+    if (paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, w_out != nullptr))
+        return done(launch_paged_token(a, dt == HLTA_BF16, (cudaStream_t)stream), "paged attention");
     if (w_out) {
         // the weights are taken in a second pass, from the log-sum-exp
         if (!lse) a.lse = (float *)ws;

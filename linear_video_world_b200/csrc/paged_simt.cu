@@ -1,17 +1,21 @@
-// Attention of a chunk over a paged cache on the CUDA cores: the HLTA_FP32 element type's path
-// (full single precision throughout), with the accumulated attention weights.
+// Attention of a chunk over a paged cache on the CUDA cores: the HLTA_FP32 element type's path for
+// more than a few rows (full single precision throughout), and its accumulated attention weights.
 //
-// Exact softmax by tiles with a running maximum and sum (log2 domain). A block of four warps owns
-// 16 packed rows of one key head and walks the 64-key tiles of a share of the keys those rows see
+// Exact softmax by 64-key tiles with a running maximum and sum (log2 domain). A block of 256 threads
+// owns 64 packed rows of one key head and walks the key tiles of a share of the keys those rows see
 // (grid z); with more than one share, each leaves (maximum, sum, unnormalised output) in the
-// workspace and a second kernel joins them in the order of the shares. Scores: a lane owns two
-// keys and four rows, K rows padded by one 16-byte word so that the lanes' vector reads fall in
-// different banks: six 16-byte shared reads per 32 multiply-adds. Output: a lane owns four
-// channels, two reads per 16 multiply-adds.
+// workspace and a second kernel joins them in the order of the shares.
+// Bound by the multiply-adds: a thread forms 4 rows x 4 keys of scores (eight 16-byte shared reads
+// per 64 multiply-adds) and 4 rows x 8 channels of output (twelve per 128); 16 threads share a row,
+// so its maximum and sum stay inside half a warp and P inside a warp. Tiles are copied
+// asynchronously into two stages, one ahead. (A first form, 16 rows a block with tiles copied
+// between two barriers, took 590 us where this takes 183: 2 x 200 rows of 8 heads over 700
+// and 3000 keys of 2.)
 // Positions outside the keys that the block's rows see are staged as zeros and masked, whatever
 // the cache holds there.
 #include "hlta_internal.cuh"
 #include "paged.cuh"
+#include "paged_f32.cuh"
 
 #include <algorithm>
 #include <math.h>
@@ -20,177 +24,193 @@ namespace hlta {
 namespace {
 
 using namespace paged;
+using namespace f32;
 
-constexpr int QB = 16, KT = 64, THREADS = 128, RPW = 4;   // rows, keys, threads, rows per warp
+constexpr int TM = 64, TN = 64, THREADS = 256;          // rows, keys, threads
+constexpr int PST = TN + 4;                             // row stride of P
+std::atomic<unsigned long long> g_shared{0}, g_shared_w{0};
 
-__device__ __forceinline__ float warp_max(float x)
+__device__ __forceinline__ float half_max(float x)
 {
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
 }
-__device__ __forceinline__ float warp_sum(float x)
+__device__ __forceinline__ float half_sum(float x)
 {
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float *p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// [rows][d] of the cache from position p0 on into shared memory, row stride `st` floats, channels
-// from d to dp and positions outside [lo, hi) as zeros
-template <typename E>
-__device__ __forceinline__ void stage(const PagedKV &c, const void *pages, int b, int h, int p0, int lo, int hi,
-                                      float *dst, int st, int dp)
+// s[i][j] = row (4 rg + i) . key (kg + 16 j)
+__device__ __forceinline__ void scores(const float *Q, const float *K, int st, int dp, int rg, int kg, float (&s)[4][4])
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int j = warp; j < KT; j += THREADS / 32) {
-        const int p = p0 + j;
-        const bool in = p >= lo && p < hi;
-        const E *src = nullptr;
-        if (in) {
-            const int psz = 1 << c.page_log2;
-            src = (const E *)pages + (((long)page_of(c, b, p) * c.H + h) * psz + (p & (psz - 1))) * c.d;
-        }
-        for (int x = lane; x < dp; x += 32) dst[j * st + x] = in && x < c.d ? to_f(src[x]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int x = 0; x < dp; x += 4) {
+        float4 q[4], k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = *(const float4 *)(Q + (4 * rg + i) * st + x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = *(const float4 *)(K + (kg + 16 * j) * st + x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[i][j] = fmaf(q[i].x, k[j].x, fmaf(q[i].y, k[j].y, fmaf(q[i].z, k[j].z, fmaf(q[i].w, k[j].w, s[i][j]))));
     }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(THREADS) paged_attn_kernel(PagedAttnArgs a, Mask mask, int nsplit, float *ws_m, float *ws_l, float *ws_o)
+// rows [r0, r0 + TM) of the head group's queries, times the scale; rows that are none as zeros
+__device__ __forceinline__ void stage_q(const PagedAttnArgs &a, const FastDiv &byL, const Roll &ro, long head, int R, int r0, float *Q, int st, int dp)
 {
-    extern __shared__ float smem[];
-    const int d = a.c.d, dp = (d + 3) & ~3, kst = dp + 4;
-    float *Qs = smem;                       // [QB][dp]
-    float *Ks = Qs + QB * dp;               // [KT][dp + 4]
-    float *Vs = Ks + KT * kst;              // [KT][dp]
-    float *Ps = Vs + KT * dp;               // per warp [KT][RPW]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.y % a.c.H, b = blockIdx.y / a.c.H;
-    const int R = a.G * (int)a.L;
-    const int r0 = blockIdx.x * QB;
-    const long row0 = (long)blockIdx.y * R + r0;
+    for (int e = threadIdx.x; e < TM * dp; e += THREADS) {
+        const int r = e / dp, x = e - r * dp;
+        const bool in = r0 + r < R && x < a.c.d && frem(r0 + r, byL) < ro.n;
+        Q[r * st + x] = in ? ((const float *)a.q)[(head * R + r0 + r) * a.c.d + x] * a.sl2 : 0.f;
+    }
+}
+
+// the span of the live rows among packed rows [r0, r0 + TM): see the chunk kernel
+__device__ __forceinline__ Span rows_span(const Roll &ro, const FastDiv &byL, const Mask &mask, int r0, int R)
+{
+    const int L = (int)byL.d, r1 = min(r0 + TM, R);
+    int i0 = frem(r0, byL), i1 = i0 + (r1 - 1 - r0);
+    if (i1 >= L) {
+        i0 = 0;
+        i1 = L - 1;
+    }
+    if (i0 >= ro.n) return Span{0, 0};
+    const Span s{span_of(ro, i0, mask).lo, span_of(ro, min(i1, ro.n - 1), mask).hi};
+    return s.hi > s.lo ? s : Span{0, 0};
+}
+
+__global__ void __launch_bounds__(THREADS) paged_attn_f32_kernel(PagedAttnArgs a, FastDiv byL, Mask mask, int nsplit, float *ws_m, float *ws_l, float *ws_o)
+{
+    extern __shared__ __align__(16) float smem[];
+    const int d = a.c.d, dp = (d + 3) & ~3, st = dp + 4;
+    float *Q = smem, *KV = Q + TM * st, *P = KV + 4 * TN * st;          // K and V of two stages
+    const int rg = threadIdx.x >> 4, kg = threadIdx.x & 15;
+    const int h = blockIdx.y % a.c.H, b = blockIdx.y / a.c.H, R = a.G * (int)a.L, r0 = blockIdx.x * TM;
     const Roll ro = roll_of(a.c.kv_lens, a.new_lens, b, (int)a.L, a.c.max_pages << a.c.page_log2);
     if (ro.bad && threadIdx.x == 0) atomicOr(a.c.err, DEVERR_TABLE);
-
-    // the block's rows, and the keys that any of them sees
-    Span sp[RPW];
-    bool live[RPW];
-    int lo = 0x7fffffff, hi = 0;
-    for (int r = 0; r < QB; ++r) {
-        const int i = (r0 + r) % (int)a.L;
-        if (r0 + r >= R || i >= ro.n) continue;
-        const Span s = span_of(ro, i, mask);
-        if (s.hi > s.lo) {
-            lo = min(lo, s.lo);
-            hi = max(hi, s.hi);
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < RPW; ++r) {
-        const int rr = r0 + warp * RPW + r, i = rr % (int)a.L;
-        live[r] = rr < R && i < ro.n;
-        sp[r] = live[r] ? span_of(ro, i, mask) : Span{0, 0};
-    }
-    const int t_lo = hi > lo ? lo / KT : 0, nt = hi > lo ? (hi + KT - 1) / KT - t_lo : 0;
+    const Span u = rows_span(ro, byL, mask, r0, R);
+    const int t_lo = u.lo / TN, nt = u.hi > u.lo ? (u.hi + TN - 1) / TN - t_lo : 0;
     const int ta = t_lo + (int)((long)nt * blockIdx.z / nsplit), tb = t_lo + (int)((long)nt * (blockIdx.z + 1) / nsplit);
-
-    for (int e = threadIdx.x; e < QB * dp; e += THREADS) {
-        const int r = e / dp, x = e % dp;
-        Qs[e] = r0 + r < R && x < d ? to_f(((const E *)a.q)[(row0 + r) * d + x]) * a.sl2 : 0.f;
-    }
-    float m[RPW], l[RPW], acc[RPW][4];
+    Span sp[4];
+    bool live[4];
+    float m[4], l[4], acc[4][8];
 #pragma unroll
-    for (int r = 0; r < RPW; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-        for (int x = 0; x < 4; ++x) acc[r][x] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 4 * rg + i, tok = frem(r, byL);
+        live[i] = r < R && tok < ro.n;
+        sp[i] = live[i] ? span_of(ro, tok, mask) : Span{0, 0};
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[i][x] = 0.f;
     }
-    float *P = Ps + warp * KT * RPW;
+    auto load = [&](int t) {
+        float *k = KV + (t & 1) * 2 * TN * st;
+        copy_tile<TN, THREADS>(a.c, b, h, t * TN, u, k, k + TN * st, st, dp);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (tb > ta) load(ta);
+    stage_q(a, byL, ro, blockIdx.y, R, r0, Q, st, dp);
     for (int t = ta; t < tb; ++t) {
-        const int p0 = t * KT;
-        __syncthreads();
-        stage<E>(a.c, a.c.k, b, h, p0, lo, hi, Ks, kst, dp);
-        stage<E>(a.c, a.c.v, b, h, p0, lo, hi, Vs, dp, dp);
-        __syncthreads();
-        float s[RPW][2];
-#pragma unroll
-        for (int r = 0; r < RPW; ++r) s[r][0] = s[r][1] = 0.f;
-        const float *k0 = Ks + lane * kst, *k1 = Ks + (lane + 32) * kst, *q = Qs + warp * RPW * dp;
-        for (int x = 0; x < dp; x += 4) {
-            const float4 a0 = *(const float4 *)(k0 + x), a1 = *(const float4 *)(k1 + x);
-#pragma unroll
-            for (int r = 0; r < RPW; ++r) {
-                const float4 v = *(const float4 *)(q + r * dp + x);
-                s[r][0] = fmaf(v.x, a0.x, fmaf(v.y, a0.y, fmaf(v.z, a0.z, fmaf(v.w, a0.w, s[r][0]))));
-                s[r][1] = fmaf(v.x, a1.x, fmaf(v.y, a1.y, fmaf(v.z, a1.z, fmaf(v.w, a1.w, s[r][1]))));
-            }
+        if (t + 1 < tb) {
+            load(t + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
+        __syncthreads();
+        const float *K = KV + (t & 1) * 2 * TN * st, *V = K + TN * st;
+        float s[4][4];
+        scores(Q, K, st, dp, rg, kg, s);
 #pragma unroll
-        for (int r = 0; r < RPW; ++r) {
-            const int pa = p0 + lane, pb = pa + 32;
-            if (pa < sp[r].lo || pa >= sp[r].hi) s[r][0] = -INFINITY;
-            if (pb < sp[r].lo || pb >= sp[r].hi) s[r][1] = -INFINITY;
-            const float mn = fmaxf(m[r], warp_max(fmaxf(s[r][0], s[r][1])));
-            const float base = mn == -INFINITY ? 0.f : mn;
-            const float p_a = exp2f(s[r][0] - base), p_b = exp2f(s[r][1] - base), f = exp2f(m[r] - base);
-            l[r] = l[r] * f + warp_sum(p_a + p_b);
-            m[r] = mn;
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) acc[r][x] *= f;
-            P[lane * RPW + r] = p_a;
-            P[(lane + 32) * RPW + r] = p_b;
+            for (int j = 0; j < 4; ++j) {
+                const int p = t * TN + kg + 16 * j;
+                if (p < sp[i].lo || p >= sp[i].hi) s[i][j] = -INFINITY;
+            }
+            const float mn = fmaxf(m[i], half_max(fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]))));
+            const float base = mn == -INFINITY ? 0.f : mn, f = exp2f(m[i] - base);
+            m[i] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - base);
+                sum += p;
+                P[(4 * rg + i) * PST + kg + 16 * j] = p;
+            }
+            l[i] = fmaf(l[i], f, sum);              // this thread's keys; joined at the end
+#pragma unroll
+            for (int x = 0; x < 8; ++x) acc[i][x] *= f;
         }
         __syncwarp();
-        if (lane * 4 < dp) {
-#pragma unroll 4
-            for (int j = 0; j < KT; ++j) {
-                const float4 p = *(const float4 *)(P + j * RPW);
-                const float4 v = *(const float4 *)(Vs + j * dp + lane * 4);
-                const float pr[4] = {p.x, p.y, p.z, p.w};
+        if (4 * kg < dp) {
+            const bool second = 64 + 4 * kg < dp;
+#pragma unroll 2
+            for (int k = 0; k < TN; k += 4) {
+                float4 p[4];
 #pragma unroll
-                for (int r = 0; r < RPW; ++r) {
-                    acc[r][0] = fmaf(pr[r], v.x, acc[r][0]);
-                    acc[r][1] = fmaf(pr[r], v.y, acc[r][1]);
-                    acc[r][2] = fmaf(pr[r], v.z, acc[r][2]);
-                    acc[r][3] = fmaf(pr[r], v.w, acc[r][3]);
+                for (int i = 0; i < 4; ++i) p[i] = *(const float4 *)(P + (4 * rg + i) * PST + k);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const float4 v0 = *(const float4 *)(V + (k + kk) * st + 4 * kg);
+                    const float4 v1 = second ? *(const float4 *)(V + (k + kk) * st + 64 + 4 * kg) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                        acc[i][0] = fmaf(w, v0.x, acc[i][0]);
+                        acc[i][1] = fmaf(w, v0.y, acc[i][1]);
+                        acc[i][2] = fmaf(w, v0.z, acc[i][2]);
+                        acc[i][3] = fmaf(w, v0.w, acc[i][3]);
+                        acc[i][4] = fmaf(w, v1.x, acc[i][4]);
+                        acc[i][5] = fmaf(w, v1.y, acc[i][5]);
+                        acc[i][6] = fmaf(w, v1.z, acc[i][6]);
+                        acc[i][7] = fmaf(w, v1.w, acc[i][7]);
+                    }
                 }
             }
         }
-        __syncwarp();
+        __syncthreads();
     }
     const long rows = (long)a.B * a.c.H * R;
 #pragma unroll
-    for (int r = 0; r < RPW; ++r) {
-        if (!live[r]) continue;
-        const long row = row0 + warp * RPW + r;
-        if (nsplit == 1) {
-            const float inv = l[r] > 0.f ? 1.f / l[r] : l[r] == l[r] ? 0.f : l[r];
-            for (int x = 0; x < 4; ++x)
-                if (lane * 4 + x < d) put((E *)a.o + row * d + lane * 4 + x, acc[r][x] * inv);
-            if (a.lse && lane == 0) a.lse[row] = (m[r] + log2f(l[r])) * 0.69314718055994531f;
-        } else {
-            const long at = blockIdx.z * rows + row;
-            for (int x = 0; x < 4; ++x)
-                if (lane * 4 + x < d) ws_o[at * d + lane * 4 + x] = acc[r][x];
-            if (lane == 0) {
-                ws_m[at] = m[r];
-                ws_l[at] = l[r];
+    for (int i = 0; i < 4; ++i) {
+        const float sum = half_sum(l[i]);
+        if (!live[i]) continue;
+        const long row = (long)blockIdx.y * R + r0 + 4 * rg + i;
+        const float inv = nsplit > 1 ? 1.f : sum > 0.f ? 1.f / sum : sum == sum ? 0.f : sum;
+        float *dst = nsplit > 1 ? ws_o + (blockIdx.z * rows + row) * d : (float *)a.o + row * d;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int ch = (x >> 2) * 64 + 4 * kg + (x & 3);
+            if (ch < d) dst[ch] = acc[i][x] * inv;
+        }
+        if (kg == 0) {
+            if (nsplit > 1) {
+                ws_m[blockIdx.z * rows + row] = m[i];
+                ws_l[blockIdx.z * rows + row] = sum;
+            } else if (a.lse) {
+                a.lse[row] = (m[i] + log2f(sum)) * 0.69314718055994531f;
             }
         }
     }
 }
 
 // Joins the shares of a row, one warp per row.
-template <typename E>
-__global__ void __launch_bounds__(THREADS) paged_join_kernel(PagedAttnArgs a, int nsplit, const float *ws_m, const float *ws_l, const float *ws_o)
+__global__ void __launch_bounds__(128) paged_join_f32_kernel(PagedAttnArgs a, FastDiv byL, int nsplit, const float *ws_m, const float *ws_l, const float *ws_o)
 {
     const int lane = threadIdx.x & 31;
-    const long rows = (long)a.B * a.c.H * a.G * a.L;
-    const long row = (long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
+    const long R = a.G * a.L, rows = (long)a.B * a.c.H * R;
+    const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= rows) return;
-    const int b = (int)(row / ((long)a.c.H * a.G * a.L)), i = (int)(row % a.L), d = a.c.d;
+    const int b = (int)(row / (a.c.H * R)), i = frem((int)(row % R), byL), d = a.c.d;
     const Roll ro = roll_of(a.c.kv_lens, a.new_lens, b, (int)a.L, a.c.max_pages << a.c.page_log2);
     if (i >= ro.n) return;
     float m = -INFINITY;
@@ -206,126 +226,66 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(PagedAttnArgs a, in
     }
     const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
     for (int x = 0; x < 4; ++x)
-        if (lane + 32 * x < d) put((E *)a.o + row * d + lane + 32 * x, acc[x] * inv);
+        if (lane + 32 * x < d) ((float *)a.o)[row * d + lane + 32 * x] = acc[x] * inv;
     if (a.lse && lane == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // Accumulated attention weights: a block owns 64 keys of one key head and sums, over every row of
-// the head group that sees them, 2^(score - lse) in the order of the rows; each warp takes every
-// fourth group of four rows, and the four partial sums are joined at the end.
-template <typename E>
-__global__ void __launch_bounds__(THREADS) paged_weights_kernel(PagedAttnArgs a, Mask mask)
+// the head group that sees them, 2^(score - lse): blocks of 64 rows in turn, a thread its four keys over
+// its four rows of each, the 16 threads of a key joined at the end in the order of their rows.
+__global__ void __launch_bounds__(THREADS) paged_weights_f32_kernel(PagedAttnArgs a, FastDiv byL, Mask mask)
 {
-    extern __shared__ float smem[];
-    const int d = a.c.d, dp = (d + 3) & ~3, kst = dp + 4;
-    float *Ks = smem;                       // [KT][dp + 4]
-    float *Qs = Ks + KT * kst;              // [QB][dp]
-    float *Sum = Qs + QB * dp;              // [warps][KT]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.y % a.c.H, b = blockIdx.y / a.c.H;
-    const int cap = a.c.max_pages << a.c.page_log2;
+    extern __shared__ __align__(16) float smem[];
+    const int d = a.c.d, dp = (d + 3) & ~3, st = dp + 4;
+    float *Q = smem, *K = Q + TM * st, *Sum = K + TN * st;              // Sum: [16 row groups][64 keys]
+    const int rg = threadIdx.x >> 4, kg = threadIdx.x & 15;
+    const int h = blockIdx.y % a.c.H, b = blockIdx.y / a.c.H, cap = a.c.max_pages << a.c.page_log2, p0 = blockIdx.x * TN;
     const Roll ro = roll_of(a.c.kv_lens, a.new_lens, b, (int)a.L, cap);
-    const int p0 = blockIdx.x * KT;
     if (p0 >= ro.kv) return;
     const int R = a.G * (int)a.L;
-    const long row0 = (long)blockIdx.y * R;
-    stage<E>(a.c, a.c.k, b, h, p0, 0, ro.n > 0 ? ro.kv : 0, Ks, kst, dp);
-    float sum[2] = {0.f, 0.f};
-    for (int rb = 0; rb < R; rb += QB) {
-        // a block of rows that sees none of these keys is skipped by all threads
-        bool any = false;
-        for (int r = rb; r < min(R, rb + QB); ++r) {
-            const int i = r % (int)a.L;
-            const Span s = i < ro.n ? span_of(ro, i, mask) : Span{0, 0};
-            any = any || (s.lo < p0 + KT && s.hi > p0 && s.hi > s.lo);
-        }
-        if (!any) continue;
+    copy_tile<TN, THREADS>(a.c, b, h, p0, ro.n > 0 ? Span{0, ro.kv} : Span{0, 0}, K, nullptr, st, dp);
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int rb = 0; rb < R; rb += TM) {
+        const Span u = rows_span(ro, byL, mask, rb, R);
+        if (u.lo >= p0 + TN || u.hi <= p0) continue;    // seen by none of these rows: all threads alike
         __syncthreads();
-        for (int e = threadIdx.x; e < QB * dp; e += THREADS) {
-            const int r = e / dp, x = e % dp;
-            Qs[e] = rb + r < R && x < d ? to_f(((const E *)a.q)[(row0 + rb + r) * d + x]) * a.sl2 : 0.f;
-        }
+        stage_q(a, byL, ro, blockIdx.y, R, rb, Q, st, dp);
         __syncthreads();
-        float s[RPW][2];
+        float s[4][4];
+        scores(Q, K, st, dp, rg, kg, s);
 #pragma unroll
-        for (int r = 0; r < RPW; ++r) s[r][0] = s[r][1] = 0.f;
-        const float *k0 = Ks + lane * kst, *k1 = Ks + (lane + 32) * kst, *q = Qs + warp * RPW * dp;
-        for (int x = 0; x < dp; x += 4) {
-            const float4 a0 = *(const float4 *)(k0 + x), a1 = *(const float4 *)(k1 + x);
+        for (int i = 0; i < 4; ++i) {
+            const int r = rb + 4 * rg + i, tok = frem(r, byL);
+            if (r >= R || tok >= ro.n) continue;
+            const Span v = span_of(ro, tok, mask);
+            const float z = a.lse[(long)blockIdx.y * R + r] * 1.4426950408889634f;
 #pragma unroll
-            for (int r = 0; r < RPW; ++r) {
-                const float4 v = *(const float4 *)(q + r * dp + x);
-                s[r][0] = fmaf(v.x, a0.x, fmaf(v.y, a0.y, fmaf(v.z, a0.z, fmaf(v.w, a0.w, s[r][0]))));
-                s[r][1] = fmaf(v.x, a1.x, fmaf(v.y, a1.y, fmaf(v.z, a1.z, fmaf(v.w, a1.w, s[r][1]))));
+            for (int j = 0; j < 4; ++j) {
+                const int p = p0 + kg + 16 * j;
+                if (p >= v.lo && p < v.hi) sum[j] += exp2f(s[i][j] - z);
             }
         }
-#pragma unroll
-        for (int r = 0; r < RPW; ++r) {
-            const int rr = rb + warp * RPW + r, i = rr % (int)a.L;
-            if (rr >= R || i >= ro.n) continue;
-            const Span v = span_of(ro, i, mask);
-            if (v.hi <= v.lo) continue;
-            const float z = a.lse[row0 + rr] * 1.4426950408889634f;
-            const int pa = p0 + lane, pb = pa + 32;
-            if (pa >= v.lo && pa < v.hi) sum[0] += exp2f(s[r][0] - z);
-            if (pb >= v.lo && pb < v.hi) sum[1] += exp2f(s[r][1] - z);
-        }
     }
-    Sum[warp * KT + lane] = sum[0];
-    Sum[warp * KT + lane + 32] = sum[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) Sum[rg * TN + kg + 16 * j] = sum[j];
     __syncthreads();
     const int p = p0 + threadIdx.x;
-    if (threadIdx.x < KT && p < ro.kv) {
+    if (threadIdx.x < TN && p < ro.kv) {
         float t = 0.f;
-        for (int w = 0; w < THREADS / 32; ++w) t += Sum[w * KT + threadIdx.x];
+        for (int g = 0; g < 16; ++g) t += Sum[g * TN + threadIdx.x];
         const long at = (long)blockIdx.y * cap + p;
         if (a.w_in && p < ro.h) t = fmaf(a.decay, a.w_in[at], t);
         a.w_out[at] = t;
     }
 }
 
-// shares of the keys: enough blocks for four per SM, no share under two tiles
+// shares of the keys: enough blocks for two rounds of the SMs, no share under two tiles
 int splits_of(int B, int Hkv, long R, int max_keys)
 {
-    const long blocks = (long)B * Hkv * ((R + QB - 1) / QB);
-    const long want = (148L * 4 + blocks - 1) / std::max(blocks, 1L);
-    return (int)std::max(1L, std::min({want, (long)(max_keys + 2 * KT - 1) / (2 * KT), 64L}));
-}
-
-template <typename E>
-cudaError_t run(const PagedAttnArgs &a, cudaStream_t s)
-{
-    const long R = a.G * a.L, rows = (long)a.B * a.c.H * R;
-    const int keys = a.c.max_pages << a.c.page_log2;
-    const int ns = splits_of(a.B, a.c.H, R, keys);
-    const int dp = (a.c.d + 3) & ~3;
-    if (R > (1L << 30) || (long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
-    float *m = (float *)a.ws, *l = m + ns * rows, *o = l + ns * rows;
-    const size_t sm = (size_t)(QB * dp + KT * (dp + 4) + KT * dp + THREADS / 32 * KT * RPW) * 4;
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-    if (e != cudaSuccess) return e;
-    if (R > 0) {
-        const dim3 grid((unsigned)((R + QB - 1) / QB), (unsigned)(a.B * a.c.H), (unsigned)ns);
-        paged_attn_kernel<E><<<grid, THREADS, sm, s>>>(a, mask_of(a.N, a.w), ns, m, l, o), note_launch();
-    }
-    if (R > 0 && ns > 1) {
-        const long blocks = (rows + THREADS / 32 - 1) / (THREADS / 32);
-        if (blocks > 0x7fffffffL) return cudaErrorNotSupported;
-        paged_join_kernel<E><<<(unsigned)blocks, THREADS, 0, s>>>(a, ns, m, l, o), note_launch();
-    }
-    return cudaGetLastError();
-}
-
-template <typename E>
-cudaError_t run_weights(const PagedAttnArgs &a, cudaStream_t s)
-{
-    const int dp = (a.c.d + 3) & ~3, keys = a.c.max_pages << a.c.page_log2;
-    if ((long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
-    const size_t sw = (size_t)(KT * (dp + 4) + QB * dp + THREADS / 32 * KT) * 4;
-    cudaError_t e = cudaFuncSetAttribute(paged_weights_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sw);
-    if (e != cudaSuccess) return e;
-    paged_weights_kernel<E><<<dim3((unsigned)((keys + KT - 1) / KT), (unsigned)(a.B * a.c.H)), THREADS, sw, s>>>(a, mask_of(a.N, a.w)), note_launch();
-    return cudaGetLastError();
+    const long blocks = (long)B * Hkv * ((R + TM - 1) / TM);
+    const long want = (148L * 2 + blocks - 1) / std::max(blocks, 1L);
+    return (int)std::max(1L, std::min({want, (long)(max_keys + 2 * TN - 1) / (2 * TN), 64L}));
 }
 
 }  // namespace
@@ -337,8 +297,35 @@ size_t paged_attn_simt_bytes(int B, int Hq, int Hkv, long L, int d, int max_keys
     return ns > 1 ? (size_t)ns * rows * (d + 2) * 4 : 0;
 }
 
-cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s) { return run<float>(a, s); }
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s)
+{
+    const long R = a.G * a.L, rows = (long)a.B * a.c.H * R;
+    const int ns = splits_of(a.B, a.c.H, R, a.c.max_pages << a.c.page_log2), st = ((a.c.d + 3) & ~3) + 4;
+    if (R < 1) return cudaSuccess;
+    if (R > (1L << 30) || (long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
+    float *m = (float *)a.ws, *l = m + ns * rows, *o = l + ns * rows;
+    cudaError_t e = allow_shared((const void *)paged_attn_f32_kernel, (size_t)((TM + 4 * TN) * 132 + TM * PST) * 4, g_shared);
+    if (e != cudaSuccess) return e;
+    const FastDiv byL = fast_div((unsigned)a.L);
+    const dim3 grid((unsigned)((R + TM - 1) / TM), (unsigned)(a.B * a.c.H), (unsigned)ns);
+    paged_attn_f32_kernel<<<grid, THREADS, (size_t)((TM + 4 * TN) * st + TM * PST) * 4, s>>>(a, byL, mask_of(a.N, a.w), ns, m, l, o), note_launch();
+    if (ns > 1) {
+        const long blocks = (rows + 3) / 4;
+        if (blocks > 0x7fffffffL) return cudaErrorNotSupported;
+        paged_join_f32_kernel<<<(unsigned)blocks, 128, 0, s>>>(a, byL, ns, m, l, o), note_launch();
+    }
+    return cudaGetLastError();
+}
 
-cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, cudaStream_t s) { return run_weights<float>(a, s); }
+cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, cudaStream_t s)
+{
+    const int keys = a.c.max_pages << a.c.page_log2, st = ((a.c.d + 3) & ~3) + 4;
+    if ((long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
+    cudaError_t e = allow_shared((const void *)paged_weights_f32_kernel, (size_t)((TM + TN) * 132 + 16 * TN) * 4, g_shared_w);
+    if (e != cudaSuccess) return e;
+    paged_weights_f32_kernel<<<dim3((unsigned)((keys + TN - 1) / TN), (unsigned)(a.B * a.c.H)), THREADS, (size_t)((TM + TN) * st + 16 * TN) * 4, s>>>(
+        a, fast_div((unsigned)std::max(a.L, 1L)), mask_of(a.N, a.w)), note_launch();
+    return cudaGetLastError();
+}
 
 }  // namespace hlta

@@ -1,5 +1,5 @@
-// Attention of a few tokens over a paged cache (at most 16 packed rows of a key head), bf16, head
-// dim 128, with the accumulated attention weights.
+// Attention of a few tokens over a paged cache (at most 16 packed rows of a key head), with the
+// accumulated attention weights. bf16, head dim 128, on the tensor cores; fp32 on the CUDA cores.
 //
 // Bound by HBM: every key and value is read once, 512 bytes for at most 16 rows. The division of
 // the work is that of paged.cuh with single blocks as gangs, two blocks per SM: an equal number of
@@ -16,8 +16,14 @@
 //
 // What the cache holds where no row looks: as in the chunk kernel, scores are masked before use and
 // values outside the span of the rows are zeroed in shared memory.
+//
+// fp32 tensors (any d <= 128): the same division and the same second kernel; 32-key tiles copied
+// asynchronously into three stages, four warps of eight keys each. A score is summed by four lanes
+// (32 channels each), a lane owns four channels of the output; rows in groups of 4 or 16, so that few
+// rows do not pay for 16. Bound by HBM for few rows, by shared-memory reads for 16.
 #include "hlta_internal.cuh"
 #include "paged.cuh"
+#include "paged_f32.cuh"
 #include "sm100_ptx.cuh"
 #include "tc_ptx.cuh"
 
@@ -48,10 +54,10 @@ struct Params {
     PagedKV c;
     int G, R;
     float sl2;
-    const __nv_bfloat16 *q;
-    __nv_bfloat16 *o;
+    const void *q;
+    void *o;
     float *lse;
-    float *part;                    // [block][2][64 registers][32 lanes]
+    float *part;                    // bf16: [block][2][64 registers][32 lanes]; fp32: [block][2][16 rows][128]
     float2 *ml;                     // [block][2][16 rows]
     float *scores;                  // [b][h][R][cap], log2 units; null without weights
     float2 *whole;                  // [b][h][16 rows] (maximum, sum) of heads that one block had whole
@@ -211,7 +217,7 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
             v[j] = live[j] ? span_of(x.x.r, i, p.line.mask) : Span{0, 0};
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t *s = reinterpret_cast<const uint32_t *>(p.q + (row0 + r) * D + 16 * kk + 2 * c);
+                const uint32_t *s = reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)p.q + (row0 + r) * D + 16 * kk + 2 * c);
                 qa[kk][j] = live[j] ? s[0] : 0u;
                 qa[kk][2 + j] = live[j] ? s[4] : 0u;
             }
@@ -340,7 +346,7 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                     const float inv = l[j] > 0.f ? 1.f / l[j] : l[j] == l[j] ? 0.f : l[j];
 #pragma unroll
                     for (int n = 0; n < 16; ++n)
-                        *reinterpret_cast<uint32_t *>(p.o + row * D + 8 * n + 2 * c) = tc::pack_bf16(o[n][2 * j] * inv, o[n][2 * j + 1] * inv);
+                        *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)p.o + row * D + 8 * n + 2 * c) = tc::pack_bf16(o[n][2 * j] * inv, o[n][2 * j + 1] * inv);
                     if (p.lse && c == 0) p.lse[row] = (m[j] + log2f(l[j])) * 0.69314718055994531f;
                     if (p.scores && c == 0) p.whole[(long)(x.b * p.c.H + x.h) * MROWS + g + 8 * j] = make_float2(m[j], l[j]);
                 }
@@ -360,11 +366,159 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     }
 }
 
+// fp32: RB rows at a time (4 or 16).
+constexpr int FN = 32, FSTAGES = 3, FT = 128;           // keys per tile, stages, threads
+std::atomic<unsigned long long> g_shared_f4{0}, g_shared_f16{0};
+constexpr size_t f32_floats(int rb, int st) { return (size_t)FSTAGES * 2 * FN * st + (size_t)rb * st + 4 * 8 * rb; }
+
+template <int RB>
+__global__ void __launch_bounds__(FT) paged_token_f32_kernel(const __grid_constant__ Params p)
+{
+    extern __shared__ __align__(16) float fs[];
+    __shared__ Place s_place;
+    __shared__ float2 s_ml[4][RB];
+    const int d = p.c.d, dp = (d + 3) & ~3, st = dp + 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *KV = fs, *Q = KV + FSTAGES * 2 * FN * st, *P = Q + RB * st + warp * 8 * RB;     // P: this warp's [8 keys][RB]
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (warp == 0) {
+        const Place c = place_of<FN>(p.line, blockIdx.x);
+        if (lane == 0) s_place = c;
+    }
+    __syncthreads();
+    Place at = s_place;
+    Piece<FN> x;
+    const int key = 8 * warp + (lane >> 2), dq = 4 * (lane & 3);            // this lane's key of a tile, first channel
+    for (int piece = 0; next_piece<FN>(p.line, at, x); ++piece) {
+        if (x.x.r.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
+        const Span u{span_of(x.x.r, 0, p.line.mask).lo, span_of(x.x.r, x.x.r.n - 1, p.line.mask).hi};
+        const long row0 = (long)(x.b * p.c.H + x.h) * p.R;
+        auto load = [&](int t) {
+            if (t < x.tb) {
+                float *k = KV + (t % FSTAGES) * 2 * FN * st;
+                f32::copy_tile<FN, FT>(p.c, x.b, x.h, t * FN, u, k, k + FN * st, st, dp);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        __syncthreads();                    // the piece before this one was read
+        load(x.ta);
+        load(x.ta + 1);
+        for (int e = threadIdx.x; e < RB * dp; e += FT) {
+            const int r = e / dp, y = e - r * dp;
+            const bool in = r < p.R && y < d && frem(r, p.line.byL) < x.x.r.n;
+            Q[r * st + y] = in ? ((const float *)p.q)[(row0 + r) * d + y] * p.sl2 : 0.f;
+        }
+        float m[RB], l[RB], acc[RB][4];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) acc[r][y] = 0.f;
+        }
+        for (int t = x.ta; t < x.tb; ++t) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+            load(t + 2);                    // into the stage of tile t - 1, which all have read
+            const float *K = KV + (t % FSTAGES) * 2 * FN * st, *V = K + FN * st;
+            float s[RB];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) s[r] = 0.f;
+#pragma unroll 2
+            for (int y = dq; y < dp; y += 16) {
+                const float4 k = *(const float4 *)(K + key * st + y);
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    const float4 q = *(const float4 *)(Q + r * st + y);
+                    s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+                }
+            }
+            const int pos = t * FN + key;
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+                s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+                const int i = frem(r, p.line.byL);
+                const bool live = r < p.R && i < x.x.r.n;
+                const Span v = live ? span_of(x.x.r, i, p.line.mask) : Span{0, 0};
+                if (pos < v.lo || pos >= v.hi) s[r] = -INFINITY;
+                if (p.scores && live && pos < x.x.r.kv && (lane & 3) == 0) p.scores[(row0 + r) * p.line.cap + pos] = s[r];
+                float mx = s[r];
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn, f = exp2f(m[r] - base);
+                m[r] = mn;
+                s[r] = exp2f(s[r] - base);
+                l[r] = fmaf(l[r], f, s[r]);         // this lane's key; joined at the end
+#pragma unroll
+                for (int y = 0; y < 4; ++y) acc[r][y] *= f;
+                if ((lane & 3) == 0) P[(lane >> 2) * RB + r] = s[r];
+            }
+            __syncwarp();
+            if (4 * lane < dp) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float4 v = *(const float4 *)(V + (8 * warp + k) * st + 4 * lane);
+#pragma unroll
+                    for (int r = 0; r < RB; r += 4) {
+                        const float4 w = *(const float4 *)(P + k * RB + r);
+                        const float ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            acc[r + j][0] = fmaf(ws[j], v.x, acc[r + j][0]);
+                            acc[r + j][1] = fmaf(ws[j], v.y, acc[r + j][1]);
+                            acc[r + j][2] = fmaf(ws[j], v.z, acc[r + j][2]);
+                            acc[r + j][3] = fmaf(ws[j], v.w, acc[r + j][3]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        // join the four warps through the stages' memory, in their order
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        float *M = KV;                      // [warp][RB][128]
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 4);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
+            if (lane == 0) s_ml[warp][r] = make_float2(m[r], l[r]);
+            if (4 * lane < dp) *(float4 *)(M + (warp * RB + r) * D + 4 * lane) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+        }
+        __syncthreads();
+        const long sl = (long)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
+        for (int r = 0; r < min(RB, p.R); ++r) {
+            if (frem(r, p.line.byL) >= x.x.r.n) continue;
+            const float mm = fmaxf(fmaxf(s_ml[0][r].x, s_ml[1][r].x), fmaxf(s_ml[2][r].x, s_ml[3][r].x)), base = mm == -INFINITY ? 0.f : mm;
+            float o = 0.f, ll = 0.f;
+            for (int w = 0; w < 4; ++w) {
+                const float f = exp2f(s_ml[w][r].x - base);
+                ll = fmaf(s_ml[w][r].y, f, ll);
+                if (threadIdx.x < d) o = fmaf(M[(w * RB + r) * D + threadIdx.x], f, o);
+            }
+            if (x.whole) {
+                const float inv = ll > 0.f ? 1.f / ll : ll == ll ? 0.f : ll;
+                if (threadIdx.x < d) ((float *)p.o)[(row0 + r) * d + threadIdx.x] = o * inv;
+                if (threadIdx.x == 0) {
+                    if (p.lse) p.lse[row0 + r] = (mm + log2f(ll)) * 0.69314718055994531f;
+                    if (p.scores) p.whole[(long)(x.b * p.c.H + x.h) * MROWS + r] = make_float2(mm, ll);
+                }
+            } else {
+                p.part[(sl * MROWS + r) * D + threadIdx.x] = o;
+                if (threadIdx.x == 0) p.ml[sl * MROWS + r] = make_float2(mm, ll);
+            }
+        }
+    }
+}
+
 // Joins the pieces of heads whose keys were cut, in the order of the blocks, and turns the scores
 // into weights. Block (x, b * H + h): keys x * KEYS ... of that head; block x = 0 also joins. The
 // pieces' factors come first, a lane per piece, so that the sums over pieces wait for no chain of
 // loads.
 constexpr int JT = 256, MAXP = 512;                     // threads; pieces of a head (blocks of the first kernel)
+template <typename E, int TK>
 __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_constant__ Params p)
 {
     __shared__ float s_f[MAXP][MROWS];      // factor of a piece's row
@@ -374,7 +528,7 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
     const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
     const int k0 = blockIdx.x * KEYS;
     if (blockIdx.x > 0 && k0 >= ro.kv) return;
-    const Holders hd = holders_of<BN>(p.line, 0, b, h);
+    const Holders hd = holders_of<TK>(p.line, 0, b, h);
     const bool cut = hd.T > 0 && hd.g0 != hd.g1;
     if (blockIdx.x == 0 && ro.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the first kernel's results from here on
@@ -404,18 +558,20 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
     }
     __syncthreads();
     if (blockIdx.x == 0 && (hd.T == 0 || cut)) {
-        // An item is eight channels of a row: a pair of registers of the fragment in four lanes, 16
-        // items a row. With few rows several lanes share an item and take its pieces in turn.
+        // An item is eight channels of a row, 16 items a row (bf16: a pair of registers of the fragment
+        // in four lanes). With few rows several lanes share an item and take its pieces in turn.
         int share = 1;
         while (share < 16 && 2 * share * p.R <= JT / 16) share *= 2;
         const int item = threadIdx.x / share, r = item >> 4, n = item & 15;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
         if (r < p.R) {
-            // row r of the fragment: lanes 4 (r & 7) .., registers 4 n + 2 (r >> 3) and the next
-            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (4 * n + 2 * (r >> 3)) * 8 + (r & 7);
+            // bf16: row r of the fragment is lanes 4 (r & 7) .., registers 4 n + 2 (r >> 3) and the next
+            // (even and odd channels); fp32: the two words of the row's channels
+            constexpr int next = sizeof(E) == 2 ? 8 : 1;
+            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (sizeof(E) == 2 ? (4 * n + 2 * (r >> 3)) * 8 + (r & 7) : r * 32 + 2 * n);
 #pragma unroll 8
             for (int i = threadIdx.x % share; i < np; i += share) {
-                const float4 u = src[slot(i) * 512], v = src[slot(i) * 512 + 8];
+                const float4 u = src[slot(i) * 512], v = src[slot(i) * 512 + next];
                 const float f = s_f[i][r];
                 a.x = fmaf(u.x, f, a.x); a.y = fmaf(u.y, f, a.y); a.z = fmaf(u.z, f, a.z); a.w = fmaf(u.w, f, a.w);
                 d.x = fmaf(v.x, f, d.x); d.y = fmaf(v.y, f, d.y); d.z = fmaf(v.z, f, d.z); d.w = fmaf(v.w, f, d.w);
@@ -429,8 +585,12 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
         }
         if (threadIdx.x % share == 0 && r < p.R && frem(r, p.line.byL) < ro.n) {
             const float inv = s_ml[r].y;
-            *reinterpret_cast<uint4 *>(p.o + (row0 + r) * D + 8 * n) =
-                make_uint4(tc::pack_bf16(a.x * inv, d.x * inv), tc::pack_bf16(a.y * inv, d.y * inv), tc::pack_bf16(a.z * inv, d.z * inv), tc::pack_bf16(a.w * inv, d.w * inv));
+            if constexpr (sizeof(E) == 4) {
+                const float y[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+                for (int x = 0; x < 8; ++x)
+                    if (8 * n + x < p.c.d) ((float *)p.o)[(row0 + r) * p.c.d + 8 * n + x] = y[x] * inv;
+            } else
+                *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.o + (row0 + r) * D + 8 * n) = make_uint4(tc::pack_bf16(a.x * inv, d.x * inv), tc::pack_bf16(a.y * inv, d.y * inv), tc::pack_bf16(a.z * inv, d.z * inv), tc::pack_bf16(a.w * inv, d.w * inv));
         }
     }
     if (!p.w_out) return;
@@ -490,34 +650,46 @@ size_t paged_token_bytes(int B, int H, int G, long L, int cap, bool weights)
     return part_bytes() + (weights ? (size_t)B * H * (G * L * (size_t)cap * 4 + MROWS * 8) : 0);
 }
 
-cudaError_t launch_paged_token(const PagedAttnArgs &a, cudaStream_t s)
+cudaError_t launch_paged_token(const PagedAttnArgs &a, bool bf16, cudaStream_t s)
 {
     const long kv_rows = a.c.num_pages * a.c.H << a.c.page_log2;
-    if (kv_rows + BN >= (1L << 31) || (long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
-    const uint32_t box = (uint32_t)std::min(1 << a.c.page_log2, BN);
-    CUtensorMap mk, mv;
+    if ((bf16 && kv_rows + BN >= (1L << 31)) || (long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
     cudaError_t e;
-    if ((e = make_tmap_2d_bf16(&mk, a.c.k, kv_rows, D, 64, box, true)) != cudaSuccess) return e;
-    if ((e = make_tmap_2d_bf16(&mv, a.c.v, kv_rows, D, 64, box, true)) != cudaSuccess) return e;
-    const int sms = device_sms();
+    const int sms = device_sms(), tile = bf16 ? BN : FN;
     Params p;
     p.c = a.c;
     p.G = a.G;
     p.R = (int)(a.G * a.L);
     // no more blocks than the longest rollouts have tiles
-    const long most = (long)a.B * a.c.H * (((a.c.max_pages << a.c.page_log2) + BN - 1) / BN);
+    const long most = (long)a.B * a.c.H * (((a.c.max_pages << a.c.page_log2) + tile - 1) / tile);
     p.line = line_of(a, 1, (int)std::min<long>(std::min<long>(2L * sms, MAXP), most), 1);
     p.sl2 = a.sl2;
-    p.q = (const __nv_bfloat16 *)a.q;
-    p.o = (__nv_bfloat16 *)a.o;
+    p.q = a.q;
+    p.o = a.o;
     p.lse = a.lse;
     p.part = (float *)a.ws;
     p.ml = (float2 *)((char *)a.ws + (size_t)sms * 4 * 64 * 32 * 4);
     p.whole = (float2 *)((char *)a.ws + part_bytes());
     p.scores = a.w_out ? (float *)(p.whole + (size_t)a.B * a.c.H * MROWS) : nullptr;
     p.w_in = a.w_in; p.w_out = a.w_out; p.decay = a.decay;
-    if ((e = allow_shared((const void *)paged_token_kernel, SMEM_BYTES, g_shared)) != cudaSuccess) return e;
-    paged_token_kernel<<<p.line.ngang, THREADS, SMEM_BYTES, s>>>(mk, mv, p), note_launch();
+    if (bf16) {
+        const uint32_t box = (uint32_t)std::min(1 << a.c.page_log2, BN);
+        CUtensorMap mk, mv;
+        if ((e = make_tmap_2d_bf16(&mk, a.c.k, kv_rows, D, 64, box, true)) != cudaSuccess) return e;
+        if ((e = make_tmap_2d_bf16(&mv, a.c.v, kv_rows, D, 64, box, true)) != cudaSuccess) return e;
+        if ((e = allow_shared((const void *)paged_token_kernel, SMEM_BYTES, g_shared)) != cudaSuccess) return e;
+        paged_token_kernel<<<p.line.ngang, THREADS, SMEM_BYTES, s>>>(mk, mv, p), note_launch();
+    } else {
+        const int st = ((a.c.d + 3) & ~3) + 4;
+        // the stages also hold the four warps' outputs at the end of a piece
+        const bool few = p.R <= 4;
+        const size_t need = std::max(f32_floats(few ? 4 : 16, st), (size_t)4 * (few ? 4 : 16) * D) * 4;
+        if ((e = few ? allow_shared((const void *)paged_token_f32_kernel<4>, f32_floats(4, 132) * 4, g_shared_f4)
+                     : allow_shared((const void *)paged_token_f32_kernel<16>, f32_floats(16, 132) * 4, g_shared_f16)) != cudaSuccess)
+            return e;
+        if (few) paged_token_f32_kernel<4><<<p.line.ngang, FT, need, s>>>(p), note_launch();
+        else paged_token_f32_kernel<16><<<p.line.ngang, FT, need, s>>>(p), note_launch();
+    }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.w_out ? (p.line.cap + KEYS - 1) / KEYS : 1), (unsigned)(a.B * a.c.H));
@@ -528,7 +700,8 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_token_join_kernel, p), note_launch();
+    e = bf16 ? cudaLaunchKernelEx(&cfg, paged_token_join_kernel<__nv_bfloat16, BN>, p) : cudaLaunchKernelEx(&cfg, paged_token_join_kernel<float, FN>, p);
+    if (e == cudaSuccess) note_launch();
     return e;
 }
 
