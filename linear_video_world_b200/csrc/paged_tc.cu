@@ -580,9 +580,14 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 }
 
 // Joins the pieces of heads whose keys were cut, in the order of the gangs; rows that see no key
-// get zeros here. A block takes 32 rows (a lane each), a warp 16 channels of them.
+// get zeros here. A block takes 32 rows (a lane each): the pieces' factors first, the warps taking
+// them in turn, then 16 channels a warp, eight pieces' loads in flight (one head of 40 pieces: 25 us
+// as a chain of loads, JOIN_TIME so).
+constexpr int MAXG = 160;               // pieces whose factors are kept; there are no more gangs
 __global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constant__ Params p)
 {
+    __shared__ float s_f[MAXG][32];
+    __shared__ float s_m[8][32], s_l[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nb = (p.R + 31) / 32;
     const int bh = blockIdx.x / nb, r = (blockIdx.x % nb) * 32 + lane;
@@ -593,32 +598,43 @@ __global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constan
     if (g.T > 0 && g.g0 == g.g1) return;
     const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
     if (ro.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
-    if (r >= p.R || frem(r, p.line.byL) >= ro.n) return;
-    float m = -INFINITY, l = 0.f;
+    const bool live = r < p.R && frem(r, p.line.byL) < ro.n;
+    const int np = g.T > 0 ? g.g1 - g.g0 + 1 : 0;
+    auto slot = [&](int i) { return ((long)(g.g0 + i) * p.line.gs + member) * 2 + (i == 0 ? g.slot0 : 0); };
+    float m = -INFINITY;
+    for (int i = warp; i < np; i += 8)
+        if (live) m = fmaxf(m, p.ml[slot(i) * ROWS + rr].x);
+    s_m[warp][lane] = m;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, s_m[w][lane]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int i = warp; i < np; i += 8) {
+        const float2 y = live ? p.ml[slot(i) * ROWS + rr] : make_float2(-INFINITY, 0.f);
+        // none of the piece's keys: no output was written
+        const float f = y.x == -INFINITY && y.y == 0.f ? 0.f : exp2f(y.x - base);
+        s_f[i][lane] = f;
+        l = fmaf(y.y, f, l);
+    }
+    s_l[warp][lane] = l;
+    __syncthreads();
+    l = 0.f;
+    for (int w = 0; w < 8; ++w) l += s_l[w][lane];
+    if (!live) return;
     float4 acc[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (g.T > 0) {
-        for (int i = g.g0; i <= g.g1; ++i) {
-            const long slot = ((long)i * p.line.gs + member) * 2 + (i == g.g0 ? g.slot0 : 0);
-            m = fmaxf(m, p.ml[slot * ROWS + rr].x);
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        for (int i = g.g0; i <= g.g1; ++i) {
-            const long slot = ((long)i * p.line.gs + member) * 2 + (i == g.g0 ? g.slot0 : 0);
-            const float2 ml = p.ml[slot * ROWS + rr];
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;       // none of the piece's keys: no output written
-            const float f = exp2f(ml.x - base);
-            l = fmaf(ml.y, f, l);
-            const float4 *src = reinterpret_cast<const float4 *>(p.part) + slot * (D / 4) * ROWS + rr;
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+        const float f = s_f[i][lane];
+        const float4 *src = reinterpret_cast<const float4 *>(p.part) + slot(i) * (D / 4) * ROWS + rr;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float4 v = src[(warp * 4 + x) * ROWS];
-                acc[x].x = fmaf(v.x, f, acc[x].x);
-                acc[x].y = fmaf(v.y, f, acc[x].y);
-                acc[x].z = fmaf(v.z, f, acc[x].z);
-                acc[x].w = fmaf(v.w, f, acc[x].w);
-            }
+        for (int x = 0; x < 4; ++x) {
+            const float4 v = f != 0.f ? src[(warp * 4 + x) * ROWS] : make_float4(0.f, 0.f, 0.f, 0.f);
+            acc[x].x = fmaf(v.x, f, acc[x].x);
+            acc[x].y = fmaf(v.y, f, acc[x].y);
+            acc[x].z = fmaf(v.z, f, acc[x].z);
+            acc[x].w = fmaf(v.w, f, acc[x].w);
         }
     }
     const long row = (long)bh * p.R + r;
@@ -675,7 +691,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     p.R = (int)R;
     p.nr = (int)((R + ROWS - 1) / ROWS);
     const int gs = gang_size(p.nr, sms);
-    p.line = line_of(a, gs, sms / gs, (p.nr + gs - 1) / gs);
+    p.line = line_of(a, gs, std::min(sms / gs, MAXG), (p.nr + gs - 1) / gs);
     p.sl2 = a.sl2;
     p.o = (__nv_bfloat16 *)a.o;
     p.lse = a.lse;
