@@ -95,21 +95,28 @@ __device__ __forceinline__ int page_of(const PagedKV &c, int b, int p)
 // last.
 struct Line {
     int B, H, L, cap, gs, ngang, passes;
+    int least;                      // places a gang takes at least (while there are gangs to spare)
     int steps;                      // places on the line per key tile (1; more where a tile's work is cut too)
     FastDiv byL;
     Mask mask;
     const int *kv_lens, *new_lens;
 };
-__host__ inline Line line_of(const PagedAttnArgs &a, int gs, int ngang, int passes, int steps = 1)
+__host__ inline Line line_of(const PagedAttnArgs &a, int gs, int ngang, int passes, int least = 1, int steps = 1)
 {
     Line p;
     p.B = a.B; p.H = a.c.H; p.L = (int)a.L;
     p.cap = a.c.max_pages << a.c.page_log2;
-    p.gs = gs; p.ngang = ngang; p.passes = passes; p.steps = steps;
+    p.gs = gs; p.ngang = ngang; p.passes = passes; p.least = least; p.steps = steps;
     p.byL = fast_div((unsigned)(a.L > 0 ? a.L : 1));
     p.mask = mask_of(a.N, a.w);
     p.kv_lens = a.c.kv_lens; p.new_lens = a.new_lens;
     return p;
+}
+// Gangs that take part: none with less than `least` places, and no cut is empty.
+__device__ __forceinline__ long long gangs(const Line &p, long long W)
+{
+    const long long n = (W + p.least - 1) / p.least;
+    return n < p.ngang ? n : p.ngang;
 }
 // 64-bit quotient; in 32 bits where both fit (a third of the time)
 __device__ __forceinline__ long long quot(long long a, long long b)
@@ -160,7 +167,7 @@ __device__ __forceinline__ Place place_of(const Line &p, int g)
 {
     const int lane = threadIdx.x & 31;
     const long long per = tiles_before<TK>(p, p.B) * p.H, W = per * p.passes;
-    const long long ng = W < p.ngang ? W : p.ngang;         // no gang's cut is empty
+    const long long ng = gangs(p, W);
     Place c;
     c.left = 0;
     c.pass = c.b = c.h = c.t = 0;
@@ -243,7 +250,7 @@ __device__ __forceinline__ Holders holders_at(const Line &p, long long W, long l
     o.g0 = o.g1 = o.slot0 = 0;
     if (n == 0) return o;
     // gang g holds [W g / ng, W (g + 1) / ng), rounded down
-    const long long ng = W < p.ngang ? W : p.ngang;
+    const long long ng = gangs(p, W);
     o.g0 = (int)quot((a + 1) * ng - 1, W);
     o.g1 = (int)quot((a + n) * ng - 1, W);
     o.slot0 = quot(W * o.g0, ng) == a ? 0 : 1;

@@ -365,7 +365,7 @@ cudaError_t launch_paged_weights_tc(const PagedAttnArgs &a, cudaStream_t s)
     p.R = (int)R;
     const int nrt = (int)((R + RT - 1) / RT);
     if ((long)((a.c.max_pages << a.c.page_log2) / BN + 2) * nrt >= (1L << 30)) return cudaErrorNotSupported;
-    p.line = line_of(a, 1, sms, 1, nrt);
+    p.line = line_of(a, 1, sms, 1, 1, nrt);
     p.part = (float *)a.ws;         // the attention's pieces are joined by now
     p.sl2 = a.sl2;
     p.lse = a.lse; p.w_in = a.w_in; p.w_out = a.w_out; p.decay = a.decay;

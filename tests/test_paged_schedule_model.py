@@ -8,12 +8,12 @@ import pytest
 
 # ---- the line (csrc/paged.cuh) ---------------------------------------------------------------
 
-def _pieces(T, H, passes, ngang, steps):
+def _pieces(T, H, passes, ngang, steps, least):
     """What each gang takes, as place_of / next_piece do it: {(pass, b, h): [(from, to, gang, slot, whole)]}."""
     T = [t * steps for t in T]
     per = sum(T) * H
     W = per * passes
-    ng = min(W, ngang)
+    ng = min(-(-W // least), ngang)
     got = {}
     for g in range(ng):
         a = W * g // ng
@@ -57,7 +57,7 @@ def test_line_division_and_join_agree(seed):
             continue
         if steps > 1:
             passes = 1
-        T, per, W, ng, got = _pieces(T, H, passes, r.choice([1, 2, 3, 21, 148, 296, r.randint(1, 148)]), steps)
+        T, per, W, ng, got = _pieces(T, H, passes, r.choice([1, 2, 3, 21, 148, 296, r.randint(1, 148)]), steps, r.choice([1, 1, 2, 3]))
         sizes = [sum(p[1] - p[0] for c in got.values() for p in c if p[2] == g) for g in range(ng)]
         assert max(sizes) - min(sizes) <= 1 and sum(sizes) == W
         for ps in range(passes):
