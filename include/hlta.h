@@ -473,8 +473,10 @@ hlta_status hlta_rope_axes(const void *q, const void *k, void *q_out, void *k_ou
  * never read or written through: such a token is not appended and reads as page 0, lengths are
  * clamped to what fits; the outputs of that rollout are unspecified.
  * All calls enqueue on `stream`, hold no state between calls, and can be captured into a CUDA
- * graph (make the library's first call on a device before a capture). Calls that share a
- * workspace must be ordered on one stream.
+ * graph (make a call of the same kind on the device once before the capture: the library's helpers
+ * and kernels are set up then). Calls that share a workspace must be ordered on one stream, and the
+ * tables must not change while a call runs. HLTA_ERR_UNSUPPORTED: B * Hkv above 65535, or a bf16 pool
+ * or query tensor of 2^31 rows.
  */
 
 /*

@@ -213,7 +213,10 @@ __device__ __forceinline__ bool next_piece(const Line &p, Place &c, Piece<TK> &o
 {
     if (c.left <= 0) return false;
     o.x = tiles_of<TK>(p, c.b);
-    while (o.x.T == 0) {            // rollouts without tiles have no place on the line
+    // rollouts without tiles have no place on the line (bounded, like `take` below, in case the lengths
+    // are changed under the kernel)
+    for (int seen = 0; o.x.T == 0; ++seen) {
+        if (seen > p.B) return false;
         if (++c.b == p.B) {
             c.b = 0;
             ++c.pass;
@@ -224,6 +227,7 @@ __device__ __forceinline__ bool next_piece(const Line &p, Place &c, Piece<TK> &o
     o.b = c.b;
     o.h = c.h;
     const int take = min(c.left, o.x.T - c.t);
+    if (take <= 0) return false;
     o.ta = o.x.t0 * p.steps + c.t;
     o.tb = o.ta + take;
     o.whole = take == o.x.T;

@@ -165,8 +165,7 @@ def test_unseen_keys_never_leak(h, dtype, L, Hq):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("L", [1, 40])
 def test_large_scores_and_infinities(h, dtype, L):
-    """Scores of +-1e3: one key takes all the weight. A key of +inf score gives NaN rows, and only
-    the rows that see it."""
+    """Scores of +-1e3: one key takes all the weight. An infinite value reaches the row that sees it."""
     c = Cache([200], 1, 128, 32, dtype, seed=5)
     q = (torch.randn(1, 2, L, 128, generator=torch.Generator().manual_seed(2)) * 100).to(dtype)
     o, lse, _, w = _run(h, c, q, [L], dict(Hkv=1, N=1, w=0))
@@ -363,3 +362,25 @@ def test_error_bound_would_show_a_lost_key():
         keep = [j for j in range(64) if j != drop]
         p = torch.softmax(c.keys[0][0, keep].double() @ q[0, 0, 0].double() / math.sqrt(40), 0)
         assert float(((p @ c.vals[0][0, keep].double() - ro[0, 0, 0]).abs() / ob[0, 0, 0]).max()) > 5
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weights_of_few_rows_over_a_huge_capacity(h, dtype):
+    """Rows x capacity past what single tokens keep scores for: the weights then come from a second
+    pass over the keys, the same within both paths' bounds."""
+    page, kv = 128, 300
+    c = Cache([kv], 1, 128, page, dtype, seed=4)
+    q = torch.randn(1, 16, 1, 128, generator=torch.Generator().manual_seed(3)).to(dtype)
+    kp, vp, table, lens = c.cuda()
+    wide = torch.full((1, (1 << 24) // page + 64), -3, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    ro, _, rw, ob, _, wb = attn_ref(q, c, [1], 1, 0)
+    for t in (table, wide):
+        cap = t.shape[1] * page
+        assert (h.hlta_paged_attn_workspace_bytes(1, 16, 1, 1, 128, page, t.shape[1], True, h._dt(q)) < 1 << 30) or t is table
+        w = torch.full((1, 1, cap), 5.0, device="cuda")
+        o = h.paged_attn(q.cuda(), kp, vp, t, lens, w_out=w).cpu()
+        assert bool(((o.double() - ro).abs() <= ob).all())
+        assert bool(((w[..., :kv].cpu().double() - rw[..., :kv]).abs() <= wb[..., :kv]).all())
+        assert bool((w[..., kv:] == 5).all())
+    assert h.hlta_device_status() == 0

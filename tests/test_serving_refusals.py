@@ -79,6 +79,9 @@ def test_paged_attn(h):
               (dict(ws=ctypes.c_void_p((1 << 40) + 16)), BAD), (dict(dt=3), BAD), (dict(d=64), NO), (dict(d=0), BAD), (dict(Hq=4 * 129), NO),
               (dict(B=0), ok), (dict(L=0, w_in=None, w_out=None), ok)]
     _refused(h, h._lib.hlta_paged_attn_fwd, good, cases)
+    big = dict(good, B=70000, H=1, Hq=1, ws=_p(8), wsb=1 << 60)
+    # past what a launch can index (the shape is refused before anything is enqueued, if there is a device at all)
+    assert h._lib.hlta_paged_attn_fwd(*[dict(big, w_in=None, w_out=None)[n] for n in good]) in (NO, h.HLTA_ERR_CUDA)
     size = h.hlta_paged_attn_workspace_bytes
     assert size(2, 9, 4, 3, 128, 16, 4) == 0 and size(2, 8, 4, 3, 200, 16, 4) == 0 and size(-1, 8, 4, 3, 128, 16, 4) == 0
     assert size(2, 8, 4, 3, 128, 16, 4, False) < ws
