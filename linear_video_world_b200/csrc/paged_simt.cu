@@ -18,6 +18,7 @@
 #include "paged_f32.cuh"
 
 #include <algorithm>
+#include <cooperative_groups.h>
 #include <math.h>
 
 namespace hlta {
@@ -62,13 +63,25 @@ __device__ __forceinline__ void scores(const float *Q, const float *K, int st, i
     }
 }
 
-// rows [r0, r0 + TM) of the head group's queries, times the scale; rows that are none as zeros
-__device__ __forceinline__ void stage_q(const PagedAttnArgs &a, const FastDiv &byL, const Roll &ro, long head, int R, int r0, float *Q, int st, int dp)
+// rows [r0, r0 + TM) of the head group's queries, asynchronously; rows that are none, and channels from d to dp, as zeros
+__device__ __forceinline__ void copy_q(const PagedAttnArgs &a, const FastDiv &byL, const Roll &ro, long head, int R, int r0, float *Q, int st, int dp)
 {
-    for (int e = threadIdx.x; e < TM * dp; e += THREADS) {
-        const int r = e / dp, x = e - r * dp;
-        const bool in = r0 + r < R && x < a.c.d && frem(r0 + r, byL) < ro.n;
-        Q[r * st + x] = in ? ((const float *)a.q)[(head * R + r0 + r) * a.c.d + x] * a.sl2 : 0.f;
+    const int per = dp >> 2, d = a.c.d;
+    const bool words = (d & 3) == 0;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < TM * per; e += THREADS) {
+        const int r = e / per, x = 4 * (e - r * per);
+        const bool in = r0 + r < R && frem(r0 + r, byL) < ro.n;
+        const float *src = (const float *)a.q + (in ? (head * R + r0 + r) * d + x : 0);
+        float *dst = Q + r * st + x;
+        if (words) {
+            copy16(dst, src, in);
+        } else {
+            for (int y = 0; y < 4; ++y) {
+                const bool ch = in && x + y < d;
+                copy4(dst + y, ch ? src + y : (const float *)a.q, ch);
+            }
+        }
     }
 }
 
@@ -116,8 +129,10 @@ __global__ void __launch_bounds__(THREADS) paged_attn_f32_kernel(PagedAttnArgs a
         copy_tile<TN, THREADS>(a.c, b, h, t * TN, u, k, k + TN * st, st, dp);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    if (tb > ta) load(ta);
-    stage_q(a, byL, ro, blockIdx.y, R, r0, Q, st, dp);
+    if (tb > ta) {
+        copy_q(a, byL, ro, blockIdx.y, R, r0, Q, st, dp);
+        load(ta);
+    }
     for (int t = ta; t < tb; ++t) {
         if (t + 1 < tb) {
             load(t + 1);
@@ -134,7 +149,7 @@ __global__ void __launch_bounds__(THREADS) paged_attn_f32_kernel(PagedAttnArgs a
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int p = t * TN + kg + 16 * j;
-                if (p < sp[i].lo || p >= sp[i].hi) s[i][j] = -INFINITY;
+                s[i][j] = p < sp[i].lo || p >= sp[i].hi ? -INFINITY : s[i][j] * a.sl2;
             }
             const float mn = fmaxf(m[i], half_max(fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]))));
             const float base = mn == -INFINITY ? 0.f : mn, f = exp2f(m[i] - base);
@@ -230,54 +245,90 @@ __global__ void __launch_bounds__(128) paged_join_f32_kernel(PagedAttnArgs a, Fa
     if (a.lse && lane == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
-// Accumulated attention weights: a block owns 64 keys of one key head and sums, over every row of
-// the head group that sees them, 2^(score - lse): blocks of 64 rows in turn, a thread its four keys over
-// its four rows of each, the 16 threads of a key joined at the end in the order of their rows.
+// Accumulated attention weights: 64 keys of one key head, and over every row of the head group that
+// sees them the sum of 2^(score - lse). A cluster of one to eight blocks (grid z) shares those keys, each
+// with every nz-th block of 64 rows, copied asynchronously one ahead; a thread sums its four keys over
+// its four rows of each, and the 16 threads of a key and the blocks are joined at the end in a fixed
+// order. (One block for all rows, which it copied word by word between two barriers: 1600 rows over
+// 381 keys TODO.)
 __global__ void __launch_bounds__(THREADS) paged_weights_f32_kernel(PagedAttnArgs a, FastDiv byL, Mask mask)
 {
     extern __shared__ __align__(16) float smem[];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int nz = (int)gridDim.z, z = (int)blockIdx.z;
     const int d = a.c.d, dp = (d + 3) & ~3, st = dp + 4;
-    float *Q = smem, *K = Q + TM * st, *Sum = K + TN * st;              // Sum: [16 row groups][64 keys]
+    float *K = smem, *Qs = K + TN * st, *Sum = Qs + 2 * TM * st;        // Q of two stages; Sum: [16 row groups][64 keys]
+    __shared__ float total[TN];
     const int rg = threadIdx.x >> 4, kg = threadIdx.x & 15;
     const int h = blockIdx.y % a.c.H, b = blockIdx.y / a.c.H, cap = a.c.max_pages << a.c.page_log2, p0 = blockIdx.x * TN;
     const Roll ro = roll_of(a.c.kv_lens, a.new_lens, b, (int)a.L, cap);
-    if (p0 >= ro.kv) return;
-    const int R = a.G * (int)a.L;
-    copy_tile<TN, THREADS>(a.c, b, h, p0, ro.n > 0 ? Span{0, ro.kv} : Span{0, 0}, K, nullptr, st, dp);
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    if (p0 >= ro.kv) return;                    // the whole cluster alike
+    const int R = a.G * (int)a.L, nrb = (R + TM - 1) / TM;
+    // this block's next block of rows from rb that sees some of the keys: all threads alike
+    auto seen = [&](int rb) {
+        for (; rb < nrb; rb += nz) {
+            const Span u = rows_span(ro, byL, mask, rb * TM, R);
+            if (u.lo < p0 + TN && u.hi > p0) break;
+        }
+        return rb;
+    };
+    int rb = seen(z), stage = 0;
+    if (rb < nrb) {
+        copy_tile<TN, THREADS>(a.c, b, h, p0, Span{0, ro.kv}, K, nullptr, st, dp);
+        copy_q(a, byL, ro, blockIdx.y, R, rb * TM, Qs, st, dp);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int rb = 0; rb < R; rb += TM) {
-        const Span u = rows_span(ro, byL, mask, rb, R);
-        if (u.lo >= p0 + TN || u.hi <= p0) continue;    // seen by none of these rows: all threads alike
-        __syncthreads();
-        stage_q(a, byL, ro, blockIdx.y, R, rb, Q, st, dp);
-        __syncthreads();
-        float s[4][4];
-        scores(Q, K, st, dp, rg, kg, s);
+    while (rb < nrb) {
+        const int next = seen(rb + nz);
+        if (next < nrb) {
+            copy_q(a, byL, ro, blockIdx.y, R, next * TM, Qs + (stage ^ 1) * TM * st, st, dp);
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        float lse[4];
+        Span v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = rb + 4 * rg + i, tok = frem(r, byL);
-            if (r >= R || tok >= ro.n) continue;
-            const Span v = span_of(ro, tok, mask);
-            const float z = a.lse[(long)blockIdx.y * R + r] * 1.4426950408889634f;
+            const int r = rb * TM + 4 * rg + i, tok = frem(r, byL);
+            const bool in = r < R && tok < ro.n;
+            v[i] = in ? span_of(ro, tok, mask) : Span{0, 0};
+            lse[i] = in ? a.lse[(long)blockIdx.y * R + r] * 1.4426950408889634f : 0.f;
+        }
+        __syncthreads();
+        float s[4][4];
+        scores(Qs + stage * TM * st, K, st, dp, rg, kg, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int p = p0 + kg + 16 * j;
-                if (p >= v.lo && p < v.hi) sum[j] += exp2f(s[i][j] - z);
+                if (p >= v[i].lo && p < v[i].hi) sum[j] += exp2f(fmaf(s[i][j], a.sl2, -lse[i]));
             }
-        }
+        __syncthreads();
+        rb = next;
+        stage ^= 1;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) Sum[rg * TN + kg + 16 * j] = sum[j];
     __syncthreads();
-    const int p = p0 + threadIdx.x;
-    if (threadIdx.x < TN && p < ro.kv) {
+    if (threadIdx.x < TN) {
         float t = 0.f;
         for (int g = 0; g < 16; ++g) t += Sum[g * TN + threadIdx.x];
+        total[threadIdx.x] = t;
+    }
+    if (nz > 1) cluster.sync();
+    const int p = p0 + threadIdx.x;
+    if (z == 0 && threadIdx.x < TN && p < ro.kv) {
+        float t = total[threadIdx.x];
+        for (int o = 1; o < nz; ++o) t += cluster.map_shared_rank(total, o)[threadIdx.x];
         const long at = (long)blockIdx.y * cap + p;
         if (a.w_in && p < ro.h) t = fmaf(a.decay, a.w_in[at], t);
         a.w_out[at] = t;
     }
+    if (nz > 1) cluster.sync();                 // no block ends while its sums are read
 }
 
 // shares of the keys: enough blocks for two rounds of the SMs, no share under two tiles
@@ -320,12 +371,28 @@ cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s)
 cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, cudaStream_t s)
 {
     const int keys = a.c.max_pages << a.c.page_log2, st = ((a.c.d + 3) & ~3) + 4;
-    if ((long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
-    cudaError_t e = allow_shared((const void *)paged_weights_f32_kernel, (size_t)((TM + TN) * 132 + 16 * TN) * 4, g_shared_w);
+    const long heads = (long)a.B * a.c.H, nrb = (a.G * a.L + TM - 1) / TM;
+    if (heads > 65535) return cudaErrorNotSupported;
+    cudaError_t e = allow_shared((const void *)paged_weights_f32_kernel, (size_t)((2 * TM + TN) * 132 + 16 * TN) * 4, g_shared_w);
     if (e != cudaSuccess) return e;
-    paged_weights_f32_kernel<<<dim3((unsigned)((keys + TN - 1) / TN), (unsigned)(a.B * a.c.H)), THREADS, (size_t)((TM + TN) * st + 16 * TN) * 4, s>>>(
-        a, fast_div((unsigned)std::max(a.L, 1L)), mask_of(a.N, a.w)), note_launch();
-    return cudaGetLastError();
+    // blocks per key tile: while the SMs have room (two fit one) and each has two blocks of rows
+    const long tiles = heads * ((keys + TN - 1) / TN);
+    unsigned nz = 1;
+    while (nz < 8 && tiles * nz * 2 <= 2L * device_sms() && nrb >= 4L * nz) nz *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((keys + TN - 1) / TN), (unsigned)heads, nz);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = (size_t)((2 * TM + TN) * st + 16 * TN) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = nz;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_weights_f32_kernel, a, fast_div((unsigned)std::max(a.L, 1L)), mask_of(a.N, a.w));
+    if (e == cudaSuccess) note_launch();
+    return e;
 }
 
 }  // namespace hlta
