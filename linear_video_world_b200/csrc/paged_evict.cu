@@ -1,8 +1,10 @@
 // Eviction from a paged cache by accumulated attention weight: choose the positions to keep, then
 // copy their keys, values and weights to the destination's pages.
 //
-// Choice, a cluster of one to eight blocks per (rollout, key head), as many as still fill the GPU
-// (64 rows of 20000 to 32760 positions: 38 us with one block each, 24 us with two): of the
+// Choice, one block per (rollout, key head), or a cluster of two for long rows that fit the GPU
+// together (64 rows of 20000 to 32760 positions: the choice 38 us with one block each, 24 us
+// with two; the whole call, 16 rows of 9231: 20.8 and 20.7 us; 16 of 900: 10.8 and 13.9 us; clusters of four and
+// eight were never the faster: 23 and 53 us at 9231): of the
 // middle positions the `take` largest weights, found by a radix select over order-preserving 32-bit
 // keys of the weights (three passes of 11, 11 and 10 bits, from the top: each counts the digits of
 // the keys that still match the threshold's prefix; the blocks read one another's counts). Each
@@ -242,13 +244,12 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, bool bf16, cudaStream_t 
     int *kept = a.kept ? a.kept : (int *)a.ws;
     cudaError_t e = allow_shared((const void *)evict_choose_kernel, CHOOSE_SMEM, g_shared);
     if (e != cudaSuccess) return e;
-    // blocks per row: while they fit the SMs, and none has fewer positions than threads
-    int nblk = 1;
-    while (nblk < 8 && bh * nblk * 2 <= device_sms() && (long)(a.c.max_pages << a.c.page_log2) >= 2L * nblk * ST) nblk *= 2;
+    const int cap = a.c.max_pages << a.c.page_log2;
+    const int nblk = cap > 8 * ST && bh * 2 <= device_sms() ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bh * nblk));
     cfg.blockDim = dim3(ST);
-    cfg.dynamicSmemBytes = CHOOSE_SMEM;
+    cfg.dynamicSmemBytes = (size_t)(std::min((cap + nblk - 1) / nblk, KEEP) + 2 * BINS) * 4;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -81,9 +81,10 @@ def test_evict(h, kind, dtype, d, page, kv, budget, sink, recent):
     assert torch.equal(kp2[:kp.shape[0]].nan_to_num(1.25), kp.nan_to_num(1.25))
 
 
-def test_long_rows(h):
-    """More positions than one block holds in shared memory, equal weights straddling the border."""
-    n, budget, H = 120000, 50001, 1
+@pytest.mark.parametrize("n,budget,H", [(120000, 50001, 1), (20000, 7001, 3), (20000, 7001, 80)])
+def test_long_rows(h, n, budget, H):
+    """Two blocks a row or one, more positions than they hold in shared memory, equal weights
+    straddling the border."""
     page = 128
     width = -(-n // page)
     kp, vp = (torch.randn(width, H, page, 16, device="cuda") for _ in range(2))
@@ -96,10 +97,11 @@ def test_long_rows(h):
     lens = torch.tensor([n], dtype=torch.int32, device="cuda")
     h.paged_evict(w.cuda(), kp, vp, table, lens, budget, 100, 1000, kd, vd, dst, kept=kept)
     assert h.hlta_device_status() == 0
-    assert kept[0, 0].tolist() == _keep(w[0, 0].tolist(), n, budget, 100, 1000)
-    at = kept[0, 0].long()
-    assert torch.equal(kd.view(-1, 16)[:budget], kp[table[0].long()].view(-1, 16)[at])
-    assert torch.equal(vd.view(-1, 16)[:budget], vp[table[0].long()].view(-1, 16)[at])
+    for x in {0, H - 1}:
+        assert kept[0, x].tolist() == _keep(w[0, x].tolist(), n, budget, 100, 1000)
+        at = kept[0, x].long()
+        assert torch.equal(kd[:, x].reshape(-1, 16)[:budget], kp[table[0].long(), x].reshape(-1, 16)[at])
+        assert torch.equal(vd[:, x].reshape(-1, 16)[:budget], vp[table[0].long(), x].reshape(-1, 16)[at])
 
 
 def test_tables_out_of_range_are_reported(h):
