@@ -112,10 +112,11 @@ __host__ inline Line line_of(const PagedAttnArgs &a, int gs, int ngang, int pass
     p.kv_lens = a.c.kv_lens; p.new_lens = a.new_lens;
     return p;
 }
-// Gangs that take part: none with less than `least` places, and no cut is empty.
+// Gangs that take part: none with less than `least` places (one where there are no more places than
+// heads: such cuts fall between them), and no cut is empty.
 __device__ __forceinline__ long long gangs(const Line &p, long long W)
 {
-    const long long n = (W + p.least - 1) / p.least;
+    const long long n = W <= (long long)p.B * p.H * p.passes ? W : (W + p.least - 1) / p.least;
     return n < p.ngang ? n : p.ngang;
 }
 // 64-bit quotient; in 32 bits where both fit (a third of the time)

@@ -543,28 +543,43 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             } else if (live) {
                 p.ml[slot * ROWS + rr] = make_float2(m, lsum);
             }
+            // (a whole piece's rows go through this warp's rows of P, whose last product is done: stored
+            // from the accumulators, 16 bytes of 32 rows an access, they took 1 us more)
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
                 uint32_t ov[32];
                 __syncwarp();
                 if (have) tc::tmem_ld32(o_tm + cc * 32, ov);
-                if (!live) continue;
                 if (s.x.whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + grow * D + cc * 32);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         uint32_t w[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             w[y] = have ? tc::pack_bf16(__uint_as_float(ov[8 * x + 2 * y]) * inv, __uint_as_float(ov[8 * x + 2 * y + 1]) * inv) : 0u;
-                        dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + (uint32_t)(cc >> 1) * HALF + ((((uint32_t)(cc & 1) * 4u + x) ^ rx) << 4)),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
                     }
-                } else if (have) {
+                } else if (have && live) {
                     float4 *dst = reinterpret_cast<float4 *>(p.part) + (slot * (D / 4) + 8 * cc) * ROWS + rr;
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         dst[x * ROWS] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]), __uint_as_float(ov[4 * x + 3]));
                 }
+            }
+            if (s.x.whole) {
+                // two rows an access, half a warp each
+                const unsigned rows_live = __ballot_sync(0xffffffffu, live);
+                uint4 *dst = reinterpret_cast<uint4 *>(p.o + (grow - lane) * D) + (lane & 15);
+#pragma unroll 2
+                for (int i = lane >> 4; i < 32; i += 2) {
+                    const uint32_t from = prow - (uint32_t)lane * 128u + (uint32_t)i * 128u + (uint32_t)((lane >> 3) & 1) * HALF + (uint32_t)(((lane & 7) ^ (i & 7)) << 4);
+                    uint4 w;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(from) : "memory");
+                    if (rows_live >> i & 1u) dst[i * (D / 8)] = w;
+                }
+                __syncwarp();
             }
             if (n > 0) {
                 tc::fence_before_sync();
@@ -694,8 +709,8 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     p.R = (int)R;
     p.nr = (int)((R + ROWS - 1) / ROWS);
     const int gs = gang_size(p.nr, sms);
-    // two tiles a gang at least: a block's start and end cost as much as several tiles, and the join
-    // grows with the pieces (128 rows over 5000 keys of 2 heads: 32 us with one, 25 with two)
+    // two tiles a gang at least (unless the heads have but one each): a block's start and end cost as
+    // much as several tiles, and the join grows with the pieces (128 rows over 5000 keys of 2 heads: 32 us with one, 25 with two)
     p.line = line_of(a, gs, std::min(sms / gs, MAXG), (p.nr + gs - 1) / gs, 2);
     p.sl2 = a.sl2;
     p.o = (__nv_bfloat16 *)a.o;

@@ -13,7 +13,7 @@ def _pieces(T, H, passes, ngang, steps, least):
     T = [t * steps for t in T]
     per = sum(T) * H
     W = per * passes
-    ng = min(-(-W // least), ngang)
+    ng = min(W if W <= len(T) * H * passes else -(-W // least), ngang)
     got = {}
     for g in range(ng):
         a = W * g // ng
