@@ -330,6 +330,9 @@ __global__ void __launch_bounds__(BN) paged_weights_join_kernel(const __grid_con
     const int h = blockIdx.y % p.c.H, b = blockIdx.y / p.c.H;
     const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
     const int t = blockIdx.x, k = t * BN + threadIdx.x;
+    // one block waits whatever there is to do, so that this kernel never ends before the first one
+    // (what is captured behind it depends on this kernel alone)
+    if (t == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t * BN >= ro.kv) return;
     const Tiles<BN> x = tiles_of<BN>(p.line, b);
     const int nt = x.T / p.line.steps;
