@@ -42,13 +42,26 @@ __device__ __forceinline__ float half_sum(float x)
     return x;
 }
 
-// s[i][j] = row (4 rg + i) . key (kg + 16 j)
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+        "mov.b64 pc, {%6, %7};\n\tfma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// s[i][j] = row (4 rg + i) . key (kg + 16 j): even and odd pairs of channels in the two halves of a
+// two-wide multiply-add
 __device__ __forceinline__ void scores(const float *Q, const float *K, int st, int dp, int rg, int kg, float (&s)[4][4])
 {
+    float2 acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 2
     for (int x = 0; x < dp; x += 4) {
         float4 q[4], k[4];
 #pragma unroll
@@ -58,9 +71,15 @@ __device__ __forceinline__ void scores(const float *Q, const float *K, int st, i
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                s[i][j] = fmaf(q[i].x, k[j].x, fmaf(q[i].y, k[j].y, fmaf(q[i].z, k[j].z, fmaf(q[i].w, k[j].w, s[i][j]))));
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = ffma2(make_float2(q[i].x, q[i].y), make_float2(k[j].x, k[j].y), acc[i][j]);
+                acc[i][j] = ffma2(make_float2(q[i].z, q[i].w), make_float2(k[j].z, k[j].w), acc[i][j]);
+            }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = acc[i][j].x + acc[i][j].y;
 }
 
 // rows [r0, r0 + TM) of the head group's queries, asynchronously; rows that are none, and channels from d to dp, as zeros
@@ -113,7 +132,8 @@ __global__ void __launch_bounds__(THREADS) paged_attn_f32_kernel(PagedAttnArgs a
     const int ta = t_lo + (int)((long)nt * blockIdx.z / nsplit), tb = t_lo + (int)((long)nt * (blockIdx.z + 1) / nsplit);
     Span sp[4];
     bool live[4];
-    float m[4], l[4], acc[4][8];
+    float m[4], l[4];
+    float2 acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + 4 * rg + i, tok = frem(r, byL);
@@ -122,7 +142,7 @@ __global__ void __launch_bounds__(THREADS) paged_attn_f32_kernel(PagedAttnArgs a
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) acc[i][x] = 0.f;
+        for (int x = 0; x < 4; ++x) acc[i][x] = make_float2(0.f, 0.f);
     }
     auto load = [&](int t) {
         float *k = KV + (t & 1) * 2 * TN * st;
@@ -163,7 +183,10 @@ __global__ void __launch_bounds__(THREADS) paged_attn_f32_kernel(PagedAttnArgs a
             }
             l[i] = fmaf(l[i], f, sum);              // this thread's keys; joined at the end
 #pragma unroll
-            for (int x = 0; x < 8; ++x) acc[i][x] *= f;
+            for (int x = 0; x < 4; ++x) {
+                acc[i][x].x *= f;
+                acc[i][x].y *= f;
+            }
         }
         __syncwarp();
         if (4 * kg < dp) {
@@ -180,14 +203,11 @@ __global__ void __launch_bounds__(THREADS) paged_attn_f32_kernel(PagedAttnArgs a
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-                        acc[i][0] = fmaf(w, v0.x, acc[i][0]);
-                        acc[i][1] = fmaf(w, v0.y, acc[i][1]);
-                        acc[i][2] = fmaf(w, v0.z, acc[i][2]);
-                        acc[i][3] = fmaf(w, v0.w, acc[i][3]);
-                        acc[i][4] = fmaf(w, v1.x, acc[i][4]);
-                        acc[i][5] = fmaf(w, v1.y, acc[i][5]);
-                        acc[i][6] = fmaf(w, v1.z, acc[i][6]);
-                        acc[i][7] = fmaf(w, v1.w, acc[i][7]);
+                        const float2 ww = make_float2(w, w);
+                        acc[i][0] = ffma2(ww, make_float2(v0.x, v0.y), acc[i][0]);
+                        acc[i][1] = ffma2(ww, make_float2(v0.z, v0.w), acc[i][1]);
+                        acc[i][2] = ffma2(ww, make_float2(v1.x, v1.y), acc[i][2]);
+                        acc[i][3] = ffma2(ww, make_float2(v1.z, v1.w), acc[i][3]);
                     }
                 }
             }
@@ -205,7 +225,7 @@ __global__ void __launch_bounds__(THREADS) paged_attn_f32_kernel(PagedAttnArgs a
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
             const int ch = (x >> 2) * 64 + 4 * kg + (x & 3);
-            if (ch < d) dst[ch] = acc[i][x] * inv;
+            if (ch < d) dst[ch] = ((x & 1) ? acc[i][x >> 1].y : acc[i][x >> 1].x) * inv;
         }
         if (kg == 0) {
             if (nsplit > 1) {
