@@ -512,8 +512,8 @@ size_t hlta_paged_attn_workspace_bytes(int B, int Hq, int Hkv, long L, int d, in
  * w_out[j] = decay * w_in[j] + the sum of the softmax weights that the chunk's rows of the head
  * group give position j; w_in is read for the positions before the chunk only (NULL for zero),
  * may be w_out, else must not overlap it; decay is finite; positions from kv_lens[b] on are left as they were.
- * bf16: d = 128; fp32: 1 <= d <= 128; Hq / Hkv <= 128. N >= 1, w >= 0; L <= 2^29, max_pages * page <=
- * 2^30.
+ * scale: of the scores, finite, 0 or less for 1/sqrt(d). bf16: d = 128; fp32: 1 <= d <= 128; Hq / Hkv
+ * <= 128. N >= 1, w >= 0; L <= 2^29, max_pages * page <= 2^30.
  * workspace: at least hlta_paged_attn_workspace_bytes(...), 256-byte aligned; its contents on entry
  * are ignored. Sums run in a fixed order: equal calls give equal bits. Errors: HLTA_ERR_INVALID_ARG,
  * HLTA_ERR_UNSUPPORTED; a bounded wait that expires as hlta_swa_fwd.

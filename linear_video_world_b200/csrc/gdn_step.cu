@@ -9,6 +9,9 @@
 // d = 128: eight lanes share a row (16 channels each, as four 16-byte words 128 bytes apart, so
 // that a warp's load covers whole 128-byte lines of four rows); a thread keeps the rows' channels
 // in registers for all of the step's tokens, so the state moves once however many tokens there are.
+// Two rows a thread, 32 a block, six blocks per SM: 256 rollouts of 8 heads, up to four tokens each,
+// take 59.7 us (4.6 TB/s of states in and out; one row a thread 81, four rows 70); one token of 8 heads
+// 3.3 us.
 // Other d (fp32 tensors): a warp walks a row.
 #include "hlta_internal.cuh"
 

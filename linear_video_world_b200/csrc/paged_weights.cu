@@ -12,7 +12,7 @@
 // tile, row tile) steps (paged.cuh, one block a gang): the sums of a key tile that is cut between
 // blocks go to the workspace and a second kernel joins them in the order of the blocks. (Whole key
 // tiles per block: 312 of them on 148 SMs took three rounds for two; with the log-sum-exp fetched by
-// the summing warps themselves 61 us, now 45.)
+// the summing warps themselves 61 us, now 44: 3 chunks of 517 tokens of 16 heads, window 4096, 312 key tiles.)
 #include "hlta_internal.cuh"
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
