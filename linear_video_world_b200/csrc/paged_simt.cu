@@ -296,7 +296,9 @@ __global__ void __launch_bounds__(THREADS) paged_weights_f32_kernel(PagedAttnArg
     };
     int rb = seen(z), stage = 0;
     if (rb < nrb) {
-        copy_tile<TN, THREADS>(a.c, b, h, p0, Span{0, ro.kv}, K, nullptr, st, dp);
+        // no position outside what the chunk's rows see: their pages may be gone
+        const Span u{span_of(ro, 0, mask).lo, span_of(ro, ro.n - 1, mask).hi};
+        copy_tile<TN, THREADS>(a.c, b, h, p0, u, K, nullptr, st, dp);
         copy_q(a, byL, ro, blockIdx.y, R, rb * TM, Qs, st, dp);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }

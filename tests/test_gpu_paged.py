@@ -384,3 +384,23 @@ def test_weights_of_few_rows_over_a_huge_capacity(h, dtype):
         assert bool(((w[..., :kv].cpu().double() - rw[..., :kv]).abs() <= wb[..., :kv]).all())
         assert bool((w[..., kv:] == 5).all())
     assert h.hlta_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("L,Hq", [(1, 2), (3, 4), (40, 4)])
+def test_pages_before_the_window_may_be_gone(h, dtype, L, Hq):
+    """The window starts inside a tile of keys: the pages before it, same tile or not, are no longer
+    in the table."""
+    kv, w, page = [331, 90], 70, 16
+    c = Cache(kv, 2, 128, page, dtype, seed=L)
+    for b, n in enumerate(kv):
+        c.table[b, :max(0, n - L - w + 1) // page] = -1
+    q = torch.randn(2, Hq, L, 128, generator=torch.Generator().manual_seed(3)).to(dtype)
+    kp, vp, table, lens = c.cuda()
+    wo = torch.zeros((2, 2, table.shape[1] * page), device="cuda")
+    o = h.paged_attn(q.cuda(), kp, vp, table, lens, N=1, w=w, w_out=wo)
+    assert h.hlta_device_status() == 0
+    ro, _, rw, ob, _, wb = attn_ref(q, c, [L, L], 1, w)
+    assert bool(((o.cpu().double() - ro).abs() <= ob).all())
+    for b, n in enumerate(kv):
+        assert bool(((wo[b, :, :n].cpu().double() - rw[b, :, :n]).abs() <= wb[b, :, :n]).all())
