@@ -642,19 +642,14 @@ def hybrid(q, k, v, a, b, Hs, Hd, Hg, T, N, w_swa, w_dswa, r, S0=None, chunk=64,
     return o, S_out
 
 
-def _on(stream, *tensors):
-    """Tensors allocated here for a call on another stream than the current one: torch's
-    allocator may not hand their memory on before that stream's work is done."""
+def _made(stream, make):
+    """make(): tensors allocated, and filled, on the call's own stream (None: the current one), so that
+    their memory is free there and a fill is ahead of the call."""
     if stream is None:
-        return
-    import torch
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    if stream.cuda_stream == torch.cuda.current_stream().cuda_stream:
-        return
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+        return make()
+    th = _th()
+    with th.cuda.stream(stream if hasattr(stream, "cuda_stream") else th.cuda.ExternalStream(int(stream))):
+        return make()
 
 
 def rope_axes(q, k, pairs, grid=None, pos=None, t0=None, base=10000.0, halves=False,
@@ -666,8 +661,8 @@ def rope_axes(q, k, pairs, grid=None, pos=None, t0=None, base=10000.0, halves=Fa
     Hk = k.shape[1] if k is not None else 0
     spec = rope_axes_spec(pairs, grid, pos, t0, base, halves, shared_freq, B, L)
     if out is None:
-        out = (None if q is None else th.empty_like(q), None if k is None else th.empty_like(k))
-        _on(stream, *out)
+        out = _made(stream, lambda: (None if q is None else th.empty_like(q),
+                                     None if k is None else th.empty_like(k)))
     dt, qs, ks = ref.dtype, (B, H, L, d), (B, Hk, L, d)
     _check(_lib.hlta_rope_axes(
         *_args(th, (q, "q", dt, qs), (k, "k", dt, ks), (out[0], "q_out", dt, qs),
@@ -705,14 +700,12 @@ def paged_attn(q, k_pages, v_pages, table, kv_lens, new_lens=None, N=1, w=0, sca
     B, width = table.shape
     Hq, L = qs[1], qs[2]
     if out is None:
-        out = th.empty_like(q) if new_lens is None else th.zeros_like(q)
-        _on(stream, out)
+        out = _made(stream, lambda: th.empty_like(q) if new_lens is None else th.zeros_like(q))
     code = _dt(q)
     if workspace is None:
-        workspace = th.empty(_lib.hlta_paged_attn_workspace_bytes(
-            B, Hq, H, L, d, page, width, 0 if w_out is None else 1, code), dtype=th.uint8,
-            device=q.device)
-        _on(stream, workspace)
+        need = _lib.hlta_paged_attn_workspace_bytes(B, Hq, H, L, d, page, width,
+                                                    0 if w_out is None else 1, code)
+        workspace = _made(stream, lambda: th.empty(need, dtype=th.uint8, device=q.device))
     bs, ws_shape = (B,), (B, H, width * page)
     *addr, ws = _args(th, (q, "q", dt, (B, Hq, L, d)), (k_pages, "k_pages", dt, pages),
                       (v_pages, "v_pages", dt, pages), (table, "table", i32, None),
@@ -736,12 +729,10 @@ def paged_evict(weights, k_pages, v_pages, table, kv_lens, budget, sink, recent,
     (B, width), (_, dwidth) = table.shape, dst_table.shape
     bs = (B,)
     if new_lens is None:
-        new_lens = th.empty_like(kv_lens)
-        _on(stream, new_lens)
+        new_lens = _made(stream, lambda: th.empty_like(kv_lens))
     if workspace is None:
-        workspace = th.empty(_lib.hlta_paged_evict_workspace_bytes(B, H, budget), dtype=th.uint8,
-                             device=weights.device)
-        _on(stream, workspace)
+        need = _lib.hlta_paged_evict_workspace_bytes(B, H, budget)
+        workspace = _made(stream, lambda: th.empty(need, dtype=th.uint8, device=weights.device))
     src = _args(th, (weights, "weights", f32, (B, H, width * page)),
                 (k_pages, "k_pages", dt, pages), (v_pages, "v_pages", dt, pages),
                 (table, "table", i32, None), (kv_lens, "kv_lens", i32, bs))
@@ -760,8 +751,7 @@ def _gdn_step(raw, q, k, v, a, b, S, slots, lens, out, S_out, stream):
     th, qs = _th(), q.shape
     B, H, L, d = qs
     if out is None:
-        out = th.empty_like(q) if slots is None and lens is None else th.zeros_like(q)
-        _on(stream, out)
+        out = _made(stream, lambda: th.empty_like(q) if slots is None and lens is None else th.zeros_like(q))
     if S_out is None:
         S_out = S
     num = S.shape[0]

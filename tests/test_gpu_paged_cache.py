@@ -3,7 +3,7 @@ windows and eviction, beside the recurrent gated delta rule, against a 64-bit fo
 import pytest
 import torch
 
-from serving_util import attn_ref, gdn_ref, grid_positions, rope_ref
+from serving_util import Cache, attn_ref, gdn_ref, grid_positions, rope_ref
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -160,3 +160,26 @@ def test_rollout_continues_as_one_call(h):
     bound = 4 * 2.0 ** -8 * float(v.abs().max())
     assert float((got[0] - got[1]).abs().max()) <= bound and float((got[0] - got[2]).abs().max()) <= bound
     assert h.hlta_device_status() == 0
+
+
+def test_results_allocated_on_the_call_s_stream(h):
+    """A call on another stream than the current one, which is busy: what the wrappers allocate and
+    fill belongs to the call's stream."""
+    c = Cache([70, 33], 2, 128, 16, torch.bfloat16, seed=5)
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(2, 4, 3, 128, generator=g).to(torch.bfloat16).cuda()
+    kp, vp, table, lens = c.cuda()
+    new = torch.tensor([3, 2], dtype=torch.int32).cuda()
+    S, a = torch.randn(2, 4, 128, 128, generator=g).cuda(), torch.rand(2, 4, 3, generator=g).cuda()
+    u = torch.nn.functional.normalize(q.float(), dim=-1).to(torch.bfloat16)
+    want = h.paged_attn(q, kp, vp, table, lens, new), h.gdn_step(u, u, q, a, a, S.clone(), lens=new)[0]
+    So = torch.empty_like(S)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)              # the current stream is busy for about 0.1 s
+    got = []
+    for s in (side, side.cuda_stream):
+        got += [h.paged_attn(q, kp, vp, table, lens, new, stream=s), h.gdn_step(u, u, q, a, a, S, S_out=So, lens=new, stream=s)[0]]
+    torch.cuda.synchronize()
+    for x, y in zip(got, want * 2):
+        assert torch.equal(x, y)
