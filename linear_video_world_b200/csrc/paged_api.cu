@@ -280,6 +280,9 @@ static hlta_status gdn_step(const void *q, const void *k, const void *v, const f
     if (misaligned4(a) || misaligned4(b) || misaligned4(slots) || misaligned4(lens)) return FAIL("gates and tables must be 4-byte aligned");
     const size_t ns = (size_t)num_slots * H * d * d * 4;
     if (S != S_out && overlap(S, ns, S_out, ns)) return FAIL("S_out overlaps S");
+    const size_t no = (size_t)B * H * L * d * (dt == HLTA_BF16 ? 2 : 4);
+    // blocks of different state rows read the whole of q and k
+    if (no && (overlap(o, no, q, no) || overlap(o, no, k, no) || overlap(o, no, v, no))) return FAIL("o overlaps an input");
     if (B == 0 || H == 0) return HLTA_OK;
     ERR_WORD(err);
     GdnStepArgs g;

@@ -110,6 +110,7 @@ def test_gdn_step(h):
     cases += [({n: ctypes.c_void_p(1 << 35 | 2)}, BAD) for n in ("a", "b", "slots", "lens")]
     cases += [(dict(B=-1), BAD), (dict(H=-1), BAD), (dict(L=-1), BAD), (dict(num_slots=0), BAD), (dict(num_slots=1), BAD), (dict(d=64), NO), (dict(dt=4), BAD),
               (dict(So=ctypes.c_void_p((1 << 32) * 7 + 64)), BAD), (dict(B=0), ok), (dict(H=0), ok)]
+    cases += [(dict(o=good[n]), BAD) for n in ("q", "k", "v")]
     _refused(h, h._lib.hlta_gdn_step, good, cases)
     raw = dict(list(good.items())[:5] + [("c", F(1.0))] + list(good.items())[5:])
     _refused(h, h._lib.hlta_gdn_step_raw, raw, [(dict(c=F(-1.0)), BAD), (dict(c=F(float("nan"))), BAD), (dict(c=F(float("inf"))), BAD), (dict(B=0), ok)])
