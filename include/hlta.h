@@ -553,8 +553,8 @@ hlta_status hlta_paged_evict(const float *weights, const void *k_pages, const vo
  * Gated delta rule, recurrent form, over a pool of states: the recurrence of hlta_gdn_chunk_fwd
  * token by token, for steps of one or a few tokens per rollout (the chunk form prepares 64-token
  * chunks whatever L is, and is the faster one from some dozens of tokens on).
- * q, k, v, o: [B, H, L, d] device, o overlapping none of them; a, b: [B, H, L] float32. S, S_out: [num_slots, H, d, d] float32,
- * S_out may be S (in place), else must not overlap it. slots: [B] int32 device, the state of each
+ * q, k, v, o: [B, H, L, d] device, o apart from the others; a, b: [B, H, L] float32. S, S_out:
+ * [num_slots, H, d, d] float32, S_out may be S (in place), else must not overlap it. slots: [B] int32 device, the state of each
  * rollout, NULL for 0 .. B-1; a negative slot marks a padded rollout: its rows of o are left as
  * they were. Slots that no rollout names are left as they were. lens: [B] int32 device: tokens that
  * each rollout really has, NULL for all L; rows behind are left as they were; with no token the

@@ -657,6 +657,8 @@ def rope_axes(q, k, pairs, grid=None, pos=None, t0=None, base=10000.0, halves=Fa
     """q and k ([B, H, L, d], either may be None) rotated by positions on three axes (see
     hlta_rope_axes); `out` = (q_out, k_out), which may be (q, k) for in place."""
     th, ref = _th(), q if q is not None else k
+    if ref is None:
+        raise HltaError(HLTA_ERR_INVALID_ARG, "neither q nor k is given")
     B, H, L, d = ref.shape
     Hk = k.shape[1] if k is not None else 0
     spec = rope_axes_spec(pairs, grid, pos, t0, base, halves, shared_freq, B, L)
@@ -831,12 +833,22 @@ class PagedCache:
         new = [L] * self.B if new_lens is None else [int(n) for n in new_lens]
         if len(new) != self.B or any(n < 0 or n > L for n in new):
             raise HltaError(HLTA_ERR_INVALID_ARG, f"new_lens must be {self.B} numbers in [0, {L}] (got {new})")
+        before, held = self.lens, [len(p) for p in self._pages]
         lens = [a + n for a, n in zip(self.lens, new)]
         pages = self._grow(lens)
         self.lens = lens
         self._tables(pages)
         self.new_lens.copy_(_th().tensor(new, dtype=_th().int32))
-        paged_append(k, v, self.k_pages, self.v_pages, self.table, self.kv_lens, self.new_lens, rope)
+        try:
+            paged_append(k, v, self.k_pages, self.v_pages, self.table, self.kv_lens, self.new_lens, rope)
+        except Exception:
+            # refused: the rollouts and the pool as they were
+            self.lens = before
+            for p, n in zip(self._pages, held):
+                self._free.extend(reversed(p[n:]))
+                del p[n:]
+            self._tables(pages)
+            raise
 
     def attend(self, q, N=1, w=0, scale=0.0, out=None, lse=None):
         """Attention of the chunk appended last (q [B, Hq, L, d]); adds to the weights if kept."""

@@ -183,3 +183,19 @@ def test_results_allocated_on_the_call_s_stream(h):
     torch.cuda.synchronize()
     for x, y in zip(got, want * 2):
         assert torch.equal(x, y)
+
+
+def test_refused_append_changes_nothing(h):
+    c = h.PagedCache(2, 2, 128, 8, 64, page=16)
+    k = torch.randn(2, 2, 20, 128, device="cuda").to(torch.bfloat16)
+    c.append(k, k, [20, 3])
+    state = list(c.lens), [list(p) for p in c._pages], sorted(c._free), c.table.clone(), c.kv_lens.clone()
+    for bad in (k.float(), k[..., :64], k[:, :1], k[:1], k.transpose(1, 2)):
+        with pytest.raises(h.HltaError):
+            c.append(bad, bad, [bad.shape[2], 20])
+        with pytest.raises(h.HltaError):
+            c.append(k, k, rope=dict(pairs=(60, 60, 0), grid=(1, 1)))
+        assert (c.lens, c._pages, sorted(c._free)) == state[:3]
+        assert torch.equal(c.kv_lens, state[4]) and torch.equal(c.table, state[3])
+    c.append(k, k, [5, 20])
+    assert c.lens == [25, 23] and h.hlta_device_status() == 0

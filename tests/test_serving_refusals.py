@@ -123,6 +123,8 @@ def test_wrappers_refuse_host_tensors_and_shapes(h):
         h.rope_axes(q, None, (22, 21, 21), grid=(1, 1))
     with pytest.raises(h.HltaError):
         h.rope_axes(q, torch.zeros(1, 2, 4, 128), (22, 21, 21), grid=(1, 1))
+    with pytest.raises(h.HltaError):
+        h.rope_axes(None, None, (22, 21, 21), grid=(1, 1))
     for bad in (dict(), dict(grid=(1, 1), pos=torch.zeros(1, 3, 3, dtype=torch.int32)), dict(pos=torch.zeros(1, 3, 3, dtype=torch.int32), t0=torch.zeros(1, dtype=torch.int32))):
         with pytest.raises(h.HltaError):
             h.rope_axes_spec((1, 1, 1), **bad)
