@@ -851,7 +851,8 @@ class PagedCache:
             raise
 
     def attend(self, q, N=1, w=0, scale=0.0, out=None, lse=None):
-        """Attention of the chunk appended last (q [B, Hq, L, d]); adds to the weights if kept."""
+        """Attention of the chunk appended last (q [B, Hq, L, d]; the rows of a rollout that was cut or
+        released since are zero, or as they were in `out`); adds to the weights if kept."""
         return paged_attn(q, self.k_pages, self.v_pages, self.table, self.kv_lens, self.new_lens, N,
                           w, scale, out, lse, self.weights, self.weights, self.decay)
 
@@ -882,6 +883,7 @@ class PagedCache:
             self._free.extend(self._pages[b])
             self._pages[b] = to[b]
             self.lens[b] = budget
+            self.new_lens[b] = 0                        # its last chunk is no longer its last positions
         self.weights = weights
         self._tables(True)
         return cut
@@ -891,6 +893,7 @@ class PagedCache:
         self._free.extend(self._pages[b])
         self._pages[b] = []
         self.lens[b] = 0
+        self.new_lens[b] = 0
         self._tables(True)
 
 

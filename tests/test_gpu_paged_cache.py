@@ -199,3 +199,18 @@ def test_refused_append_changes_nothing(h):
         assert torch.equal(c.kv_lens, state[4]) and torch.equal(c.table, state[3])
     c.append(k, k, [5, 20])
     assert c.lens == [25, 23] and h.hlta_device_status() == 0
+
+
+def test_attending_after_a_rollout_was_cut_or_released(h):
+    c = h.PagedCache(3, 2, 128, 20, 64, page=16, weights=True)
+    k, q = (torch.randn(3, n, 40, 128, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda() for n in (2, 4))
+    c.append(k, k, [40, 30, 20])
+    o = c.attend(q, N=40)
+    w = c.weights.clone()
+    assert c.evict(33) == [0]
+    c.release(1)
+    again = c.attend(q, N=40)
+    assert h.hlta_device_status() == 0
+    assert torch.equal(again[2], o[2]) and bool((again[:2] == 0).all())
+    # what the cut rollout kept has its weights, once
+    assert torch.equal(c.weights[0, :, :33].sort(-1).values, w[0, :, :40].sort(-1).values[:, -33:])
