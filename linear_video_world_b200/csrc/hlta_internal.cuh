@@ -249,6 +249,7 @@ struct PagedAttnArgs {
 size_t paged_attn_simt_bytes(int B, int Hq, int Hkv, long L, int d, int max_keys);
 cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s);                 // fp32
 cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, cudaStream_t s);              // fp32, after the attention
+bool paged_weights_fit(long R, int cap);        // key tiles x row tiles of a head below 2^30
 cudaError_t launch_paged_weights_tc(const PagedAttnArgs &a, cudaStream_t s);                // bf16, after the attention
 size_t paged_attn_tc_bytes();
 cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s);                   // bf16

@@ -215,6 +215,8 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
     if (paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, w_out != nullptr))
         return done(launch_paged_token(a, dt == HLTA_BF16, (cudaStream_t)stream), "paged attention");
     if (w_out) {
+        if (dt == HLTA_BF16 && !paged_weights_fit(a.G * a.L, max_pages * page))
+            return record_error(HLTA_ERR_UNSUPPORTED, "weights of %ld rows over a capacity of %d", a.G * a.L, max_pages * page);
         // the weights are taken in a second pass, from the log-sum-exp
         if (!lse) a.lse = (float *)ws;
         a.ws = ws + pad((size_t)B * Hq * L * 4);

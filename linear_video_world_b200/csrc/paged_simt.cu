@@ -376,18 +376,14 @@ cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s)
     const long R = a.G * a.L, rows = (long)a.B * a.c.H * R;
     const int ns = splits_of(a.B, a.c.H, R, a.c.max_pages << a.c.page_log2), st = ((a.c.d + 3) & ~3) + 4;
     if (R < 1) return cudaSuccess;
-    if (R > (1L << 30) || (long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
+    if (R > (1L << 30) || (long)a.B * a.c.H > 65535 || (rows + 3) / 4 > 0x7fffffffL) return cudaErrorNotSupported;
     float *m = (float *)a.ws, *l = m + ns * rows, *o = l + ns * rows;
     cudaError_t e = allow_shared((const void *)paged_attn_f32_kernel, (size_t)((TM + 4 * TN) * 132 + TM * PST) * 4, g_shared);
     if (e != cudaSuccess) return e;
     const FastDiv byL = fast_div((unsigned)a.L);
     const dim3 grid((unsigned)((R + TM - 1) / TM), (unsigned)(a.B * a.c.H), (unsigned)ns);
     paged_attn_f32_kernel<<<grid, THREADS, (size_t)((TM + 4 * TN) * st + TM * PST) * 4, s>>>(a, byL, mask_of(a.N, a.w), ns, m, l, o), note_launch();
-    if (ns > 1) {
-        const long blocks = (rows + 3) / 4;
-        if (blocks > 0x7fffffffL) return cudaErrorNotSupported;
-        paged_join_f32_kernel<<<(unsigned)blocks, 128, 0, s>>>(a, byL, ns, m, l, o), note_launch();
-    }
+    if (ns > 1) paged_join_f32_kernel<<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a, byL, ns, m, l, o), note_launch();
     return cudaGetLastError();
 }
 

@@ -695,7 +695,8 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     const long R = a.G * a.L;
     const long q_rows = (long)a.B * a.c.H * R, kv_rows = a.c.num_pages * a.c.H << a.c.page_log2;
     if (R == 0 || a.B == 0) return cudaSuccess;
-    if (q_rows + ROWS >= (1L << 31) || kv_rows + BN >= (1L << 31)) return cudaErrorNotSupported;
+    const long blocks = (long)a.B * a.c.H * ((R + 31) / 32);            // of the join
+    if (q_rows + ROWS >= (1L << 31) || kv_rows + BN >= (1L << 31) || blocks > 0x7fffffffL) return cudaErrorNotSupported;
     const int psz = 1 << a.c.page_log2;
     CUtensorMap mq, mk, mv;
     cudaError_t e;
@@ -719,8 +720,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     p.ml = (float2 *)((char *)a.ws + (size_t)sms * 2 * ROWS * D * 4);
     if ((e = allow_shared((const void *)paged_attn_tc_kernel, SMEM_BYTES, g_shared)) != cudaSuccess) return e;
     paged_attn_tc_kernel<<<p.line.gs * p.line.ngang, THREADS, SMEM_BYTES, s>>>(mq, mk, mv, p), note_launch();
-    const long blocks = (long)a.B * a.c.H * ((R + 31) / 32);
-    if (blocks > 0x7fffffffL) return cudaErrorNotSupported;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(256);
@@ -730,7 +730,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_join_tc_kernel, p), note_launch();
+    if ((e = cudaLaunchKernelEx(&cfg, paged_join_tc_kernel, p)) == cudaSuccess) note_launch();
     return e;
 }
 

@@ -354,6 +354,8 @@ __global__ void __launch_bounds__(BN) paged_weights_join_kernel(const __grid_con
 
 }  // namespace
 
+bool paged_weights_fit(long R, int cap) { return (cap / BN + 2L) * ((R + RT - 1) / RT) < (1L << 30); }
+
 cudaError_t launch_paged_weights_tc(const PagedAttnArgs &a, cudaStream_t s)
 {
     const long R = a.G * a.L, q_rows = (long)a.B * a.c.H * R, kv_rows = a.c.num_pages * a.c.H << a.c.page_log2;
@@ -367,7 +369,6 @@ cudaError_t launch_paged_weights_tc(const PagedAttnArgs &a, cudaStream_t s)
     p.c = a.c;
     p.R = (int)R;
     const int nrt = (int)((R + RT - 1) / RT);
-    if ((long)((a.c.max_pages << a.c.page_log2) / BN + 2) * nrt >= (1L << 30)) return cudaErrorNotSupported;
     p.line = line_of(a, 1, sms, 1, 1, nrt);
     p.part = (float *)a.ws;         // the attention's pieces are joined by now
     p.sl2 = a.sl2;
@@ -384,7 +385,7 @@ cudaError_t launch_paged_weights_tc(const PagedAttnArgs &a, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_weights_join_kernel, p), note_launch();
+    if ((e = cudaLaunchKernelEx(&cfg, paged_weights_join_kernel, p)) == cudaSuccess) note_launch();
     return e;
 }
 

@@ -82,6 +82,8 @@ def test_paged_attn(h):
     big = dict(good, B=70000, H=1, Hq=1, ws=_p(8), wsb=1 << 60)
     # past what a launch can index (the shape is refused before anything is enqueued, if there is a device at all)
     assert h._lib.hlta_paged_attn_fwd(*[dict(big, w_in=None, w_out=None)[n] for n in good]) in (NO, h.HLTA_ERR_CUDA)
+    wide = dict(good, B=1, L=1 << 24, page=128, max_pages=1 << 20, num_pages=9, o=ctypes.c_void_p(1 << 50), w_out=ctypes.c_void_p(1 << 51), w_in=None, ws=_p(8), wsb=1 << 60)
+    assert h._lib.hlta_paged_attn_fwd(*[wide[n] for n in good]) in (NO, h.HLTA_ERR_CUDA)
     size = h.hlta_paged_attn_workspace_bytes
     assert size(2, 9, 4, 3, 128, 16, 4) == 0 and size(2, 8, 4, 3, 200, 16, 4) == 0 and size(-1, 8, 4, 3, 128, 16, 4) == 0
     assert size(2, 8, 4, 3, 128, 16, 4, False) < ws
