@@ -329,29 +329,39 @@ def _th():
 def _args(th, *wanted):
     """Addresses of (tensor, name, dtype, shape) tuples (None: a null pointer, any dtype or shape):
     each contiguous, on the current device (where the kernels are launched), as described."""
-    dev = th.cuda.current_device() if th.cuda.is_initialized() else -2
-    out = []
+    out, dev = [], None
     for t, n, dtype, shape in wanted:
         if t is None:
             out.append(None)
             continue
-        if dtype is not None and t.dtype != dtype:
-            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {dtype} (got {t.dtype})")
-        if shape is not None and t.shape != shape:
-            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {list(shape)} (got {list(t.shape)})")
-        if t.get_device() != dev or not t.is_contiguous():
-            if not t.is_cuda or not t.is_contiguous():
-                raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be a contiguous CUDA tensor")
-            raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} is on {t.device}, the current device is cuda:{dev}")
+        at = t.get_device()
+        if dev is None and at >= 0:
+            dev = th._C._cuda_getDevice()
+        if (at != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype)
+                or (shape is not None and t.shape != shape)):
+            _misfit(t, n, dtype, shape, dev)
         out.append(t.data_ptr())
     return out
+
+
+def _misfit(t, n, dtype, shape, dev):
+    if dtype is not None and t.dtype != dtype:
+        raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {dtype} (got {t.dtype})")
+    if shape is not None and t.shape != shape:
+        raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be {list(shape)} (got {list(t.shape)})")
+    if not t.is_cuda or not t.is_contiguous():
+        raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} must be a contiguous CUDA tensor")
+    raise HltaError(HLTA_ERR_INVALID_ARG, f"{n} is on {t.device}, the current device is cuda:{dev}")
 
 
 def _stream_address(th, stream):
     if stream is None:
         # the address alone: a Stream object costs as much as a launch
-        return th._C._cuda_getCurrentRawStream(th.cuda.current_device())
+        return th._C._cuda_getCurrentRawStream(th._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_INT3 = ctypes.c_int * 3
 
 
 def rope_axes_spec(pairs, grid=None, pos=None, t0=None, base=10000.0, halves=False,
@@ -368,7 +378,7 @@ def rope_axes_spec(pairs, grid=None, pos=None, t0=None, base=10000.0, halves=Fal
         th = _th()
         at_pos, at_t0 = _args(th, (pos, "pos", th.int32, None if B is None else (B, L, 3)),
                               (t0, "t0", th.int32, None if B is None else (B,)))
-    return hlta_rope_axes_t((ctypes.c_int * 3)(*pairs), halves, shared_freq, gh, gw, base, at_pos,
+    return hlta_rope_axes_t(_INT3(*pairs), halves, shared_freq, gh, gw, base, at_pos,
                             at_t0)
 
 
@@ -642,14 +652,14 @@ def hybrid(q, k, v, a, b, Hs, Hd, Hg, T, N, w_swa, w_dswa, r, S0=None, chunk=64,
     return o, S_out
 
 
-def _made(stream, make):
-    """make(): tensors allocated, and filled, on the call's own stream (None: the current one), so that
-    their memory is free there and a fill is ahead of the call."""
+def _made(stream, make, *args, **kw):
+    """make(...): a tensor allocated, and filled, on the call's own stream (None: the current one), so
+    that its memory is free there and a fill is ahead of the call."""
     if stream is None:
-        return make()
+        return make(*args, **kw)
     th = _th()
     with th.cuda.stream(stream if hasattr(stream, "cuda_stream") else th.cuda.ExternalStream(int(stream))):
-        return make()
+        return make(*args, **kw)
 
 
 def rope_axes(q, k, pairs, grid=None, pos=None, t0=None, base=10000.0, halves=False,
@@ -663,8 +673,8 @@ def rope_axes(q, k, pairs, grid=None, pos=None, t0=None, base=10000.0, halves=Fa
     Hk = k.shape[1] if k is not None else 0
     spec = rope_axes_spec(pairs, grid, pos, t0, base, halves, shared_freq, B, L)
     if out is None:
-        out = _made(stream, lambda: (None if q is None else th.empty_like(q),
-                                     None if k is None else th.empty_like(k)))
+        out = (None if q is None else _made(stream, th.empty_like, q),
+               None if k is None else _made(stream, th.empty_like, k))
     dt, qs, ks = ref.dtype, (B, H, L, d), (B, Hk, L, d)
     _check(_lib.hlta_rope_axes(
         *_args(th, (q, "q", dt, qs), (k, "k", dt, ks), (out[0], "q_out", dt, qs),
@@ -702,12 +712,12 @@ def paged_attn(q, k_pages, v_pages, table, kv_lens, new_lens=None, N=1, w=0, sca
     B, width = table.shape
     Hq, L = qs[1], qs[2]
     if out is None:
-        out = _made(stream, lambda: th.empty_like(q) if new_lens is None else th.zeros_like(q))
+        out = _made(stream, th.empty_like if new_lens is None else th.zeros_like, q)
     code = _dt(q)
     if workspace is None:
         need = _lib.hlta_paged_attn_workspace_bytes(B, Hq, H, L, d, page, width,
                                                     0 if w_out is None else 1, code)
-        workspace = _made(stream, lambda: th.empty(need, dtype=th.uint8, device=q.device))
+        workspace = _made(stream, q.new_empty, need, dtype=th.uint8)
     bs, ws_shape = (B,), (B, H, width * page)
     *addr, ws = _args(th, (q, "q", dt, (B, Hq, L, d)), (k_pages, "k_pages", dt, pages),
                       (v_pages, "v_pages", dt, pages), (table, "table", i32, None),
@@ -731,10 +741,10 @@ def paged_evict(weights, k_pages, v_pages, table, kv_lens, budget, sink, recent,
     (B, width), (_, dwidth) = table.shape, dst_table.shape
     bs = (B,)
     if new_lens is None:
-        new_lens = _made(stream, lambda: th.empty_like(kv_lens))
+        new_lens = _made(stream, th.empty_like, kv_lens)
     if workspace is None:
         need = _lib.hlta_paged_evict_workspace_bytes(B, H, budget)
-        workspace = _made(stream, lambda: th.empty(need, dtype=th.uint8, device=weights.device))
+        workspace = _made(stream, weights.new_empty, need, dtype=th.uint8)
     src = _args(th, (weights, "weights", f32, (B, H, width * page)),
                 (k_pages, "k_pages", dt, pages), (v_pages, "v_pages", dt, pages),
                 (table, "table", i32, None), (kv_lens, "kv_lens", i32, bs))
@@ -753,7 +763,7 @@ def _gdn_step(raw, q, k, v, a, b, S, slots, lens, out, S_out, stream):
     th, qs = _th(), q.shape
     B, H, L, d = qs
     if out is None:
-        out = _made(stream, lambda: th.empty_like(q) if slots is None and lens is None else th.zeros_like(q))
+        out = _made(stream, th.empty_like if slots is None and lens is None else th.zeros_like, q)
     if S_out is None:
         S_out = S
     num = S.shape[0]
