@@ -370,7 +370,7 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
 
 // fp32: RB rows at a time (4 or 16).
 constexpr int FN = 32, FSTAGES = 3, FT = 128;           // keys per tile, stages, threads
-std::atomic<unsigned long long> g_shared_f4{0}, g_shared_f16{0};
+std::atomic<unsigned long long> g_shared_f4{0}, g_shared_f8{0}, g_shared_f16{0};
 constexpr size_t f32_floats(int rb, int st) { return (size_t)FSTAGES * 2 * FN * st + (size_t)rb * st + 4 * 8 * rb; }
 
 template <int RB>
@@ -656,7 +656,7 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, bool bf16, cudaStream_t s
 {
     const long kv_rows = a.c.num_pages * a.c.H << a.c.page_log2;
     if ((bf16 && kv_rows + BN >= (1L << 31)) || (long)a.B * a.c.H > 65535) return cudaErrorNotSupported;
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
     const int sms = device_sms(), tile = bf16 ? BN : FN;
     Params p;
     p.c = a.c;
@@ -684,13 +684,16 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, bool bf16, cudaStream_t s
     } else {
         const int st = ((a.c.d + 3) & ~3) + 4;
         // the stages also hold the four warps' outputs at the end of a piece
-        const bool few = p.R <= 4;
-        const size_t need = std::max(f32_floats(few ? 4 : 16, st), (size_t)4 * (few ? 4 : 16) * D) * 4;
-        if ((e = few ? allow_shared((const void *)paged_token_f32_kernel<4>, f32_floats(4, 132) * 4, g_shared_f4)
-                     : allow_shared((const void *)paged_token_f32_kernel<16>, f32_floats(16, 132) * 4, g_shared_f16)) != cudaSuccess)
-            return e;
-        if (few) paged_token_f32_kernel<4><<<p.line.ngang, FT, need, s>>>(p), note_launch();
-        else paged_token_f32_kernel<16><<<p.line.ngang, FT, need, s>>>(p), note_launch();
+        const int rb = p.R <= 4 ? 4 : p.R <= 8 ? 8 : 16;
+        const size_t need = std::max(f32_floats(rb, st), (size_t)4 * rb * D) * 4;
+        auto go = [&](void (*kernel)(Params), std::atomic<unsigned long long> &done) {
+            if ((e = allow_shared((const void *)kernel, f32_floats(rb, 132) * 4, done)) != cudaSuccess) return;
+            kernel<<<p.line.ngang, FT, need, s>>>(p), note_launch();
+        };
+        if (rb == 4) go(paged_token_f32_kernel<4>, g_shared_f4);
+        else if (rb == 8) go(paged_token_f32_kernel<8>, g_shared_f8);
+        else go(paged_token_f32_kernel<16>, g_shared_f16);
+        if (e != cudaSuccess) return e;
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
