@@ -18,15 +18,17 @@ __device__ __forceinline__ void copy4(float *dst, const float *src, bool in)
 }
 
 // Positions [p0, p0 + N) of key head h into K and (unless null) V, rows of `st` floats; positions
-// outside u and channels from d to dp (d rounded up to four) as zeros.
+// outside u and channels from d to dp (d rounded up to four) as zeros. A warp per row, four channels a
+// lane.
 template <int N, int THREADS>
 __device__ __forceinline__ void copy_tile(const PagedKV &c, int b, int h, int p0, const Span &u, float *K, float *V, int st, int dp)
 {
-    const int psz = 1 << c.page_log2, per = dp >> 2;
+    const int psz = 1 << c.page_log2, warp = threadIdx.x >> 5, x = 4 * (threadIdx.x & 31);
+    if (x >= dp) return;
     const bool words = (c.d & 3) == 0;
 #pragma unroll 4
-    for (int e = threadIdx.x; e < N * per; e += THREADS) {
-        const int r = e / per, x = 4 * (e - r * per), p = p0 + r;
+    for (int r = warp; r < N; r += THREADS / 32) {
+        const int p = p0 + r;
         const bool in = p >= u.lo && p < u.hi;
         const long at = in ? (((long)page_of(c, b, p) * c.H + h) * psz + (p & (psz - 1))) * c.d + x : 0;
         const float *k = (const float *)c.k + at, *v = (const float *)c.v + at;

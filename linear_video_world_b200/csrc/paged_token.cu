@@ -21,8 +21,10 @@
 //
 // fp32 tensors (any d <= 128): the same division and the same second kernel; 32-key tiles copied
 // asynchronously into three stages, four warps of eight keys each. A score is summed by four lanes
-// (32 channels each), a lane owns four channels of the output; rows in groups of 4 or 16, so that few
-// rows do not pay for 16. Bound by HBM for few rows, by shared-memory reads for 16.
+// (32 channels each), a lane owns four channels of the output; built for 1, 2, 4, 8 and 16 rows, so that
+// few rows do not pay for 16 (8 tokens over 500 to 3000 keys of 8 heads: 42 us, 62 with no form below
+// four rows; 32 query heads over 4: 44 us, 66 with 16 rows for eight). Bound by the instructions of a tile
+// (a warp's copies, score sums over lanes, softmax), for 16 rows by shared-memory reads.
 #include "hlta_internal.cuh"
 #include "paged.cuh"
 #include "paged_f32.cuh"
@@ -368,9 +370,9 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     }
 }
 
-// fp32: RB rows at a time (4 or 16).
+// fp32: at most RB rows.
 constexpr int FN = 32, FSTAGES = 3, FT = 128;           // keys per tile, stages, threads
-std::atomic<unsigned long long> g_shared_f4{0}, g_shared_f8{0}, g_shared_f16{0};
+std::atomic<unsigned long long> g_shared_f1{0}, g_shared_f2{0}, g_shared_f4{0}, g_shared_f8{0}, g_shared_f16{0};
 constexpr size_t f32_floats(int rb, int st) { return (size_t)FSTAGES * 2 * FN * st + (size_t)rb * st + 4 * 8 * rb; }
 
 template <int RB>
@@ -410,6 +412,17 @@ __global__ void __launch_bounds__(FT) paged_token_f32_kernel(const __grid_consta
             Q[r * st + y] = in ? ((const float *)p.q)[(row0 + r) * d + y] * p.sl2 : 0.f;
         }
         float m[RB], l[RB], acc[RB][4];
+        // the rows' spans (empty for rows that are none), kept where there are registers for them
+        constexpr bool KEPT = RB <= 8;
+        auto row_span = [&](int r) {
+            const int i = frem(r, p.line.byL);
+            return r < p.R && i < x.x.r.n ? span_of(x.x.r, i, p.line.mask) : Span{0, -1};
+        };
+        Span kept[KEPT ? RB : 1];
+        if constexpr (KEPT) {
+#pragma unroll
+            for (int r = 0; r < RB; ++r) kept[r] = row_span(r);
+        }
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
             m[r] = -INFINITY;
@@ -439,11 +452,9 @@ __global__ void __launch_bounds__(FT) paged_token_f32_kernel(const __grid_consta
             for (int r = 0; r < RB; ++r) {
                 s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
                 s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
-                const int i = frem(r, p.line.byL);
-                const bool live = r < p.R && i < x.x.r.n;
-                const Span v = live ? span_of(x.x.r, i, p.line.mask) : Span{0, 0};
+                const Span v = KEPT ? kept[KEPT ? r : 0] : row_span(r);
                 if (pos < v.lo || pos >= v.hi) s[r] = -INFINITY;
-                if (p.scores && live && pos < x.x.r.kv && (lane & 3) == 0) p.scores[(row0 + r) * p.line.cap + pos] = s[r];
+                if (p.scores && v.hi >= 0 && pos < x.x.r.kv && (lane & 3) == 0) p.scores[(row0 + r) * p.line.cap + pos] = s[r];
                 float mx = s[r];
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -461,12 +472,15 @@ __global__ void __launch_bounds__(FT) paged_token_f32_kernel(const __grid_consta
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float4 v = *(const float4 *)(V + (8 * warp + k) * st + 4 * lane);
+                    constexpr int W = RB < 4 ? RB : 4;
 #pragma unroll
-                    for (int r = 0; r < RB; r += 4) {
-                        const float4 w = *(const float4 *)(P + k * RB + r);
-                        const float ws[4] = {w.x, w.y, w.z, w.w};
+                    for (int r = 0; r < RB; r += W) {
+                        float ws[4];
+                        if constexpr (W == 4) *(float4 *)ws = *(const float4 *)(P + k * RB + r);
+                        else if constexpr (W == 2) *(float2 *)ws = *(const float2 *)(P + k * RB + r);
+                        else ws[0] = P[k];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < W; ++j) {
                             acc[r + j][0] = fmaf(ws[j], v.x, acc[r + j][0]);
                             acc[r + j][1] = fmaf(ws[j], v.y, acc[r + j][1]);
                             acc[r + j][2] = fmaf(ws[j], v.z, acc[r + j][2]);
@@ -684,13 +698,15 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, bool bf16, cudaStream_t s
     } else {
         const int st = ((a.c.d + 3) & ~3) + 4;
         // the stages also hold the four warps' outputs at the end of a piece
-        const int rb = p.R <= 4 ? 4 : p.R <= 8 ? 8 : 16;
+        const int rb = p.R <= 1 ? 1 : p.R <= 2 ? 2 : p.R <= 4 ? 4 : p.R <= 8 ? 8 : 16;
         const size_t need = std::max(f32_floats(rb, st), (size_t)4 * rb * D) * 4;
         auto go = [&](void (*kernel)(Params), std::atomic<unsigned long long> &done) {
             if ((e = allow_shared((const void *)kernel, f32_floats(rb, 132) * 4, done)) != cudaSuccess) return;
             kernel<<<p.line.ngang, FT, need, s>>>(p), note_launch();
         };
-        if (rb == 4) go(paged_token_f32_kernel<4>, g_shared_f4);
+        if (rb == 1) go(paged_token_f32_kernel<1>, g_shared_f1);
+        else if (rb == 2) go(paged_token_f32_kernel<2>, g_shared_f2);
+        else if (rb == 4) go(paged_token_f32_kernel<4>, g_shared_f4);
         else if (rb == 8) go(paged_token_f32_kernel<8>, g_shared_f8);
         else go(paged_token_f32_kernel<16>, g_shared_f16);
         if (e != cudaSuccess) return e;
