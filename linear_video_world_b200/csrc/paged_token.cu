@@ -51,7 +51,6 @@ constexpr uint32_t SM_ABORT = SM_PLACE + 32;
 std::atomic<unsigned long long> g_shared{0};
 constexpr size_t SMEM_BYTES = SM_ABORT + 16;
 static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two blocks per SM");
-constexpr int KEYS = 4096;                              // keys per block of the second kernel
 
 struct Params {
     Line line;
@@ -67,6 +66,7 @@ struct Params {
     float2 *whole;                  // [b][h][16 rows] (maximum, sum) of heads that one block had whole
     const float *w_in;
     float *w_out, decay;
+    int nj, keys;                   // second kernel: blocks of a head that join; keys per block of the weights
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
@@ -530,9 +530,10 @@ __global__ void __launch_bounds__(FT) paged_token_f32_kernel(const __grid_consta
 }
 
 // Joins the pieces of heads whose keys were cut, in the order of the blocks, and turns the scores
-// into weights. Block (x, b * H + h): keys x * KEYS ... of that head; block x = 0 also joins. The
-// pieces' factors come first, a lane per piece, so that the sums over pieces wait for no chain of
-// loads.
+// into weights. Block (x, b * H + h): x < nj joins 32 of that head's items (eight channels of a row; 16 for a
+// single row), x - nj = i the weights of its keys from i * keys on. The pieces' factors come first, a
+// lane per piece, so that the sums over pieces wait for no chain of loads. (One joining block a head took
+// 57 us for 8 rows over 19781 keys of 2 heads, 148 pieces each.)
 constexpr int JT = 256, MAXP = 512;                     // threads; pieces of a head (blocks of the first kernel)
 template <typename E, int TK>
 __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_constant__ Params p)
@@ -542,8 +543,9 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y % p.c.H, b = blockIdx.y / p.c.H;
     const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
-    const int k0 = blockIdx.x * KEYS;
-    if (blockIdx.x > 0 && k0 >= ro.kv) return;
+    const bool joins = (int)blockIdx.x < p.nj;
+    const int k0 = ((int)blockIdx.x - p.nj) * p.keys;
+    if (!joins && k0 >= ro.kv) return;
     const Holders hd = holders_of<TK>(p.line, 0, b, h);
     const bool cut = hd.T > 0 && hd.g0 != hd.g1;
     if (blockIdx.x == 0 && ro.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
@@ -573,12 +575,11 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
         s_ml[threadIdx.x] = make_float2(y.x, 1.f / y.y);
     }
     __syncthreads();
-    if (blockIdx.x == 0 && (hd.T == 0 || cut)) {
+    if (joins && (hd.T == 0 || cut)) {
         // An item is eight channels of a row, 16 items a row (bf16: a pair of registers of the fragment
-        // in four lanes). With few rows several lanes share an item and take its pieces in turn.
-        int share = 1;
-        while (share < 16 && 2 * share * p.R <= JT / 16) share *= 2;
-        const int item = threadIdx.x / share, r = item >> 4, n = item & 15;
+        // in four lanes); the lanes that share it take its pieces in turn.
+        const int share = p.R > 1 ? 8 : 16;
+        const int item = blockIdx.x * (JT / share) + threadIdx.x / share, r = item >> 4, n = item & 15;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), d = a;
         if (r < p.R) {
             // bf16: row r of the fragment is lanes 4 (r & 7) .., registers 4 n + 2 (r >> 3) and the next
@@ -609,12 +610,12 @@ __global__ void __launch_bounds__(JT) paged_token_join_kernel(const __grid_const
                 *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.o + (row0 + r) * D + 8 * n) = make_uint4(tc::pack_bf16(a.x * inv, d.x * inv), tc::pack_bf16(a.y * inv, d.y * inv), tc::pack_bf16(a.z * inv, d.z * inv), tc::pack_bf16(a.w * inv, d.w * inv));
         }
     }
-    if (!p.w_out) return;
+    if (joins) return;
     const Span u = ro.n > 0 ? Span{span_of(ro, 0, p.line.mask).lo, span_of(ro, ro.n - 1, p.line.mask).hi} : Span{0, 0};
     // four keys a thread: the capacity is a multiple of 16, so neither rows nor words straddle
     const long head = (long)blockIdx.y * p.line.cap;
 #pragma unroll 2
-    for (int k = k0 + 4 * threadIdx.x; k < min(k0 + KEYS, ro.kv); k += 4 * JT) {
+    for (int k = k0 + 4 * threadIdx.x; k < min(k0 + p.keys, ro.kv); k += 4 * JT) {
         float t[4] = {0.f, 0.f, 0.f, 0.f};
         if (k + 3 >= u.lo && k < u.hi) {
 #pragma unroll 4
@@ -688,6 +689,10 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, bool bf16, cudaStream_t s
     p.whole = (float2 *)((char *)a.ws + part_bytes());
     p.scores = a.w_out ? (float *)(p.whole + (size_t)a.B * a.c.H * MROWS) : nullptr;
     p.w_in = a.w_in; p.w_out = a.w_out; p.decay = a.decay;
+    p.nj = (p.R + 1) / 2 > 0 ? (p.R + 1) / 2 : 1;
+    // long runs of keys a block, unless there are too few to fill the SMs twice
+    p.keys = 4096;
+    while (p.keys > 1024 && (long)a.B * a.c.H * ((p.line.cap + p.keys - 1) / p.keys) < 2L * sms) p.keys /= 2;
     if (bf16) {
         const uint32_t box = (uint32_t)std::min(1 << a.c.page_log2, BN);
         CUtensorMap mk, mv;
@@ -713,7 +718,7 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, bool bf16, cudaStream_t s
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.w_out ? (p.line.cap + KEYS - 1) / KEYS : 1), (unsigned)(a.B * a.c.H));
+    cfg.gridDim = dim3((unsigned)(p.nj + (a.w_out ? (p.line.cap + p.keys - 1) / p.keys : 0)), (unsigned)(a.B * a.c.H));
     cfg.blockDim = dim3(JT);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
