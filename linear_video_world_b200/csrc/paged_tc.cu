@@ -599,15 +599,18 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 
 // Joins the pieces of heads whose keys were cut, in the order of the gangs; rows that see no key
 // get zeros here. A block takes 32 rows (a lane each): the pieces' factors first, the warps taking
-// them in turn, then 16 channels a warp, the loads of four pieces in flight (128 rows over 5000 keys
-// of 2 heads, 40 pieces each: the call took 42 us with a chain of loads, 32 so).
+// them in turn, then 4 W channels a warp, the loads of four pieces in flight (128 rows over 5000 keys
+// of 2 heads, 40 pieces each: the call took 42 us with a chain of loads, 32 so). W = 4, a block for all
+// channels; W = 1, four blocks, where the rows are too few to fill half of the SMs (the same 27.8 and 23.8;
+// 224 blocks of W = 4, whole pieces: 17.2 and 21.1).
 constexpr int MAXG = 160;               // pieces whose factors are kept; there are no more gangs
+template <int W>
 __global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constant__ Params p)
 {
     __shared__ float s_f[MAXG][32];
     __shared__ float s_m[8][32], s_l[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nb = (p.R + 31) / 32;
+    const int nb = (p.R + 31) / 32, quad = (blockIdx.y * 8 + warp) * W;         // this warp's first four channels
     const int bh = blockIdx.x / nb, r = (blockIdx.x % nb) * 32 + lane;
     const int b = bh / p.c.H, h = bh % p.c.H;
     const int rt = r / ROWS, pass = rt / p.line.gs, member = rt % p.line.gs, rr = r % ROWS;
@@ -615,7 +618,7 @@ __global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constan
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the first kernel's results from here on
     if (g.T > 0 && g.g0 == g.g1) return;
     const Roll ro = roll_of(p.line.kv_lens, p.line.new_lens, b, p.line.L, p.line.cap);
-    if (ro.bad && threadIdx.x == 0) atomicOr(p.c.err, DEVERR_TABLE);
+    if (ro.bad && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.c.err, DEVERR_TABLE);
     const bool live = r < p.R && frem(r, p.line.byL) < ro.n;
     const int np = g.T > 0 ? g.g1 - g.g0 + 1 : 0;
     auto slot = [&](int i) { return ((long)(g.g0 + i) * p.line.gs + member) * 2 + (i == 0 ? g.slot0 : 0); };
@@ -639,16 +642,16 @@ __global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constan
     l = 0.f;
     for (int w = 0; w < 8; ++w) l += s_l[w][lane];
     if (!live) return;
-    float4 acc[4];
+    float4 acc[W];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < W; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = 0; i < np; ++i) {
         const float f = s_f[i][lane];
         const float4 *src = reinterpret_cast<const float4 *>(p.part) + slot(i) * (D / 4) * ROWS + rr;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float4 v = f != 0.f ? src[(warp * 4 + x) * ROWS] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < W; ++x) {
+            const float4 v = f != 0.f ? src[(quad + x) * ROWS] : make_float4(0.f, 0.f, 0.f, 0.f);
             acc[x].x = fmaf(v.x, f, acc[x].x);
             acc[x].y = fmaf(v.y, f, acc[x].y);
             acc[x].z = fmaf(v.z, f, acc[x].z);
@@ -657,16 +660,10 @@ __global__ void __launch_bounds__(256) paged_join_tc_kernel(const __grid_constan
     }
     const long row = (long)bh * p.R + r;
     const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
-    uint32_t w[8];
+    uint2 *dst = reinterpret_cast<uint2 *>(p.o + row * D + quad * 4);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        w[2 * x] = tc::pack_bf16(acc[x].x * inv, acc[x].y * inv);
-        w[2 * x + 1] = tc::pack_bf16(acc[x].z * inv, acc[x].w * inv);
-    }
-    uint4 *dst = reinterpret_cast<uint4 *>(p.o + row * D + warp * 16);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (p.lse && warp == 0) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
+    for (int x = 0; x < W; ++x) dst[x] = make_uint2(tc::pack_bf16(acc[x].x * inv, acc[x].y * inv), tc::pack_bf16(acc[x].z * inv, acc[x].w * inv));
+    if (p.lse && quad == 0) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // Blocks per gang for nr row tiles on `sms` SMs: as many as waste the fewest block-passes, the
@@ -711,7 +708,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     p.nr = (int)((R + ROWS - 1) / ROWS);
     const int gs = gang_size(p.nr, sms);
     // two tiles a gang at least (unless the heads have but one each): a block's start and end cost as
-    // much as several tiles, and the join grows with the pieces (128 rows over 5000 keys of 2 heads: 32 us with one, 25 with two)
+    // much as several tiles, and the join grows with the pieces (128 rows over 5000 keys of 2 heads: 32 us with one, 25 to 28 with two)
     p.line = line_of(a, gs, std::min(sms / gs, MAXG), (p.nr + gs - 1) / gs, 2);
     p.sl2 = a.sl2;
     p.o = (__nv_bfloat16 *)a.o;
@@ -722,7 +719,8 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     paged_attn_tc_kernel<<<p.line.gs * p.line.ngang, THREADS, SMEM_BYTES, s>>>(mq, mk, mv, p), note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    const bool split = 2 * blocks <= sms;
+    cfg.gridDim = dim3((unsigned)blocks, split ? 4 : 1);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -730,7 +728,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, paged_join_tc_kernel, p)) == cudaSuccess) note_launch();
+    if ((e = cudaLaunchKernelEx(&cfg, split ? paged_join_tc_kernel<1> : paged_join_tc_kernel<4>, p)) == cudaSuccess) note_launch();
     return e;
 }
 

@@ -67,6 +67,7 @@ struct Params {
     const float *w_in;
     float *w_out, decay;
     int nj, keys;                   // second kernel: blocks of a head that join; keys per block of the weights
+    int early;                      // whether its blocks may take their places while the first kernel runs
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
@@ -110,7 +111,7 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     auto FULL = [&](int i) { return sbase + SM_BAR + 16u * (uint32_t)i; };
     auto EMPTY = [&](int i) { return sbase + SM_BAR + 16u * (uint32_t)i + 8u; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;");      // the second kernel may be set up meanwhile
+    if (p.early) asm volatile("griddepcontrol.launch_dependents;");     // the second kernel may be set up meanwhile
     if (sbase & 1023u) {                    // not seen: the attribute asks for it
         if (threadIdx.x == 0) atomicOr(p.c.err, DEVERR_ATTN_WAIT);
         return;
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(FT) paged_token_f32_kernel(const __grid_consta
     __shared__ float2 s_ml[4][RB];
     const int d = p.c.d, dp = (d + 3) & ~3, st = dp + 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float *KV = fs, *Q = KV + FSTAGES * 2 * FN * st, *P = Q + RB * st + warp * 8 * RB;     // P: this warp's [8 keys][RB]
-    asm volatile("griddepcontrol.launch_dependents;");
+    if (p.early) asm volatile("griddepcontrol.launch_dependents;");
     if (warp == 0) {
         const Place c = place_of<FN>(p.line, blockIdx.x);
         if (lane == 0) s_place = c;
@@ -689,7 +690,11 @@ cudaError_t launch_paged_token(const PagedAttnArgs &a, bool bf16, cudaStream_t s
     p.whole = (float2 *)((char *)a.ws + part_bytes());
     p.scores = a.w_out ? (float *)(p.whole + (size_t)a.B * a.c.H * MROWS) : nullptr;
     p.w_in = a.w_in; p.w_out = a.w_out; p.decay = a.decay;
-    p.nj = (p.R + 1) / 2 > 0 ? (p.R + 1) / 2 : 1;
+    p.nj = std::max(1, (p.R + 1) / 2);
+    // Early blocks gather on the SMs that the first kernel leaves first: 1 us won where they have little to
+    // read (one token over 1560 keys of 8 heads 11.3 us, 12.1 late), lost where they have much (8 rows over
+    // 19781 keys of 2 heads 42 us, 22 late; 16 rows over 6861 keys of 10 heads 27 and 21).
+    p.early = p.R <= 3;
     // long runs of keys a block, unless there are too few to fill the SMs twice
     p.keys = 4096;
     while (p.keys > 1024 && (long)a.B * a.c.H * ((p.line.cap + p.keys - 1) / p.keys) < 2L * sms) p.keys /= 2;
