@@ -246,7 +246,7 @@ struct PagedAttnArgs {
     float sl2;                      // softmax scale * log2(e)
     void *ws;
 };
-size_t paged_attn_simt_bytes(int B, int Hq, int Hkv, long L, int d, int max_keys);
+size_t paged_attn_simt_bytes(int B, int Hq, int Hkv, long L, int cap);
 cudaError_t launch_paged_attn_simt(const PagedAttnArgs &a, cudaStream_t s);                 // fp32
 cudaError_t launch_paged_weights_simt(const PagedAttnArgs &a, cudaStream_t s);              // fp32, after the attention
 bool paged_weights_fit(long R, int cap);        // key tiles x row tiles of a head below 2^30

@@ -170,7 +170,7 @@ size_t hlta_paged_attn_workspace_bytes(int B, int Hq, int Hkv, long L, int d, in
     if (paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, weights != 0))
         return pad(paged_token_bytes(B, Hkv, Hq / Hkv, L, max_pages * page, weights != 0)) + 256;
     const size_t lse = weights ? pad((size_t)B * Hq * L * 4) : 0;
-    return lse + pad(dt == HLTA_BF16 ? paged_attn_tc_bytes() : paged_attn_simt_bytes(B, Hq, Hkv, L, d, max_pages * page)) + 256;
+    return lse + pad(dt == HLTA_BF16 ? paged_attn_tc_bytes() : paged_attn_simt_bytes(B, Hq, Hkv, L, max_pages * page)) + 256;
 }
 
 hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages, const int *table, const int *kv_lens,
