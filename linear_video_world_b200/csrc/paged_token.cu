@@ -289,15 +289,24 @@ paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 }
                 __syncwarp();
             }
-            // P as the left operand: the scores' layout is already that of its fragment
-            const uint32_t pa[4] = {tc::pack_bf16(s[0][0], s[0][1]), tc::pack_bf16(s[0][2], s[0][3]), tc::pack_bf16(s[1][0], s[1][1]),
-                                    tc::pack_bf16(s[1][2], s[1][3])};
+            // P as the left operand: the scores' layout is already that of its fragment. Two bf16 numbers a
+            // weight, the second what the first's rounding left (2^-16 of the weight is lost, not 2^-8): the
+            // products it costs are hidden behind the copies
+            uint32_t pa[4], pb[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const float e0 = s[y >> 1][2 * (y & 1)], e1 = s[y >> 1][2 * (y & 1) + 1];
+                pa[y] = tc::pack_bf16(e0, e1);
+                pb[y] = tc::pack_bf16(e0 - __uint_as_float(pa[y] << 16), e1 - __uint_as_float(pa[y] & 0xffff0000u));
+            }
 #pragma unroll
             for (int n2 = 0; n2 < 8; ++n2) {
                 uint32_t b[4];
                 ldsm4t(v_addr(base, n2), b);
                 mma16816(o[2 * n2], pa, b[0], b[1]);
                 mma16816(o[2 * n2 + 1], pa, b[2], b[3]);
+                mma16816(o[2 * n2], pb, b[0], b[1]);
+                mma16816(o[2 * n2 + 1], pb, b[2], b[3]);
             }
             if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
