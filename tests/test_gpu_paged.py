@@ -91,6 +91,7 @@ CASES = [
     dict(kv=[500, 260], new=[150, 150], Hq=2, Hkv=2, L=150, N=50, w=2, page=64),         # frame window inside tiles
     dict(kv=[420], new=[270], Hq=2, Hkv=2, L=270, N=1, w=33, page=128),                  # short window, several row tiles
     dict(kv=[600, 300], new=[40, 33], Hq=16, Hkv=2, L=40, N=1, w=0, page=32),            # 320 packed rows of 8 heads
+    dict(kv=[900, 300, 700], new=[150, 150, 149], Hq=8, Hkv=4, L=150, N=50, w=0, page=64),   # twelve heads of two row tiles, cut
 ]
 
 
@@ -115,9 +116,20 @@ def _run(h, c, q, new, cfg, lse=True, weights=True, decay=0.5):
 @pytest.mark.parametrize("dtype,d", [(F32, 128), (F32, 40), (F32, 7), (BF, 128)])
 @pytest.mark.parametrize("i", range(len(CASES)))
 def test_attention(h, i, dtype, d):
+    _against_64_bits(h, i, dtype, d, None)
+
+
+@pytest.mark.parametrize("dtype,d", [(F32, 128), (F32, 30), (BF, 128)])
+@pytest.mark.parametrize("i", [1, 4, 6, 8, 9, 10])
+def test_attention_in_a_wide_table(h, i, dtype, d):
+    """A table of far more pages than the rollouts have: the capacity decides about tiles and blocks."""
+    _against_64_bits(h, i, dtype, d, 30000 // CASES[i]["page"])
+
+
+def _against_64_bits(h, i, dtype, d, width):
     cfg = CASES[i]
     kv, new, L = cfg["kv"], cfg["new"], cfg["L"]
-    c = Cache(kv, cfg["Hkv"], d, cfg["page"], dtype, seed=i)
+    c = Cache(kv, cfg["Hkv"], d, cfg["page"], dtype, seed=i, width=width)
     q = torch.randn(len(kv), cfg["Hq"], L, d, generator=torch.Generator().manual_seed(100 + i)).to(dtype)
     for b, n in enumerate(new):
         q[b, :, n:] = float("nan")          # padded rows hold anything
