@@ -540,7 +540,7 @@ size_t hlta_paged_evict_workspace_bytes(int B, int Hkv, int budget);
  * [B, Hkv, budget] int32, the kept positions, -1 behind them, or NULL. w_out: [B, Hkv, max_dst *
  * page] float32, the kept weights, left as it was behind them, or NULL.
  * budget >= 1, sink, recent >= 0, sink + recent <= budget <= max_dst * page, 1 <= d <= 128.
- * workspace as above. Errors as hlta_paged_attn_fwd.
+ * workspace as above; with `kept` it is not used and may be NULL. Errors as hlta_paged_attn_fwd.
  */
 hlta_status hlta_paged_evict(const float *weights, const void *k_pages, const void *v_pages,
                              const int *table, const int *kv_lens, int B, int Hkv, int d,

@@ -13,6 +13,7 @@ workspaces with torch and then call those same entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -441,8 +442,9 @@ def hlta_paged_evict(weights, k_pages, v_pages, table, kv_lens, B, Hkv, d, num_p
         (dst_table, "dst_table", i32, None), (new_lens, "new_lens", i32, None),
         (kept, "kept", i32, None), (w_out, "w_out", f32, None), (workspace, "workspace", None, None))
     _check(_lib.hlta_paged_evict(*src, B, Hkv, d, num_pages, page, max_pages, budget, sink, recent,
-                                 kd, vd, dst, num_dst, max_dst, nl, kp, wo, ws, workspace.nbytes,
-                                 _dt(k_pages), _stream_address(th, stream)))
+                                 kd, vd, dst, num_dst, max_dst, nl, kp, wo, ws,
+                                 0 if workspace is None else workspace.nbytes, _dt(k_pages),
+                                 _stream_address(th, stream)))
 
 
 def _gdn_step_args(th, q, k, v, a, b, o, S, S_out, slots, lens, qs=None, gs=None, ss=None, bs=None):
@@ -701,6 +703,11 @@ def paged_append(k, v, k_pages, v_pages, table, kv_lens, new_lens=None, rope=Non
         B, H, L, d, num, page, width, spec, _dt(k), _stream_address(th, stream)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _attn_workspace(device, *shape):
+    return _lib.hlta_paged_attn_workspace_bytes(*shape)
+
+
 def paged_attn(q, k_pages, v_pages, table, kv_lens, new_lens=None, N=1, w=0, scale=0.0, out=None,
                lse=None, w_in=None, w_out=None, decay=1.0, workspace=None, stream=None):
     """Attention of a chunk (q [B, Hq, L, d]) over a paged cache it was appended to (see
@@ -715,8 +722,8 @@ def paged_attn(q, k_pages, v_pages, table, kv_lens, new_lens=None, N=1, w=0, sca
         out = _made(stream, th.empty_like if new_lens is None else th.zeros_like, q)
     code = _dt(q)
     if workspace is None:
-        need = _lib.hlta_paged_attn_workspace_bytes(B, Hq, H, L, d, page, width,
-                                                    0 if w_out is None else 1, code)
+        need = _attn_workspace(q.get_device(), B, Hq, H, L, d, page, width,
+                               0 if w_out is None else 1, code)
         workspace = _made(stream, q.new_empty, need, dtype=th.uint8)
     bs, ws_shape = (B,), (B, H, width * page)
     *addr, ws = _args(th, (q, "q", dt, (B, Hq, L, d)), (k_pages, "k_pages", dt, pages),
@@ -742,7 +749,7 @@ def paged_evict(weights, k_pages, v_pages, table, kv_lens, budget, sink, recent,
     bs = (B,)
     if new_lens is None:
         new_lens = _made(stream, th.empty_like, kv_lens)
-    if workspace is None:
+    if workspace is None and kept is None:
         need = _lib.hlta_paged_evict_workspace_bytes(B, H, budget)
         workspace = _made(stream, weights.new_empty, need, dtype=th.uint8)
     src = _args(th, (weights, "weights", f32, (B, H, width * page)),
@@ -754,7 +761,8 @@ def paged_evict(weights, k_pages, v_pages, table, kv_lens, budget, sink, recent,
         (kept, "kept", i32, (B, H, budget)), (w_out, "w_out", f32, (B, H, dwidth * page)),
         (workspace, "workspace", None, None))
     _check(_lib.hlta_paged_evict(*src, B, H, d, num, page, width, budget, sink, recent, kd, vd, dst,
-                                 to[0], dwidth, nl, kp, wo, ws, workspace.nbytes, _dt(k_pages),
+                                 to[0], dwidth, nl, kp, wo, ws,
+                                 0 if workspace is None else workspace.nbytes, _dt(k_pages),
                                  _stream_address(th, stream)))
     return new_lens
 

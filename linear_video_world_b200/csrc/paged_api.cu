@@ -252,7 +252,7 @@ hlta_status hlta_paged_evict(const float *weights, const void *k_pages, const vo
     const size_t nw = (size_t)B * Hkv * max_pages * page * 4, no = (size_t)B * Hkv * max_dst * page * 4;
     if (w_out && overlap(weights, nw, w_out, no)) return FAIL("w_out overlaps weights");
     const size_t need = hlta_paged_evict_workspace_bytes(B, Hkv, budget);
-    if (!workspace || ws_bytes < need) return FAIL("workspace too small: need %zu bytes, got %zu", need, workspace ? ws_bytes : 0);
+    if (!kept && (!workspace || ws_bytes < need)) return FAIL("workspace too small: need %zu bytes, got %zu", need, workspace ? ws_bytes : 0);
     if ((uintptr_t)workspace & 255u) return FAIL("workspace must be 256-byte aligned");
     if (B == 0 || Hkv == 0) return HLTA_OK;
     ERR_WORD(err);

@@ -100,7 +100,7 @@ def test_paged_evict(h):
               (dict(recent=-1), BAD), (dict(sink=16), BAD), (dict(max_dst=1), BAD), (dict(num_dst=0), BAD), (dict(kd=None), BAD), (dict(vd=None), BAD),
               (dict(vd=_p(5)), BAD), (dict(dt_=None), BAD), (dict(kd=ODD), BAD), (dict(w_out=_p(0)), BAD), (dict(kept=ctypes.c_void_p(2)), BAD),
               (dict(ws=None), BAD), (dict(wsb=ws - 1), BAD), (dict(ws=ctypes.c_void_p((1 << 40) + 128)), BAD), (dict(dt=9), BAD), (dict(d=129), BAD),
-              (dict(B=0), ok), (dict(H=0), ok)]
+              (dict(B=0), ok), (dict(H=0), ok), (dict(B=0, kept=_p(10), ws=None, wsb=0), ok), (dict(kept=_p(10), ws=ctypes.c_void_p((1 << 40) + 128)), BAD)]
     _refused(h, h._lib.hlta_paged_evict, good, cases)
 
 
