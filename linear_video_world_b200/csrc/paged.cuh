@@ -146,13 +146,26 @@ __device__ __forceinline__ Tiles<TK> tiles_of(const Line &p, int b)
     return x;
 }
 
-// Sum of T over rollouts [0, b) by one warp (all lanes get it).
+// Sums of T over rollouts [0, b) and over all, and rollout b's own, by one warp (all lanes get them).
+struct Sums {
+    long long before, all;
+    int own;
+};
 template <int TK>
-__device__ __forceinline__ long long tiles_before(const Line &p, int b)
+__device__ __forceinline__ Sums tile_sums(const Line &p, int b)
 {
-    long long s = 0;
-    for (int i = threadIdx.x & 31; i < b; i += 32) s += tiles_of<TK>(p, i).T;
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    Sums s{0, 0, 0};
+    for (int i = threadIdx.x & 31; i < p.B; i += 32) {
+        const int T = tiles_of<TK>(p, i).T;
+        s.all += T;
+        s.before += i < b ? T : 0;
+        s.own = i == b ? T : s.own;
+    }
+    for (int o = 16; o; o >>= 1) {
+        s.all += __shfl_xor_sync(0xffffffffu, s.all, o);
+        s.before += __shfl_xor_sync(0xffffffffu, s.before, o);
+    }
+    s.own = __shfl_sync(0xffffffffu, s.own, b & 31);
     return s;
 }
 
@@ -167,7 +180,7 @@ template <int TK>
 __device__ __forceinline__ Place place_of(const Line &p, int g)
 {
     const int lane = threadIdx.x & 31;
-    const long long per = tiles_before<TK>(p, p.B) * p.H, W = per * p.passes;
+    const long long per = tile_sums<TK>(p, 0).all * p.H, W = per * p.passes;
     const long long ng = gangs(p, W);
     Place c;
     c.left = 0;
@@ -265,9 +278,9 @@ __device__ __forceinline__ Holders holders_at(const Line &p, long long W, long l
 template <int TK>
 __device__ __forceinline__ Holders holders_of(const Line &p, int pass, int b, int h)
 {
-    const long long per = tiles_before<TK>(p, p.B) * p.H;
-    const int T = tiles_of<TK>(p, b).T;
-    return holders_at(p, per * p.passes, per * pass + tiles_before<TK>(p, b) * p.H + (long long)h * T, T);
+    const Sums s = tile_sums<TK>(p, b);
+    const long long per = s.all * p.H;
+    return holders_at(p, per * p.passes, per * pass + s.before * p.H + (long long)h * s.own, s.own);
 }
 
 }  // namespace paged

@@ -338,8 +338,9 @@ __global__ void __launch_bounds__(BN) paged_weights_join_kernel(const __grid_con
     const int nt = x.T / p.line.steps;
     float s = 0.f;
     if (t >= x.t0 && t < x.t0 + nt) {
-        const long long W = tiles_before<BN>(p.line, p.line.B) * p.line.H;
-        const Holders g = holders_at(p.line, W, tiles_before<BN>(p.line, b) * p.line.H + (long long)h * x.T + (long long)(t - x.t0) * p.line.steps, p.line.steps);
+        const Sums sums = tile_sums<BN>(p.line, b);
+        const long long W = sums.all * p.line.H;
+        const Holders g = holders_at(p.line, W, sums.before * p.line.H + (long long)h * x.T + (long long)(t - x.t0) * p.line.steps, p.line.steps);
         if (g.g0 == g.g1) return;
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's results from here on
         for (int i = g.g0; i <= g.g1; ++i) s += p.part[((long)i * 2 + (i == g.g0 ? g.slot0 : 0)) * BN + threadIdx.x];
