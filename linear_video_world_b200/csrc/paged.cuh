@@ -87,8 +87,8 @@ __device__ __forceinline__ int page_of(const PagedKV &c, int b, int p)
 // TK keys (aligned to multiples of TK in the cache); rollout b has T_b of them per key head. A gang
 // of `gs` consecutive blocks takes the row tiles pass * gs .. pass * gs + gs - 1 of a key head
 // together, a block each, over the same key tiles, so that they meet in L2. The line of all
-// (pass, rollout, key head, key tile) is cut into equal lengths, one per gang: no gang has more
-// than one tile more than another, whatever the rollouts' lengths, no counter is shared, and the
+// (pass, rollout, key head, key tile) is cut into equal lengths, one per gang (the start and end of a head
+// count as `extra` tiles, if they cost as much): no gang has more than one tile more than another, whatever the rollouts' lengths, no counter is shared, and the
 // division depends on the lengths and the grid alone. A gang's cut ends fall inside a head's
 // keys; that head's pieces are joined by a second kernel from (maximum, sum, unnormalised output)
 // in the workspace, at most two per block: slot 0 for the first piece of its range, slot 1 for the
@@ -97,16 +97,17 @@ struct Line {
     int B, H, L, cap, gs, ngang, passes;
     int least;                      // places a gang takes at least (while there are gangs to spare)
     int steps;                      // places on the line per key tile (1; more where a tile's work is cut too)
+    int extra;                      // places in front of each head's tiles: what its start and end cost
     FastDiv byL;
     Mask mask;
     const int *kv_lens, *new_lens;
 };
-__host__ inline Line line_of(const PagedAttnArgs &a, int gs, int ngang, int passes, int least = 1, int steps = 1)
+__host__ inline Line line_of(const PagedAttnArgs &a, int gs, int ngang, int passes, int least = 1, int steps = 1, int extra = 0)
 {
     Line p;
     p.B = a.B; p.H = a.c.H; p.L = (int)a.L;
     p.cap = a.c.max_pages << a.c.page_log2;
-    p.gs = gs; p.ngang = ngang; p.passes = passes; p.least = least; p.steps = steps;
+    p.gs = gs; p.ngang = ngang; p.passes = passes; p.least = least; p.steps = steps; p.extra = extra;
     p.byL = fast_div((unsigned)(a.L > 0 ? a.L : 1));
     p.mask = mask_of(a.N, a.w);
     p.kv_lens = a.c.kv_lens; p.new_lens = a.new_lens;
@@ -146,19 +147,26 @@ __device__ __forceinline__ Tiles<TK> tiles_of(const Line &p, int b)
     return x;
 }
 
-// Sums of T over rollouts [0, b) and over all, and rollout b's own, by one warp (all lanes get them).
+// Places per key head and pass of rollouts [0, b) and of all, and rollout b's own, by one warp (all
+// lanes get them). A head's start and end count only where there are more tiles than the gangs take
+// at least: then a gang has several heads, or few tiles beside one's start.
 struct Sums {
     long long before, all;
-    int own;
+    int own, extra;
 };
 template <int TK>
 __device__ __forceinline__ Sums tile_sums(const Line &p, int b)
 {
-    Sums s{0, 0, 0};
+    Sums s{0, 0, 0, 0};
+    int n_all = 0, n_before = 0;                    // rollouts with tiles
     for (int i = threadIdx.x & 31; i < p.B; i += 32) {
         const int T = tiles_of<TK>(p, i).T;
         s.all += T;
-        s.before += i < b ? T : 0;
+        n_all += T > 0;
+        if (i < b) {
+            s.before += T;
+            n_before += T > 0;
+        }
         s.own = i == b ? T : s.own;
     }
     for (int o = 16; o; o >>= 1) {
@@ -166,13 +174,20 @@ __device__ __forceinline__ Sums tile_sums(const Line &p, int b)
         s.before += __shfl_xor_sync(0xffffffffu, s.before, o);
     }
     s.own = __shfl_sync(0xffffffffu, s.own, b & 31);
+    if (p.extra && s.all * p.H * p.passes > (long long)p.least * p.ngang) {
+        s.extra = p.extra;
+        s.all += (long long)p.extra * __reduce_add_sync(0xffffffffu, n_all);
+        s.before += (long long)p.extra * __reduce_add_sync(0xffffffffu, n_before);
+        s.own += s.own > 0 ? p.extra : 0;
+    }
     return s;
 }
 
 // A place on the line: the next key tile `t` of key head h of rollout b in pass `pass`.
 struct Place {
     int pass, b, h, t;
-    int left;                       // tiles left of the range
+    int left;                       // places left of the range
+    int extra;
 };
 
 // Start of gang g's range (one warp; all lanes get it).
@@ -180,10 +195,12 @@ template <int TK>
 __device__ __forceinline__ Place place_of(const Line &p, int g)
 {
     const int lane = threadIdx.x & 31;
-    const long long per = tile_sums<TK>(p, 0).all * p.H, W = per * p.passes;
+    const Sums sums = tile_sums<TK>(p, 0);
+    const long long per = sums.all * p.H, W = per * p.passes;
     const long long ng = gangs(p, W);
     Place c;
     c.left = 0;
+    c.extra = sums.extra;
     c.pass = c.b = c.h = c.t = 0;
     if (g >= ng) return c;
     const long long a = quot(W * g, ng);
@@ -191,7 +208,8 @@ __device__ __forceinline__ Place place_of(const Line &p, int g)
     c.pass = p.passes > 1 ? (int)quot(a, per) : 0;
     long long x = a - per * c.pass;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const long long n = b0 + lane < p.B ? (long long)tiles_of<TK>(p, b0 + lane).T * p.H : 0;
+        const int own = b0 + lane < p.B ? tiles_of<TK>(p, b0 + lane).T : 0;
+        const long long n = own ? (long long)(own + c.extra) * p.H : 0;
         long long s = n;                                    // inclusive scan
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, s, o);
@@ -201,7 +219,7 @@ __device__ __forceinline__ Place place_of(const Line &p, int g)
         if (in) {
             const int f = __ffs(in) - 1;
             const long long before = __shfl_sync(0xffffffffu, s - n, f);
-            const int T = tiles_of<TK>(p, b0 + f).T;
+            const int T = tiles_of<TK>(p, b0 + f).T + c.extra;
             c.b = b0 + f;
             x -= before;
             c.h = (int)quot(x, T);
@@ -240,11 +258,12 @@ __device__ __forceinline__ bool next_piece(const Line &p, Place &c, Piece<TK> &o
     o.pass = c.pass;
     o.b = c.b;
     o.h = c.h;
-    const int take = min(c.left, o.x.T - c.t);
+    const int T = o.x.T + c.extra, take = min(c.left, T - c.t);
     if (take <= 0) return false;
-    o.ta = o.x.t0 * p.steps + c.t;
-    o.tb = o.ta + take;
-    o.whole = take == o.x.T;
+    // the places in front of the tiles hold none: a piece of them alone is empty
+    o.ta = o.x.t0 * p.steps + max(0, c.t - c.extra);
+    o.tb = o.x.t0 * p.steps + max(0, c.t + take - c.extra);
+    o.whole = take == T;
     c.left -= take;
     c.t = 0;
     if (++c.h == p.H) {

@@ -709,7 +709,10 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, cudaStream_t s)
     const int gs = gang_size(p.nr, sms);
     // two tiles a gang at least (unless the heads have but one each): a block's start and end cost as
     // much as several tiles, and the join grows with the pieces (128 rows over 5000 keys of 2 heads: 32 us with one, 25 to 28 with two)
-    p.line = line_of(a, gs, std::min(sms / gs, MAXG), (p.nr + gs - 1) / gs, 2);
+    // a head's start and end count as four tiles where blocks have several (three chunks of 517 tokens, window
+    // 4096, 108 heads of 5 to 37 tiles: 122 us in all with none, 115 with two, 107 with four; heads of many
+    // tiles the same)
+    p.line = line_of(a, gs, std::min(sms / gs, MAXG), (p.nr + gs - 1) / gs, 2, 1, 4);
     p.sl2 = a.sl2;
     p.o = (__nv_bfloat16 *)a.o;
     p.lse = a.lse;

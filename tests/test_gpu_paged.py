@@ -92,6 +92,7 @@ CASES = [
     dict(kv=[420], new=[270], Hq=2, Hkv=2, L=270, N=1, w=33, page=128),                  # short window, several row tiles
     dict(kv=[600, 300], new=[40, 33], Hq=16, Hkv=2, L=40, N=1, w=0, page=32),            # 320 packed rows of 8 heads
     dict(kv=[900, 300, 700], new=[150, 150, 149], Hq=8, Hkv=4, L=150, N=50, w=0, page=64),   # twelve heads of two row tiles, cut
+    dict(kv=[900, 300, 700], new=[270, 100, 1], Hq=16, Hkv=16, L=270, N=90, w=0, page=64),   # more tiles than blocks take at least
 ]
 
 

@@ -8,9 +8,12 @@ import pytest
 
 # ---- the line (csrc/paged.cuh) ---------------------------------------------------------------
 
-def _pieces(T, H, passes, ngang, steps, least):
-    """What each gang takes, as place_of / next_piece do it: {(pass, b, h): [(from, to, gang, slot, whole)]}."""
+def _pieces(T, H, passes, ngang, steps, least, extra=0):
+    """What each gang takes, as place_of / next_piece do it: {(pass, b, h): [(from, to, gang, slot, whole)]}
+    (in places; `extra` of them lie in front of a head's tiles when the gangs have enough to do)."""
     T = [t * steps for t in T]
+    if sum(T) * H * passes > least * ngang:
+        T = [t + extra if t else 0 for t in T]
     per = sum(T) * H
     W = per * passes
     ng = min(W if W <= len(T) * H * passes else -(-W // least), ngang)
@@ -57,7 +60,8 @@ def test_line_division_and_join_agree(seed):
             continue
         if steps > 1:
             passes = 1
-        T, per, W, ng, got = _pieces(T, H, passes, r.choice([1, 2, 3, 21, 148, 296, r.randint(1, 148)]), steps, r.choice([1, 1, 2, 3]))
+        T, per, W, ng, got = _pieces(T, H, passes, r.choice([1, 2, 3, 21, 148, 296, r.randint(1, 148)]), steps, r.choice([1, 1, 2, 3]),
+                                     r.choice([0, 0, 3, 4]) if steps == 1 else 0)
         sizes = [sum(p[1] - p[0] for c in got.values() for p in c if p[2] == g) for g in range(ng)]
         assert max(sizes) - min(sizes) <= 1 and sum(sizes) == W
         for ps in range(passes):
