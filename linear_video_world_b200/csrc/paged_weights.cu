@@ -178,8 +178,9 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
                     *(float4 *)(smem + SM_Z + (qs * RT + 4 * lane) * 4) = make_float4(z[0], z[1], z[2], z[3]);
                     if (!k.full) {
                         int4 *d = (int4 *)(smem + SM_SPAN + (qs * RT + 4 * lane) * 8);
-                        d[0] = make_int4(v[0].lo, v[0].hi, v[1].lo, v[1].hi);
-                        d[1] = make_int4(v[2].lo, v[2].hi, v[3].lo, v[3].hi);
+                        // (first position, number of positions)
+                        d[0] = make_int4(v[0].lo, max(0, v[0].hi - v[0].lo), v[1].lo, max(0, v[1].hi - v[1].lo));
+                        d[1] = make_int4(v[2].lo, max(0, v[2].hi - v[2].lo), v[3].lo, max(0, v[3].hi - v[3].lo));
                     }
                     __syncwarp();
                     if (lane == 0) {
@@ -260,7 +261,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
                     ok = __all_sync(0xffffffffu, ok && wait_bar(BAR(B_QFULL + sb), par) && wait_bar(BAR(B_SFULL + sb), par));
                     tc::fence_after_sync();
                     const float *z = (const float *)(smem + SM_Z) + sb * RT;
-                    const int2 *spans = (const int2 *)(smem + SM_SPAN) + sb * RT;
+                    const int4 *spans = (const int4 *)(smem + SM_SPAN) + sb * (RT / 2);
                     const float2 sl = make_float2(p.sl2, p.sl2);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -279,10 +280,16 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
                             }
                         } else {
 #pragma unroll
-                            for (int c = 0; c < 64; ++c) {
-                                const int2 v = spans[64 * h + c];
-                                const float e = tc::ex2(fmaf(__uint_as_float(sv[c]), p.sl2, z[64 * h + c]));
-                                acc[c & 1].x += key >= v.x && key < v.y ? e : 0.f;
+                            for (int c = 0; c < 64; c += 4) {
+                                const float4 zz = *(const float4 *)(z + 64 * h + c);
+                                const int4 v = spans[32 * h + c / 2], w = spans[32 * h + c / 2 + 1];
+                                const float2 a = ffma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sl, make_float2(zz.x, zz.y));
+                                const float2 b = ffma2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), sl, make_float2(zz.z, zz.w));
+                                const float e[4] = {tc::ex2(a.x), tc::ex2(a.y), tc::ex2(b.x), tc::ex2(b.y)};
+                                acc[0].x += (unsigned)(key - v.x) < (unsigned)v.y ? e[0] : 0.f;
+                                acc[0].y += (unsigned)(key - v.z) < (unsigned)v.w ? e[1] : 0.f;
+                                acc[1].x += (unsigned)(key - w.x) < (unsigned)w.y ? e[2] : 0.f;
+                                acc[1].y += (unsigned)(key - w.z) < (unsigned)w.w ? e[3] : 0.f;
                             }
                         }
                     }
