@@ -806,7 +806,8 @@ class PagedCache:
 
     max_len: the longest a rollout may grow; num_pages: pages of the pool (an eviction needs free
     pages for what it keeps while it copies). weights: keep the attention weights that `attend`
-    accumulates (times `decay` per call), which `evict` goes by."""
+    accumulates (times `decay` per call), which `evict` goes by; zero for positions of chunks that were
+    never attended, and behind a rollout's end."""
 
     def __init__(self, B, Hkv, d, num_pages, max_len, page=64, dtype=None, weights=False, decay=1.0):
         th = _th()
@@ -896,6 +897,7 @@ class PagedCache:
                     self.k_pages, self.v_pages, dst, w_out=w_out)
         for b in cut:
             weights[b, :, :budget] = w_out[b, :, :budget]
+            weights[b, :, budget:] = 0.0
         del self._free[len(self._free) - need * len(cut):]
         for b in cut:
             self._free.extend(self._pages[b])
@@ -912,6 +914,8 @@ class PagedCache:
         self._pages[b] = []
         self.lens[b] = 0
         self.new_lens[b] = 0
+        if self.weights is not None:
+            self.weights[b] = 0.0
         self._tables(True)
 
 

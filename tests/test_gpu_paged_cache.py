@@ -214,3 +214,41 @@ def test_attending_after_a_rollout_was_cut_or_released(h):
     assert torch.equal(again[2], o[2]) and bool((again[:2] == 0).all())
     # what the cut rollout kept has its weights, once
     assert torch.equal(c.weights[0, :, :33].sort(-1).values, w[0, :, :40].sort(-1).values[:, -33:])
+
+
+@pytest.mark.parametrize("emptied_by", ["release", "evict"])
+@pytest.mark.parametrize("Hq", [2, 4])
+def test_weights_of_an_earlier_occupant_are_gone(h, emptied_by, Hq):
+    """Chunks appended where a released or cut rollout's positions were, the last one alone attended:
+    the weights of a call that starts those positions from zero."""
+    gen = torch.Generator().manual_seed(3)
+    k, q = (torch.randn(2, n, 20, 128, generator=gen).to(BF).cuda() for n in (2, Hq))
+    c = h.PagedCache(2, 2, 128, 20, 64, page=16, weights=True, decay=0.5)
+    c.append(k, k, [20, 13])
+    c.attend(q)
+    if emptied_by == "release":
+        c.release(0)
+        kept = 0
+    else:
+        kept = 6
+        assert c.evict(kept, sink=1, recent=2) == [0, 1]
+    for n in (9, 4):
+        x = k[:, :, :n].contiguous()
+        c.append(x, x)
+    start = c.weights.clone()
+    start[:, :, kept:] = 0.0
+    if emptied_by == "release":
+        start[1] = c.weights[1]                     # as it was: nothing was cut there
+        assert bool((c.weights[1, :, :13] > 0).any())
+    want = start.clone()
+    x = q[:, :, :4].contiguous()
+    o = h.paged_attn(x, c.k_pages, c.v_pages, c.table, c.kv_lens, w_in=start, w_out=want, decay=0.5)
+    assert torch.equal(c.attend(x), o)
+    for b, n in enumerate(c.lens):
+        assert torch.equal(c.weights[b, :, :n], want[b, :, :n])
+    # eviction goes by them: positions never attended have none
+    if emptied_by == "release":
+        c.release(0)
+        c.append(k, k, [20, 0])
+        assert c.evict(5)[:1] == [0] and torch.equal(c.k_pages[c._pages[0][0], :, :5], k[0, :, :5])
+    assert h.hlta_device_status() == 0
