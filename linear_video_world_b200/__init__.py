@@ -856,18 +856,19 @@ class PagedCache:
         lens = [a + n for a, n in zip(self.lens, new)]
         pages = self._grow(lens)
         self.lens = lens
-        self._tables(pages)
-        self.new_lens.copy_(_th().tensor(new, dtype=_th().int32))
         try:
-            paged_append(k, v, self.k_pages, self.v_pages, self.table, self.kv_lens, self.new_lens, rope)
+            self._tables(pages)
+            chunk = _th().tensor(new, dtype=_th().int32).to(self.new_lens.device)
+            paged_append(k, v, self.k_pages, self.v_pages, self.table, self.kv_lens, chunk, rope)
         except Exception:
-            # refused: the rollouts and the pool as they were
+            # refused: the rollouts, their last chunk and the pool as they were
             self.lens = before
             for p, n in zip(self._pages, held):
                 self._free.extend(reversed(p[n:]))
                 del p[n:]
             self._tables(pages)
             raise
+        self.new_lens.copy_(chunk)
 
     def attend(self, q, N=1, w=0, scale=0.0, out=None, lse=None):
         """Attention of the chunk appended last (q [B, Hq, L, d]; the rows of a rollout that was cut or

@@ -252,3 +252,16 @@ def test_weights_of_an_earlier_occupant_are_gone(h, emptied_by, Hq):
         c.append(k, k, [20, 0])
         assert c.evict(5)[:1] == [0] and torch.equal(c.k_pages[c._pages[0][0], :, :5], k[0, :, :5])
     assert h.hlta_device_status() == 0
+
+
+def test_attending_after_a_refused_append(h):
+    """A refused append leaves the chunk appended before it the one that is attended."""
+    gen = torch.Generator().manual_seed(4)
+    k, q = (torch.randn(2, n, 20, 128, generator=gen).to(BF).cuda() for n in (2, 4))
+    c = h.PagedCache(2, 2, 128, 8, 64, page=16)
+    c.append(k, k, [20, 3])
+    new, want = c.new_lens.clone(), c.attend(q)
+    with pytest.raises(h.HltaError):
+        c.append(k.float(), k.float(), [1, 20])
+    assert torch.equal(c.new_lens, new) and torch.equal(c.attend(q), want)
+    assert h.hlta_device_status() == 0

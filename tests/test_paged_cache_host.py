@@ -77,3 +77,35 @@ def test_weights_of_an_earlier_occupant_are_gone(h, emptied_by):
     assert bool((c.weights[0, :, kept:] == 0).all())
     c.attend(_tokens(2, 7))
     assert bool((c.weights[0, :, :kept] == 0.5 * 40 + 7).all()) and bool((c.weights[0, :, kept:kept + 17] == 7).all())
+
+
+def test_refused_append_leaves_the_last_chunk(h):
+    c = h.PagedCache(2, 2, 128, 8, 64, page=16)
+    c.append(_tokens(2, 20), _tokens(2, 20), [20, 3])
+    state = list(c.lens), [list(p) for p in c._pages], sorted(c._free), c.table.clone(), c.kv_lens.clone(), c.new_lens.clone()
+    assert c.new_lens.tolist() == [20, 3]
+    with pytest.raises(h.HltaError):
+        c.append(_tokens(2, 20).float(), _tokens(2, 20).float(), [1, 20])
+    assert (c.lens, c._pages, sorted(c._free)) == state[:3]
+    for t, u in zip((c.table, c.kv_lens, c.new_lens), state[3:]):
+        assert torch.equal(t, u)
+    c.attend(_tokens(2, 20))
+    # a rollout that was released since the chunk stays so
+    c.release(1)
+    with pytest.raises(h.HltaError):
+        c.append(_tokens(2, 20).float(), _tokens(2, 20).float(), [1, 20])
+    assert c.new_lens.tolist() == [20, 0] and c.kv_lens.tolist() == [20, 0]
+    # so does one whose tables cannot be copied
+    tables, failed = c._tables, []
+
+    def once(pages):
+        if not failed:
+            failed.append(pages)
+            raise RuntimeError("no copy")
+        tables(pages)
+    c._tables = once
+    with pytest.raises(RuntimeError):
+        c.append(_tokens(2, 20), _tokens(2, 20))
+    assert c.lens == [20, 0] and len(c._free) == 6 and c.new_lens.tolist() == [20, 0]
+    c.append(_tokens(2, 20), _tokens(2, 20))
+    assert c.lens == [40, 20] and c.new_lens.tolist() == [20, 20] and c.kv_lens.tolist() == [40, 20]
