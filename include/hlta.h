@@ -475,8 +475,9 @@ hlta_status hlta_rope_axes(const void *q, const void *k, void *q_out, void *k_ou
  * All calls enqueue on `stream`, hold no state between calls, and can be captured into a CUDA
  * graph (make a call of the same kind on the device once before the capture: the library's helpers
  * and kernels are set up then). Calls that share a workspace must be ordered on one stream, and the
- * tables must not change while a call runs. HLTA_ERR_UNSUPPORTED: B * Hkv above 65535, a bf16 pool
- * or query tensor of 2^31 rows, bf16 weights of a chunk with 2^44 (row, position) pairs a head.
+ * tables must not change while a call runs. HLTA_ERR_UNSUPPORTED, before anything is enqueued, for
+ * attention: B * Hkv above 65535, a bf16 pool or query tensor of 2^31 rows, bf16 weights of a chunk
+ * with 2^44 (row, position) pairs a head, fp32 chunks of 2^30 rows a key head.
  */
 
 /*

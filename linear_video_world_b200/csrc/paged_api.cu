@@ -200,6 +200,15 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
     if (!workspace || ws_bytes < need) return FAIL("workspace too small: need %zu bytes, got %zu", need, workspace ? ws_bytes : 0);
     if ((uintptr_t)workspace & 255u) return FAIL("workspace must be 256-byte aligned");
     if (B == 0 || (L == 0 && !w_out)) return HLTA_OK;
+    // what one of the call's kernels could not be launched for is refused before the first is
+    const bool few = paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, w_out != nullptr);
+    const long R = (Hq / Hkv) * L, heads = (long)B * Hkv;
+    if (heads > 65535) return record_error(HLTA_ERR_UNSUPPORTED, "at most 65535 key heads of rollouts (got %d x %d)", B, Hkv);
+    if (dt == HLTA_BF16 ? heads * R + 256 >= (1L << 31) || num_pages * Hkv * page + 128 >= (1L << 31)
+                        : R > (1L << 30) || (heads * R + 3) / 4 > 0x7fffffffL)
+        return record_error(HLTA_ERR_UNSUPPORTED, "too many rows of queries (%ld) or of the pool (%ld)", heads * R, num_pages * Hkv * page);
+    if (w_out && !few && dt == HLTA_BF16 && !paged_weights_fit(R, max_pages * page))
+        return record_error(HLTA_ERR_UNSUPPORTED, "weights of %ld rows over a capacity of %d", R, max_pages * page);
     ERR_WORD(err);
     PagedAttnArgs a;
     a.c = cache_of(k_pages, v_pages, table, kv_lens, Hkv, d, num_pages, page, max_pages, err);
@@ -212,11 +221,9 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
     a.N = N; a.w = w;
     a.sl2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d)) * 1.4426950408889634f;
     a.ws = ws;
-    if (paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, w_out != nullptr))
+    if (few)
         return done(launch_paged_token(a, dt == HLTA_BF16, (cudaStream_t)stream), "paged attention");
     if (w_out) {
-        if (dt == HLTA_BF16 && !paged_weights_fit(a.G * a.L, max_pages * page))
-            return record_error(HLTA_ERR_UNSUPPORTED, "weights of %ld rows over a capacity of %d", a.G * a.L, max_pages * page);
         // the weights are taken in a second pass, from the log-sum-exp
         if (!lse) a.lse = (float *)ws;
         a.ws = ws + pad((size_t)B * Hq * L * 4);

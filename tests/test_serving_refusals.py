@@ -138,3 +138,23 @@ def test_wrappers_refuse_host_tensors_and_shapes(h):
         h.paged_attn(q, pages, pages, table, lens, w_out=torch.zeros(1, 2, 33))
     with pytest.raises(h.HltaError):
         h.gdn_step(q, q, q, torch.zeros(1, 2, 4), torch.zeros(1, 2, 3), torch.zeros(3, 2, 128, 128))
+
+
+def test_attention_of_too_many_heads_is_refused_before_anything_runs(h):
+    """B * Hkv above 65535, few rows and many, with weights and without: refused on the host, where no
+    device is asked for."""
+    for dt, L, G in ((h.HLTA_BF16, 40, 1), (h.HLTA_BF16, 40, 4), (h.HLTA_BF16, 1, 1), (h.HLTA_FP32, 40, 1), (h.HLTA_FP32, 1, 1)):
+        for w_out in (None, ctypes.c_void_p(1 << 52)):
+            for B, H, status in ((65536, 1, h.HLTA_ERR_UNSUPPORTED), (256, 256, h.HLTA_ERR_UNSUPPORTED), (70000, 3, h.HLTA_ERR_UNSUPPORTED)):
+                assert h._lib.hlta_paged_attn_fwd(ctypes.c_void_p(1 << 48), ctypes.c_void_p(1 << 44), ctypes.c_void_p(1 << 45), _p(3), _p(4), None,
+                                                  ctypes.c_void_p(1 << 49), None, None, w_out, F(1.0), B, G * H, H, L, 128, 9, 16, 4, 1, 0, F(0.0),
+                                                  ctypes.c_void_p(1 << 53), 1 << 50, dt, None) == status, (dt, L, G, w_out, B)
+
+
+def test_attention_of_a_huge_pool_or_query_is_refused_before_anything_runs(h):
+    """bf16: a pool or a query tensor of 2^31 rows."""
+    for L, B, num_pages in ((40, 1, 1 << 27), (1, 1, 1 << 27), (1 << 28, 8, 9)):
+        for w_out in (None, ctypes.c_void_p(1 << 53)):
+            assert h._lib.hlta_paged_attn_fwd(ctypes.c_void_p(1 << 50), ctypes.c_void_p(1 << 44), ctypes.c_void_p(1 << 45), _p(3), _p(4), None,
+                                              ctypes.c_void_p(1 << 51), None, None, w_out, F(1.0), B, 1, 1, L, 128, num_pages, 16, 4, 1, 0, F(0.0),
+                                              ctypes.c_void_p(1 << 54), 1 << 60, h.HLTA_BF16, None) == h.HLTA_ERR_UNSUPPORTED, (L, B, num_pages, w_out)
