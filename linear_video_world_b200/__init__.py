@@ -803,6 +803,9 @@ class PagedCache:
     paged_evict): the page pool, and the tables that the host keeps and copies to the device when
     pages change hands. The pool's pages are handed out as rollouts grow, returned by `evict` and
     `release`. Everything runs on the current stream, which has to be the same one from call to call.
+    `attend` may be captured into a CUDA graph and replayed for later chunks of as many rows (the cache's
+    tensors stay the same ones); `append`, `evict` and `release` copy lengths and tables from the host,
+    which blocks it, and cannot be captured.
 
     max_len: the longest a rollout may grow; num_pages: pages of the pool (an eviction needs free
     pages for what it keeps while it copies). weights: keep the attention weights that `attend`
@@ -892,20 +895,18 @@ class PagedCache:
         to = {b: [self._free[-1 - i * need - j] for j in range(need)] for i, b in enumerate(cut)}
         dst = th.tensor([to.get(b, [0] * need) for b in range(self.B)], dtype=th.int32).cuda()
         lens = th.tensor([n if b in to else 0 for b, n in enumerate(self.lens)], dtype=th.int32).cuda()
-        weights = self.weights.clone()
         w_out = th.empty((self.B, self.weights.shape[1], need * self.page), device="cuda")
         paged_evict(self.weights, self.k_pages, self.v_pages, self.table, lens, budget, sink, recent,
                     self.k_pages, self.v_pages, dst, w_out=w_out)
-        for b in cut:
-            weights[b, :, :budget] = w_out[b, :, :budget]
-            weights[b, :, budget:] = 0.0
+        for b in cut:                                   # in place: a captured attend holds the tensor
+            self.weights[b, :, :budget] = w_out[b, :, :budget]
+            self.weights[b, :, budget:] = 0.0
         del self._free[len(self._free) - need * len(cut):]
         for b in cut:
             self._free.extend(self._pages[b])
             self._pages[b] = to[b]
             self.lens[b] = budget
             self.new_lens[b] = 0                        # its last chunk is no longer its last positions
-        self.weights = weights
         self._tables(True)
         return cut
 

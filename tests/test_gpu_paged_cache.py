@@ -265,3 +265,31 @@ def test_attending_after_a_refused_append(h):
         c.append(k.float(), k.float(), [1, 20])
     assert torch.equal(c.new_lens, new) and torch.equal(c.attend(q), want)
     assert h.hlta_device_status() == 0
+
+
+def test_captured_attend_replayed_around_evictions(h):
+    """An attend captured once serves chunks appended before and after an eviction and a release: the
+    same bits, and the same weights, as the call made anew."""
+    gen = torch.Generator().manual_seed(6)
+    c = h.PagedCache(2, 2, 128, 20, 64, page=16, weights=True, decay=0.5)
+    k, q = (torch.randn(2, n, 5, 128, generator=gen).to(BF).cuda() for n in (2, 4))
+    out = torch.zeros_like(q)
+    c.append(k, k)
+    c.attend(q, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.attend(q, out=out)
+    for step in range(8):
+        if step == 3:
+            assert c.evict(9, sink=1, recent=3) == [0, 1]
+        if step == 5:
+            c.release(1)
+        k.copy_(torch.randn(2, 2, 5, 128, generator=gen))
+        q.copy_(torch.randn(2, 4, 5, 128, generator=gen))
+        c.append(k, k, [5, 5 - step % 3])
+        want_w = c.weights.clone()
+        want = h.paged_attn(q, c.k_pages, c.v_pages, c.table, c.kv_lens, c.new_lens, out=out.clone(), w_in=want_w, w_out=want_w, decay=0.5)
+        g.replay()
+        assert torch.equal(out, want) and torch.equal(c.weights, want_w)
+    assert h.hlta_device_status() == 0

@@ -109,3 +109,18 @@ def test_refused_append_leaves_the_last_chunk(h):
     assert c.lens == [20, 0] and len(c._free) == 6 and c.new_lens.tolist() == [20, 0]
     c.append(_tokens(2, 20), _tokens(2, 20))
     assert c.lens == [40, 20] and c.new_lens.tolist() == [20, 20] and c.kv_lens.tolist() == [40, 20]
+
+
+def test_the_cache_s_tensors_stay_the_same(h):
+    """A captured attend reads and writes the tensors that the cache had then: no call puts others in
+    their place."""
+    c = h.PagedCache(2, 2, 128, 20, 64, page=16, weights=True)
+    names = ("k_pages", "v_pages", "table", "kv_lens", "new_lens", "weights")
+    at = [getattr(c, n).data_ptr() for n in names]
+    c.append(_tokens(2, 20), _tokens(2, 20), [20, 7])
+    c.attend(_tokens(2, 20))
+    assert c.evict(8) == [0]
+    assert bool((c.weights[0, :, :8] == 20).all()) and bool((c.weights[1, :, :7] == 7).all()) and bool((c.weights[0, :, 8:] == 0).all())
+    c.release(1)
+    c.append(_tokens(2, 3), _tokens(2, 3))
+    assert [getattr(c, n).data_ptr() for n in names] == at
