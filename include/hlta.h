@@ -484,7 +484,8 @@ hlta_status hlta_rope_axes(const void *q, const void *k, void *q_out, void *k_ou
  * Appends a chunk: token i of rollout b goes to position kv_lens[b] - n + i, n its new_lens.
  * k, v: [B, Hkv, L, d] device. `spec` NULL stores k as it is; else its rotation is applied to k
  * on the way (positions by the token's index i in the chunk). Every slot must be written by one
- * rollout only. 1 <= d <= 128. One launch. Errors as hlta_rope_axes.
+ * rollout only; the pages of the keys and of the values must overlap neither one another nor any
+ * other tensor of the call. 1 <= d <= 128. One launch. Errors as hlta_rope_axes.
  */
 hlta_status hlta_paged_append(const void *k, const void *v, void *k_pages, void *v_pages,
                               const int *table, const int *kv_lens, const int *new_lens, int B,

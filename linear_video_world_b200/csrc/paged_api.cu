@@ -22,12 +22,33 @@ hlta_status check_type(hlta_dtype dt, int d, bool bf16_128)
     return HLTA_OK;
 }
 
-// two ranges of bytes that share some but are not the same range
+// two ranges of bytes that share some (the same range too)
 bool overlap(const void *a, size_t na, const void *b, size_t nb)
 {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
     return x < y + nb && y < x + na;
 }
+
+// a tensor of n bytes (none: null or empty)
+struct Bytes {
+    const void *p;
+    size_t n;
+};
+// whether a tensor that is written shares bytes with another one that is written, or with one that is read
+template <size_t NO, size_t NI>
+bool outputs_overlap(const Bytes (&out)[NO], const Bytes (&in)[NI])
+{
+    auto hit = [](const Bytes &a, const Bytes &b) { return a.p && b.p && a.n && b.n && overlap(a.p, a.n, b.p, b.n); };
+    for (size_t i = 0; i < NO; ++i) {
+        for (size_t j = i + 1; j < NO; ++j)
+            if (hit(out[i], out[j])) return true;
+        for (size_t j = 0; j < NI; ++j)
+            if (hit(out[i], in[j])) return true;
+    }
+    return false;
+}
+size_t bytes_of(hlta_dtype dt) { return dt == HLTA_BF16 ? 2 : 4; }
+size_t pool_bytes(long num_pages, int H, int page, int d, hlta_dtype dt) { return (size_t)num_pages * H * page * d * bytes_of(dt); }
 
 hlta_status check_spec(const hlta_rope_axes_t *sp, int d)
 {
@@ -155,8 +176,15 @@ hlta_status hlta_paged_append(const void *k, const void *v, void *k_pages, void 
     if (spec && (st = check_spec(spec, d)) != HLTA_OK) return st;
     if (misaligned(k) || misaligned(v)) return FAIL("tensor pointers must be 16-byte aligned");
     if (misaligned4(new_lens)) return FAIL("tables must be 4-byte aligned");
-    if (B > 0 && k_pages == v_pages) return FAIL("k_pages and v_pages must be different buffers");
-    if (B == 0 || Hkv == 0 || L == 0) return HLTA_OK;
+    if (B == 0 || Hkv == 0 || L == 0) {
+        if (B > 0 && k_pages == v_pages) return FAIL("k_pages and v_pages must be different buffers");
+        return HLTA_OK;
+    }
+    const size_t np = pool_bytes(num_pages, Hkv, page, d, dt), nk = (size_t)B * Hkv * L * d * bytes_of(dt), nb = (size_t)B * 4;
+    if (outputs_overlap({{k_pages, np}, {v_pages, np}},
+                        {{k, nk}, {v, nk}, {table, nb * max_pages}, {kv_lens, nb}, {new_lens, nb},
+                         {spec ? spec->pos : nullptr, nb * L * 3}, {spec ? spec->t0 : nullptr, nb}}))
+        return FAIL("the pages of the keys or of the values overlap another tensor");
     ERR_WORD(err);
     return done(launch_paged_append(cache_of(k_pages, v_pages, table, kv_lens, Hkv, d, num_pages, page, max_pages, err), k, v,
                                     new_lens, B, L, spec, dt == HLTA_BF16, (cudaStream_t)stream), "paged append");

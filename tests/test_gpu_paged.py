@@ -417,3 +417,22 @@ def test_pages_before_the_window_may_be_gone(h, dtype, L, Hq):
     assert bool(((o.cpu().double() - ro).abs() <= ob).all())
     for b, n in enumerate(kv):
         assert bool(((wo[b, :, :n].cpu().double() - rw[b, :, :n]).abs() <= wb[b, :, :n]).all())
+
+
+def test_append_of_tensors_side_by_side(h):
+    """Chunk, pages and tables one behind the other in one buffer: nothing overlaps."""
+    H, page, L, pages = 2, 16, 3, 4
+    pool, chunk = pages * H * page * 128, H * L * 128
+    buf = torch.zeros(2 * pool + 2 * chunk + 64, dtype=BF, device="cuda")
+    k, kp, v, vp = (t.view(shape) for t, shape in zip(buf[:-64].split([chunk, pool, chunk, pool]),
+                                                     ((1, H, L, 128), (pages, H, page, 128), (1, H, L, 128), (pages, H, page, 128))))
+    tail = buf[-64:].view(torch.int32)
+    table, lens = tail[:pages].view(1, pages), tail[pages:pages + 1]
+    table.copy_(_i32([[2, 0, 3, 1]]))
+    lens.copy_(_i32([18]))
+    k.copy_(torch.randn(k.shape, generator=torch.Generator().manual_seed(1)))
+    v.copy_(torch.randn(v.shape, generator=torch.Generator().manual_seed(2)))
+    h.paged_append(k, v, kp, vp, table, lens)
+    for x, p in ((k, kp), (v, vp)):
+        assert torch.equal(p[2, :, 15], x[0, :, 0]) and torch.equal(p[0, :, :2], x[0, :, 1:])
+    assert h.hlta_device_status() == 0

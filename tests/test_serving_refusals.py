@@ -158,3 +158,18 @@ def test_attention_of_a_huge_pool_or_query_is_refused_before_anything_runs(h):
             assert h._lib.hlta_paged_attn_fwd(ctypes.c_void_p(1 << 50), ctypes.c_void_p(1 << 44), ctypes.c_void_p(1 << 45), _p(3), _p(4), None,
                                               ctypes.c_void_p(1 << 51), None, None, w_out, F(1.0), B, 1, 1, L, 128, num_pages, 16, 4, 1, 0, F(0.0),
                                               ctypes.c_void_p(1 << 54), 1 << 60, h.HLTA_BF16, None) == h.HLTA_ERR_UNSUPPORTED, (L, B, num_pages, w_out)
+
+
+def _at(p, off):
+    return ctypes.c_void_p(p.value + off)
+
+
+def test_append_over_its_own_inputs_is_refused(h):
+    """The pool may not hold the chunk, the tables or the positions, nor the keys' pages the values'."""
+    good = dict(k=_p(0), v=_p(1), kp=_p(2), vp=_p(3), table=_p(4), kv_lens=_p(5), new=None, B=2, H=4, L=3, d=128, num_pages=9, page=16, max_pages=4,
+                spec=None, dt=h.HLTA_BF16, s=None)
+    pool, chunk = 9 * 4 * 16 * 128 * 2, 2 * 4 * 3 * 128 * 2
+    bad = [dict(vp=_at(_p(2), pool - 16)), dict(vp=_at(_p(2), 16 - pool)), dict(k=_at(_p(2), pool - 16)), dict(k=_at(_p(3), 16 - chunk)), dict(v=_at(_p(2), 256)),
+           dict(v=_at(_p(3), 0)), dict(table=_at(_p(2), pool - 4)), dict(kv_lens=_at(_p(3), 4)), dict(new=_at(_p(3), 128)),
+           dict(spec=_spec(h, pos=_p(3).value + pool - 4)), dict(spec=_spec(h, t0=_p(2).value))]
+    _refused(h, h._lib.hlta_paged_append, good, [(c, h.HLTA_ERR_INVALID_ARG) for c in bad])
