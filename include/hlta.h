@@ -448,10 +448,10 @@ typedef struct {
 /*
  * Rotates q into q_out and k into k_out. q, q_out: [B, Hq, L, d] device, k, k_out: [B, Hk, L, d],
  * element type `dt`, 1 <= d <= 128; q or k may be NULL (skipped). An output may be its own input
- * (in place), else the four tensors must not overlap. inverse != 0 turns the other way, which is
- * also the map of the gradient. The angle is formed in double precision (any int32 position), the
- * result rounded to `dt` once. One launch on `stream`. Errors: HLTA_ERR_INVALID_ARG for bad
- * shapes, fields, or misaligned (16-byte) pointers.
+ * (in place), else the four tensors must not overlap, nor an output the positions. inverse != 0
+ * turns the other way, which is also the map of the gradient. The angle is formed in double precision
+ * (any int32 position), the result rounded to `dt` once. One launch on `stream`. Errors:
+ * HLTA_ERR_INVALID_ARG for bad shapes, fields, or misaligned (16-byte) pointers.
  */
 hlta_status hlta_rope_axes(const void *q, const void *k, void *q_out, void *k_out, int B, int Hq,
                            int Hk, long L, int d, const hlta_rope_axes_t *spec, int inverse,
@@ -513,11 +513,12 @@ size_t hlta_paged_attn_workspace_bytes(int B, int Hq, int Hkv, long L, int d, in
  * Accumulated attention weights, for eviction: w_out NULL, or [B, Hkv, max_pages * page] float32:
  * w_out[j] = decay * w_in[j] + the sum of the softmax weights that the chunk's rows of the head
  * group give position j; w_in is read for the positions before the chunk only (NULL for zero),
- * may be w_out, else must not overlap it; decay is finite; positions from kv_lens[b] on are left as they were.
+ * may be w_out; decay is finite; positions from kv_lens[b] on are left as they were.
  * scale: of the scores, finite, 0 or less for 1/sqrt(d). bf16: d = 128; fp32: 1 <= d <= 128; Hq / Hkv
  * <= 128. N >= 1, w >= 0; L <= 2^29, max_pages * page <= 2^30.
  * workspace: at least hlta_paged_attn_workspace_bytes(...), 256-byte aligned; its contents on entry
- * are ignored. Sums run in a fixed order: equal calls give equal bits. Errors: HLTA_ERR_INVALID_ARG,
+ * are ignored. But for w_in, what is written (o, lse, w_out, the workspace) overlaps no other tensor of
+ * the call. Sums run in a fixed order: equal calls give equal bits. Errors: HLTA_ERR_INVALID_ARG,
  * HLTA_ERR_UNSUPPORTED; a bounded wait that expires as hlta_swa_fwd.
  */
 hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages,
@@ -542,7 +543,8 @@ size_t hlta_paged_evict_workspace_bytes(int B, int Hkv, int budget);
  * [B, Hkv, budget] int32, the kept positions, -1 behind them, or NULL. w_out: [B, Hkv, max_dst *
  * page] float32, the kept weights, left as it was behind them, or NULL.
  * budget >= 1, sink, recent >= 0, sink + recent <= budget <= max_dst * page, 1 <= d <= 128.
- * workspace as above; with `kept` it is not used and may be NULL. Errors as hlta_paged_attn_fwd.
+ * workspace as above; with `kept` it is not used and may be NULL. What is written overlaps no other
+ * tensor of the call, but for a destination in the pool that is read. Errors as hlta_paged_attn_fwd.
  */
 hlta_status hlta_paged_evict(const float *weights, const void *k_pages, const void *v_pages,
                              const int *table, const int *kv_lens, int B, int Hkv, int d,
@@ -555,15 +557,15 @@ hlta_status hlta_paged_evict(const float *weights, const void *k_pages, const vo
  * Gated delta rule, recurrent form, over a pool of states: the recurrence of hlta_gdn_chunk_fwd
  * token by token, for steps of one or a few tokens per rollout (the chunk form prepares 64-token
  * chunks whatever L is, and is the faster one from some dozens of tokens on).
- * q, k, v, o: [B, H, L, d] device, o apart from the others; a, b: [B, H, L] float32. S, S_out:
- * [num_slots, H, d, d] float32, S_out may be S (in place), else must not overlap it. slots: [B] int32 device, the state of each
- * rollout, NULL for 0 .. B-1; a negative slot marks a padded rollout: its rows of o are left as
- * they were. Slots that no rollout names are left as they were. lens: [B] int32 device: tokens that
- * each rollout really has, NULL for all L; rows behind are left as they were; with no token the
- * state is copied. A slot >= num_slots, a slot that an earlier rollout of the call names too, or a
- * length outside [0, L] is reported through hlta_device_status (HLTA_DEVERR_TABLE) and the rollout
- * skipped. bf16: d = 128; fp32: 1 <= d <= 128. The state is updated in fp32 and rounded nowhere.
- * One launch; no workspace. Errors as hlta_gdn_chunk_fwd.
+ * q, k, v, o: [B, H, L, d] device; a, b: [B, H, L] float32. S, S_out: [num_slots, H, d, d] float32,
+ * S_out may be S (in place); else o and S_out overlap no other tensor of the call. slots: [B] int32
+ * device, the state of each rollout, NULL for 0 .. B-1; a negative slot marks a padded rollout: its
+ * rows of o are left as they were. Slots that no rollout names are left as they were. lens: [B]
+ * int32 device: tokens that each rollout really has, NULL for all L; rows behind are left as they
+ * were; with no token the state is copied. A slot >= num_slots, a slot that an earlier rollout of
+ * the call names too, or a length outside [0, L] is reported through hlta_device_status
+ * (HLTA_DEVERR_TABLE) and the rollout skipped. bf16: d = 128; fp32: 1 <= d <= 128. The state is
+ * updated in fp32 and rounded nowhere. One launch; no workspace. Errors as hlta_gdn_chunk_fwd.
  */
 hlta_status hlta_gdn_step(const void *q, const void *k, const void *v, const float *a,
                           const float *b, void *o, const float *S, float *S_out, const int *slots,

@@ -159,6 +159,8 @@ hlta_status hlta_rope_axes(const void *q, const void *k, void *q_out, void *k_ou
     if ((nq && q != q_out && overlap(q, nq, q_out, nq)) || (nk && k != k_out && overlap(k, nk, k_out, nk)) ||
         (nq && nk && (overlap(q_out, nq, k, nk) || overlap(q_out, nq, k_out, nk) || overlap(q, nq, k_out, nk))))
         return FAIL("an output overlaps another tensor");
+    if (outputs_overlap({{q_out, nq}, {k_out, nk}}, {{spec->pos, (size_t)B * L * 12}, {spec->t0, (size_t)B * 4}}))
+        return FAIL("an output overlaps the positions");
     if (nq + nk == 0) return HLTA_OK;
     return done(launch_rope_axes(q, k, q_out, k_out, B, Hq, Hk, L, d, spec, inverse != 0, dt == HLTA_BF16, (cudaStream_t)stream),
                 "rotary axes");
@@ -220,13 +222,14 @@ hlta_status hlta_paged_attn_fwd(const void *q, const void *k_pages, const void *
     if (w_in && !w_out) return FAIL("w_in without w_out");
     if (!isfinite(scale)) return FAIL("scale must be finite (got %g)", (double)scale);
     if (w_out && !isfinite(decay)) return FAIL("decay must be finite (got %g)", (double)decay);
-    const size_t nw = (size_t)B * Hkv * max_pages * page * 4;
-    if (w_in && w_in != w_out && overlap(w_in, nw, w_out, nw)) return FAIL("w_out overlaps w_in");
-    const size_t nq = (size_t)B * Hq * L * d * (dt == HLTA_BF16 ? 2 : 4);
-    if (nq && overlap(q, nq, o, nq)) return FAIL("o overlaps q");
     const size_t need = hlta_paged_attn_workspace_bytes(B, Hq, Hkv, L, d, page, max_pages, w_out != nullptr, dt);
     if (!workspace || ws_bytes < need) return FAIL("workspace too small: need %zu bytes, got %zu", need, workspace ? ws_bytes : 0);
     if ((uintptr_t)workspace & 255u) return FAIL("workspace must be 256-byte aligned");
+    const size_t nw = (size_t)B * Hkv * max_pages * page * 4, nl = (size_t)B * Hq * L * 4, nq = nl / 4 * d * bytes_of(dt), nb = (size_t)B * 4,
+                 np = pool_bytes(num_pages, Hkv, page, d, dt);
+    if (outputs_overlap({{o, nq}, {lse, nl}, {w_out, nw}, {workspace, B > 0 ? need : 0}},
+                        {{q, nq}, {k_pages, np}, {v_pages, np}, {table, nb * max_pages}, {kv_lens, nb}, {new_lens, nb}, {w_in == w_out ? nullptr : w_in, nw}}))
+        return FAIL("an output or the workspace overlaps another tensor");
     if (B == 0 || (L == 0 && !w_out)) return HLTA_OK;
     // what one of the call's kernels could not be launched for is refused before the first is
     const bool few = paged_token_fits(B, Hkv, Hq / Hkv, L, max_pages * page, w_out != nullptr);
@@ -283,12 +286,17 @@ hlta_status hlta_paged_evict(const float *weights, const void *k_pages, const vo
     if (budget > (long)max_dst * page) return FAIL("budget %d does not fit %d pages of %d", budget, max_dst, page);
     if (misaligned4(weights) || misaligned4(new_lens) || misaligned4(kept) || misaligned4(w_out))
         return FAIL("weights, lengths and positions must be 4-byte aligned");
-    if (B > 0 && new_lens == kv_lens) return FAIL("new_lens must not be kv_lens");
-    const size_t nw = (size_t)B * Hkv * max_pages * page * 4, no = (size_t)B * Hkv * max_dst * page * 4;
-    if (w_out && overlap(weights, nw, w_out, no)) return FAIL("w_out overlaps weights");
     const size_t need = hlta_paged_evict_workspace_bytes(B, Hkv, budget);
     if (!kept && (!workspace || ws_bytes < need)) return FAIL("workspace too small: need %zu bytes, got %zu", need, workspace ? ws_bytes : 0);
     if ((uintptr_t)workspace & 255u) return FAIL("workspace must be 256-byte aligned");
+    const size_t bh = (size_t)B * Hkv, nw = bh * max_pages * page * 4, no = bh * max_dst * page * 4, nb = (size_t)B * 4;
+    const size_t np = pool_bytes(num_pages, Hkv, page, d, dt), nd = pool_bytes(num_dst, Hkv, page, d, dt);
+    const Bytes w = {weights, nw}, t = {table, nb * max_pages}, td = {dst_table, nb * max_dst}, kl = {kv_lens, nb};
+    // (the destination may lie in the pool that is read, in other pages)
+    if (B > 0 && (outputs_overlap({{k_dst, nd}, {v_dst, nd}}, {w, t, td, kl}) ||
+                  outputs_overlap({{new_lens, nb}, {kept, bh * budget * 4}, {w_out, no}, {kept ? nullptr : workspace, need}},
+                                  {w, t, td, kl, {k_pages, np}, {v_pages, np}, {k_dst, nd}, {v_dst, nd}})))
+        return FAIL("an output or the workspace overlaps another tensor");
     if (B == 0 || Hkv == 0) return HLTA_OK;
     ERR_WORD(err);
     PagedEvictArgs a;
@@ -315,11 +323,10 @@ static hlta_status gdn_step(const void *q, const void *k, const void *v, const f
     if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(o) || misaligned(S) || misaligned(S_out))
         return FAIL("tensor pointers must be 16-byte aligned");
     if (misaligned4(a) || misaligned4(b) || misaligned4(slots) || misaligned4(lens)) return FAIL("gates and tables must be 4-byte aligned");
-    const size_t ns = (size_t)num_slots * H * d * d * 4;
-    if (S != S_out && overlap(S, ns, S_out, ns)) return FAIL("S_out overlaps S");
-    const size_t no = (size_t)B * H * L * d * (dt == HLTA_BF16 ? 2 : 4);
-    // blocks of different state rows read the whole of q and k
-    if (no && (overlap(o, no, q, no) || overlap(o, no, k, no) || overlap(o, no, v, no))) return FAIL("o overlaps an input");
+    // (blocks of different state rows read the whole of q and k; a block reads and writes its own rows of S)
+    const size_t ns = (size_t)num_slots * H * d * d * 4, ng = (size_t)B * H * L * 4, no = ng / 4 * d * bytes_of(dt), nb = (size_t)B * 4;
+    if (outputs_overlap({{o, no}, {S_out, ns}}, {{q, no}, {k, no}, {v, no}, {a, ng}, {b, ng}, {slots, nb}, {lens, nb}, {S == S_out ? nullptr : S, ns}}))
+        return FAIL("an output overlaps another tensor");
     if (B == 0 || H == 0) return HLTA_OK;
     ERR_WORD(err);
     GdnStepArgs g;

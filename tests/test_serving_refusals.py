@@ -173,3 +173,43 @@ def test_append_over_its_own_inputs_is_refused(h):
            dict(v=_at(_p(3), 0)), dict(table=_at(_p(2), pool - 4)), dict(kv_lens=_at(_p(3), 4)), dict(new=_at(_p(3), 128)),
            dict(spec=_spec(h, pos=_p(3).value + pool - 4)), dict(spec=_spec(h, t0=_p(2).value))]
     _refused(h, h._lib.hlta_paged_append, good, [(c, h.HLTA_ERR_INVALID_ARG) for c in bad])
+
+
+def test_attention_whose_outputs_overlap_other_tensors_is_refused(h):
+    ws = h.hlta_paged_attn_workspace_bytes(2, 8, 4, 3, 128, 16, 4, True)
+    good = dict(q=_p(0), kp=_p(1), vp=_p(2), table=_p(3), kv_lens=_p(4), new=None, o=_p(5), lse=None, w_in=_p(6), w_out=_p(7), decay=F(1.0), B=2, Hq=8,
+                H=4, L=3, d=128, num_pages=9, page=16, max_pages=4, N=1, w=0, scale=F(0.0), ws=_p(8), wsb=ws, dt=h.HLTA_BF16, s=None)
+    pool, rows, nw = 9 * 4 * 16 * 128 * 2, 2 * 8 * 3, 2 * 4 * 64 * 4
+    bad = [dict(o=_at(_p(1), pool - 16)), dict(o=_at(_p(2), 16 - rows * 256)), dict(o=_at(_p(7), nw - 16)), dict(o=_at(_p(6), 0)), dict(o=_at(_p(8), 64)),
+           dict(lse=_at(_p(5), 4)), dict(lse=_at(_p(0), rows * 256 - 4)), dict(lse=_at(_p(7), nw - 4)), dict(lse=_at(_p(6), 0)), dict(lse=_at(_p(8), ws - 256)), dict(lse=_at(_p(4), 4)),
+           dict(w_out=_at(_p(1), 0)), dict(w_out=_at(_p(3), 28)), dict(w_out=_at(_p(0), 8)), dict(w_in=_p(8)),
+           dict(ws=_p(0)), dict(ws=_at(_p(2), 256)), dict(ws=_p(3)), dict(ws=_p(5)), dict(ws=_p(7)), dict(new=_at(_p(8), 256)), dict(new=_at(_p(5), 4))]
+    _refused(h, h._lib.hlta_paged_attn_fwd, good, [(c, h.HLTA_ERR_INVALID_ARG) for c in bad])
+
+
+def test_eviction_whose_outputs_overlap_other_tensors_is_refused(h):
+    ws = h.hlta_paged_evict_workspace_bytes(2, 4, 20)
+    good = dict(weights=_p(0), kp=_p(1), vp=_p(2), table=_p(3), kv_lens=_p(4), B=2, H=4, d=128, num_pages=9, page=16, max_pages=4, budget=20, sink=2,
+                recent=5, kd=_p(5), vd=_p(6), dt_=_p(7), num_dst=5, max_dst=2, new=_p(8), kept=None, w_out=None, ws=_p(9), wsb=ws, dt=h.HLTA_BF16, s=None)
+    pool, dst, nw, no, nk = 9 * 4 * 16 * 128 * 2, 5 * 4 * 16 * 128 * 2, 2 * 4 * 64 * 4, 2 * 4 * 32 * 4, 2 * 4 * 20 * 4
+    bad = [dict(vd=_at(_p(5), dst - 16)), dict(kd=_at(_p(0), nw - 16)), dict(vd=_at(_p(3), 16)), dict(kd=_at(_p(7), 0)), dict(new=_at(_p(4), 4)), dict(new=_at(_p(3), 28)),
+           dict(new=_at(_p(0), 0)), dict(new=_at(_p(5), 8)), dict(kept=_at(_p(0), nw - 4)), dict(kept=_at(_p(1), 0)), dict(kept=_at(_p(8), 4 - nk)), dict(kept=_at(_p(7), 12)),
+           dict(w_out=_at(_p(2), pool - 4)), dict(w_out=_at(_p(0), 4 - no)), dict(w_out=_p(9)), dict(w_out=_p(10), kept=_at(_p(10), no - 4)), dict(ws=_p(0)), dict(ws=_p(4)),
+           dict(ws=_p(8)), dict(ws=_at(_p(6), 256))]
+    _refused(h, h._lib.hlta_paged_evict, good, [(c, h.HLTA_ERR_INVALID_ARG) for c in bad])
+
+
+def test_gated_delta_step_whose_outputs_overlap_other_tensors_is_refused(h):
+    good = dict(q=_p(0), k=_p(1), v=_p(2), a=_p(3), b=_p(4), o=_p(5), S=_p(6), So=_p(7), slots=None, lens=None, B=2, H=4, L=3, d=128, num_slots=5,
+                dt=h.HLTA_BF16, s=None)
+    states, rows = 5 * 4 * 128 * 128 * 4, 2 * 4 * 3
+    bad = [dict(o=_at(_p(3), 16)), dict(o=_at(_p(4), 16 - rows * 256)), dict(o=_at(_p(6), states - 16)), dict(o=_at(_p(7), 0)), dict(So=_at(_p(0), 16)), dict(So=_at(_p(2), 16 - states)),
+           dict(So=_p(3)), dict(So=_p(5)), dict(slots=_at(_p(7), 8)), dict(lens=_at(_p(5), 4)), dict(S=_p(7), slots=_at(_p(7), states - 4))]
+    _refused(h, h._lib.hlta_gdn_step, good, [(c, h.HLTA_ERR_INVALID_ARG) for c in bad])
+
+
+def test_rotation_whose_outputs_overlap_the_positions_is_refused(h):
+    good = dict(q=_p(0), k=_p(1), qo=_p(2), ko=_p(3), B=1, Hq=4, Hk=2, L=10, d=128, spec=_spec(h), inv=0, dt=h.HLTA_BF16, s=None)
+    bad = [dict(spec=_spec(h, pos=_p(2).value + 4 * 10 * 256 - 4)), dict(spec=_spec(h, pos=_p(3).value - 116)), dict(spec=_spec(h, t0=_p(2).value)),
+           dict(qo=_p(0), spec=_spec(h, t0=_p(0).value + 16)), dict(q=None, spec=_spec(h, pos=_p(3).value))]
+    _refused(h, h._lib.hlta_rope_axes, good, [(c, h.HLTA_ERR_INVALID_ARG) for c in bad])
