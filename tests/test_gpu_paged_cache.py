@@ -293,3 +293,49 @@ def test_captured_attend_replayed_around_evictions(h):
         g.replay()
         assert torch.equal(out, want) and torch.equal(c.weights, want_w)
     assert h.hlta_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("L", [1, 20])
+def test_step_captured_and_replayed(h, dtype, L):
+    """A whole step in one graph: rotation, append (rotated on the way), attention with weights kept in
+    place, the gated delta rule, eviction into another pool. Replayed for other tokens and lengths, below
+    and above the budget: the bits of the calls made one by one."""
+    B, H, Hq, page, width, budget = 2, 2, 6, 16, 8, 40
+    gen, lens_of = torch.Generator().manual_seed(L), [[30, 41], [100, 40], [128, 39 + L], [L, 127]]
+    rand = lambda *s: torch.randn(*s, generator=gen).to(dtype)      # noqa: E731
+    ins = dict(q=rand(B, Hq, L, 128).cuda(), k=rand(B, H, L, 128).cuda(), v=rand(B, H, L, 128).cuda(), a=torch.rand(B, Hq, L, generator=gen).cuda(),
+               lens=torch.tensor(lens_of[0], dtype=torch.int32).cuda(), new=torch.tensor([L, L], dtype=torch.int32).cuda(), t0=torch.tensor([3, 5], dtype=torch.int32).cuda())
+    table = torch.randperm(B * width, generator=gen).to(torch.int32).view(B, width).cuda()
+    dst = torch.randperm(2 * 3, generator=gen).to(torch.int32).view(B, 3).cuda()
+    start = dict(kp=rand(B * width, H, page, 128).cuda(), vp=rand(B * width, H, page, 128).cuda(), w=torch.rand(B, H, width * page, generator=gen).cuda(),
+                 S=0.1 * torch.randn(B, Hq, 128, 128, generator=gen).cuda(), kd=torch.zeros(6, H, page, 128, dtype=dtype).cuda(),
+                 vd=torch.zeros(6, H, page, 128, dtype=dtype).cuda(), rq=torch.zeros_like(ins["q"]), o=torch.zeros_like(ins["q"]), go=torch.zeros_like(ins["q"]),
+                 lse=torch.zeros(B, Hq, L).cuda(), nl=torch.zeros(B, dtype=torch.int32).cuda(), kept=torch.zeros(B, H, budget, dtype=torch.int32).cuda(),
+                 wo=torch.zeros(B, H, 3 * page).cuda())
+
+    def step(s):
+        rope = dict(pairs=PAIRS, grid=(2, 3), t0=ins["t0"])
+        h.rope_axes(ins["q"], None, out=(s["rq"], None), **rope)
+        h.paged_append(ins["k"], ins["v"], s["kp"], s["vp"], table, ins["lens"], ins["new"], rope=rope)
+        h.paged_attn(s["rq"], s["kp"], s["vp"], table, ins["lens"], ins["new"], out=s["o"], lse=s["lse"], w_in=s["w"], w_out=s["w"], decay=0.5)
+        h.gdn_step_raw(s["rq"], s["o"], ins["q"], ins["a"], ins["a"], 1.0, s["S"], lens=ins["new"], out=s["go"])
+        h.paged_evict(s["w"], s["kp"], s["vp"], table, ins["lens"], budget, 4, 8, s["kd"], s["vd"], dst, new_lens=s["nl"], kept=s["kept"], w_out=s["wo"])
+
+    mine, one_by_one = ({k: t.clone() for k, t in start.items()} for _ in range(2))
+    step({k: t.clone() for k, t in start.items()})
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(mine)
+    for i, lens in enumerate(lens_of + lens_of[:1]):
+        for n in ("q", "k", "v"):
+            ins[n].copy_(rand(*ins[n].shape))
+        ins["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        ins["new"].copy_(torch.tensor([L, max(1, L - 3 * i)], dtype=torch.int32))
+        g.replay()
+        step(one_by_one)
+        for n in start:
+            assert torch.equal(mine[n], one_by_one[n]), (n, i)
+        assert mine["nl"].tolist() == [min(n, budget) for n in lens] and bool(torch.isfinite(mine["go"].float()).all())
+    assert h.hlta_device_status() == 0
