@@ -509,7 +509,11 @@ size_t hlta_paged_attn_workspace_bytes(int B, int Hq, int Hkv, long L, int d, in
  * q, o: [B, Hq, L, d] device; query head h reads key head h / (Hq / Hkv). lse: [B, Hq, L] float32
  * (natural log-sum-exp of the scaled scores) or NULL. Rows at or behind new_lens[b] are left as
  * they were. Slots that no row of the chunk sees (past a rollout's end, before its window) may
- * hold anything, NaN included.
+ * hold anything, NaN included; an entry of v_pages that is not finite in a slot that some row sees may
+ * make any row of the chunk NaN.
+ * Rounding: scores, softmax statistics and sums are fp32, outputs are rounded once. bf16: the softmax
+ * weights enter the product with the values as one bf16 number each where a key head has more than 16
+ * packed rows (Hq / Hkv * L; 2^-8 of a weight at most), as two where it has at most 16 (2^-16).
  * Accumulated attention weights, for eviction: w_out NULL, or [B, Hkv, max_pages * page] float32:
  * w_out[j] = decay * w_in[j] + the sum of the softmax weights that the chunk's rows of the head
  * group give position j; w_in is read for the positions before the chunk only (NULL for zero),

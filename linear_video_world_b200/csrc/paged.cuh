@@ -81,18 +81,23 @@ __device__ __forceinline__ int page_of(const PagedKV &c, int b, int p)
 }
 
 // ---------------------------------------------------------------------------------------
-// Division of the work over the GPU (bf16 kernels).
+// Division of the work over the GPU (the attention and weights kernels).
 //
 // A key head's packed rows come in row tiles. The keys that a rollout's chunk sees come in tiles of
 // TK keys (aligned to multiples of TK in the cache); rollout b has T_b of them per key head. A gang
 // of `gs` consecutive blocks takes the row tiles pass * gs .. pass * gs + gs - 1 of a key head
 // together, a block each, over the same key tiles, so that they meet in L2. The line of all
 // (pass, rollout, key head, key tile) is cut into equal lengths, one per gang (the start and end of a head
-// count as `extra` tiles, if they cost as much): no gang has more than one tile more than another, whatever the rollouts' lengths, no counter is shared, and the
-// division depends on the lengths and the grid alone. A gang's cut ends fall inside a head's
-// keys; that head's pieces are joined by a second kernel from (maximum, sum, unnormalised output)
-// in the workspace, at most two per block: slot 0 for the first piece of its range, slot 1 for the
-// last.
+// count as `extra` tiles, if they cost as much): no gang has more than one place more than another,
+// whatever the rollouts' lengths, no counter is shared, and the division depends on the lengths and the
+// grid alone. Places are not work: those of `extra` hold no tile, and of the tiles, which are those that
+// the whole chunk sees, a block walks only what its own row tile sees. With a long history that is nearly
+// all of them; of a chunk without history the first row tiles see few and the last all, and so do blocks
+// of row tiles far apart under a short window (8192 tokens of 8 heads, each seeing those before it:
+// 222 us, 0.62 PFLOP/s, where a frame over 32760 keys reaches 0.94).
+// A gang's cut ends fall inside a head's keys; that head's pieces are joined by a second kernel from
+// (maximum, sum, unnormalised output) in the workspace, at most two per block: slot 0 for the first piece
+// of its range, slot 1 for the last.
 struct Line {
     int B, H, L, cap, gs, ngang, passes;
     int least;                      // places a gang takes at least (while there are gangs to spare)

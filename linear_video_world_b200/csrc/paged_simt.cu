@@ -320,10 +320,12 @@ __global__ void __launch_bounds__(128) paged_join_f32_kernel(const __grid_consta
 
 // Accumulated attention weights: 64 keys of one key head, and over every row of the head group that
 // sees them the sum of 2^(score - lse). A cluster of one to eight blocks (grid z) shares those keys, each
-// with every nz-th block of 64 rows, copied asynchronously one ahead; a thread sums its four keys over
-// its four rows of each, and the 16 threads of a key and the blocks are joined at the end in a fixed
-// order. (One block for all rows, copied word by word between two barriers: 1600 rows over 381 keys, the
-// whole call, 287 us for 56.)
+// with every nz-th block of 32 WRW rows (64 or 128), copied asynchronously one ahead; a thread sums eight
+// keys over its WRW (two or four) rows of each, and the 32 threads of a key and the blocks are joined at
+// the end in a fixed order. Bound like the attention by the multiply-adds of the scores, which are formed a
+// second time, and the shared-memory reads that feed them. (One block for all rows, copied word by word
+// between two barriers: 1600 rows over 381 keys, the whole call, 287 us for 56. 2 x 800 rows over 562 and
+// 2736 keys of 4 heads: 299 us with the weights, 180 without.)
 template <int WRW>
 __global__ void __launch_bounds__(THREADS) paged_weights_f32_kernel(PagedAttnArgs a, FastDiv byL, Mask mask)
 {

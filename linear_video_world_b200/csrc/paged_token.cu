@@ -2,10 +2,10 @@
 // accumulated attention weights. bf16, head dim 128, on the tensor cores; fp32 on the CUDA cores.
 //
 // Bound by HBM: every key and value is read once, 512 bytes for at most 16 rows. The division of
-// the work is that of paged.cuh with single blocks as gangs, two blocks per SM: an equal number of
-// 64-key tiles for every block whatever the rollouts' lengths. One warp of a block copies tiles
-// (K and V of 64 keys, 32 KB) into a ring of three by TMA, a lane per page; 192 KB in flight per SM
-// cover the latency several times. Four warps take 16 keys of a tile each and never wait for one
+// the work is that of paged.cuh with single blocks as gangs, two blocks per SM: equal shares of the
+// 64-key tiles whatever the rollouts' lengths (a head's start and end counted as two of them where blocks
+// have several). One warp of a block copies tiles (K and V of 64 keys, 32 KB) into a ring of three by TMA,
+// a lane per page; 192 KB in flight per SM cover the latency several times. Four warps take 16 keys of a tile each and never wait for one
 // another: S = Q K^T of 16 x 16 by warp-level products (the rows fill one m16 tile, a tcgen05 product
 // would be 7/8 padding), running maximum and sum per warp, O += P V with V's fragments through
 // transposing loads. At the end of a piece the warps' results are joined through shared memory; a
